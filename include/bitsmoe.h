@@ -311,6 +311,121 @@ int bitsmoe_ssd(const float* W, int E, int dout, int din, int r, float* phi, flo
                 double* sigma2, int* sweeps, int max_sweeps, void* ws, size_t ws_bytes,
                 bitsmoe_stream_t stream);
 
+/* ------------------------------------------------- the expert layer's operators
+ * What a mixture-of-experts layer needs around the spectral projections:
+ * routing, products with dense (unfactored) experts and their gradients, the
+ * gated activation, the combine, and products with plain 4-bit weights.
+ *
+ * Ragged layout: the T*k (token, slot) pairs p = t*k + j, sorted by expert.
+ *   bounds : E + 1 int32; sorted rows [bounds[e], bounds[e+1]) are expert e's
+ *   order  : sorted row -> pair, -1 past bounds[E]
+ *   slot   : pair -> sorted row, -1 for a pair without an expert
+ * Rows past bounds[E] are neither read nor written.  Kernels clamp what they
+ * read from bounds into [0, R], so a wrong table gives wrong rows, never an
+ * access outside the buffers.
+ * Element types: BITSMOE_F16 and BITSMOE_BF16 for operands; outputs have the
+ * operands' type or BITSMOE_F32.  Row strides (ld*) are in elements; the
+ * elements of a row are contiguous.  Pointers need the alignment of their
+ * element type; rows that are 16-byte aligned (pointer, stride and sizes) are
+ * the fast case.  All calls are asynchronous on `stream` and may be captured
+ * into a graph.  Sums, softmax and norms are float32; each output is rounded
+ * once. */
+#define BITSMOE_F32  0
+#define BITSMOE_F16  1
+#define BITSMOE_BF16 2
+
+#define BITSMOE_ACT_NONE     0
+#define BITSMOE_ACT_SILU_MUL 1
+
+/* Router.  logits: T rows of E (F32, F16 or BF16).  Per token the k largest
+ * logits in falling order, equal ones by rising index:
+ *   ids[t*k + j], g[t*k + j] = scale * p_{id_j}, p = softmax(logits[t]),
+ *   divided by sum_i p_{id_i} when renorm is not 0.
+ * A logit of -inf is never chosen; slots left over get id -1 and g 0.  A row
+ * with a NaN or +inf gets ids -1 and g NaN.  E <= 2048, k <= min(E, 64).
+ * bounds, order, slot (all or none): the pairs grouped as by
+ * bitsmoe_moe_group, with its workspace.
+ * bitsmoe_moe_route_grad: dlogits (T rows of E, the logits' type) from dg and
+ * the ids of the forward call; every element is written (NaN in a row with a
+ * NaN or +inf).  An id outside [0, E) takes no part. */
+int bitsmoe_moe_route(int dtype, const void* logits, int64_t ld, int T, int E, int k, int renorm,
+                      float scale, int32_t* ids, float* g, int32_t* bounds, int32_t* order,
+                      int32_t* slot, void* ws, size_t ws_bytes, bitsmoe_stream_t stream);
+int bitsmoe_moe_route_grad(int dtype, const void* logits, int64_t ld, const int32_t* ids,
+                           const float* dg, int T, int E, int k, int renorm, float scale,
+                           void* dlogits, int64_t ldd, bitsmoe_stream_t stream);
+
+/* Groups P pairs by expert: bounds, order and slot from ids, pairs of one
+ * expert in rising pair order (the same result every time), pairs whose id
+ * lies outside [0, E) last.  E <= 2048.  ws: at least
+ * bitsmoe_moe_group_workspace_size() bytes (0 for few pairs), 4-byte aligned;
+ * its contents carry nothing between calls. */
+int bitsmoe_moe_group_workspace_size(int P, int E, size_t* bytes);
+int bitsmoe_moe_group(const int32_t* ids, int P, int E, int32_t* bounds, int32_t* order,
+                      int32_t* slot, void* ws, size_t ws_bytes, bitsmoe_stream_t stream);
+
+/* Products by expert.  w: E x N x K (dense, contiguous; E x 2N x K with
+ * BITSMOE_ACT_SILU_MUL, gate rows first).  Sorted row i of expert e:
+ *   y[i] = W_e x[i]             (or SiLU(gate) * up of that product)
+ *   dx[i] = W_e^T dy[i]
+ *   dw_e = sum_i dy[i] x[i]^T   (E x N x K, contiguous, every element
+ *                                written: 0 for an expert without rows)
+ * rows (may be NULL): sorted row i reads row rows[i] / div of x, which has
+ * x_rows rows (the order of the pairs with div = k reads tokens); an index
+ * outside them makes the products NaN.  Without rows, x_rows >= R. */
+int bitsmoe_grouped_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
+                           int div, const void* w, const int32_t* bounds, int R, int E, int N,
+                           int K, int act, void* y, int y_dtype, int64_t ldy,
+                           bitsmoe_stream_t stream);
+int bitsmoe_grouped_matmul_dx(int dtype, const void* dy, int64_t lddy, const void* w,
+                              const int32_t* bounds, int R, int E, int N, int K, void* dx,
+                              int dx_dtype, int64_t lddx, bitsmoe_stream_t stream);
+int bitsmoe_grouped_matmul_dw(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                              int x_rows, const int32_t* rows, int div, const int32_t* bounds,
+                              int R, int E, int N, int K, void* dw, int dw_dtype,
+                              bitsmoe_stream_t stream);
+
+/* Gated activation of rows a = [gate | up] (R rows of 2F): h = SiLU(gate) up;
+ * its gradient da (R rows of 2F) from dh.  bounds (may be NULL, with E): only
+ * rows below bounds[E] are read and written.  da may be a itself. */
+int bitsmoe_silu_mul(int dtype, const void* a, int64_t lda, const int32_t* bounds, int R, int E,
+                     int F, void* h, int64_t ldh, bitsmoe_stream_t stream);
+int bitsmoe_silu_mul_grad(int dtype, const void* a, int64_t lda, const void* dh, int64_t lddh,
+                          const int32_t* bounds, int R, int E, int F, void* da, int64_t ldda,
+                          bitsmoe_stream_t stream);
+
+/* Combine: out[t] = sum over j, in slot order, of g[t*k + j] y[slot[t*k + j]]
+ * (y: R rows of D; g NULL: weights of 1).  A slot outside [0, R) has no row.
+ * Gradient: dy[slot] = g dout[t] (rows that no slot names are left as they
+ * were; slots must differ), dg[t*k + j] = <dout[t], y[slot]>, 0 without a
+ * row (dg NULL: not computed, y not read). */
+int bitsmoe_moe_combine(int y_dtype, const void* y, int64_t ldy, int R, const int32_t* slot,
+                        const float* g, int T, int k, int D, void* out, int out_dtype,
+                        int64_t ldo, bitsmoe_stream_t stream);
+int bitsmoe_moe_combine_grad(const void* dout, int out_dtype, int64_t ldo, int y_dtype,
+                             const void* y, int64_t ldy, int R, const int32_t* slot,
+                             const float* g, int T, int k, int D, void* dy, int64_t lddy,
+                             float* dg, bitsmoe_stream_t stream);
+
+/* 4-bit weights: W[n, c] = mins[n, c/G] + scales[n, c/G] * q[n, c] with codes
+ * q of 0..15, two per byte along the inputs (byte c/2, even c in the low
+ * half), float16 scales and mins per group of G = 32, 64 or 128 inputs; mins
+ * NULL: symmetric, -8 * scales.  Arrays are E x rows x (K/2 bytes, K/G, K/G),
+ * rows = N, or 2N (gate first) with BITSMOE_ACT_SILU_MUL; codes 16-byte
+ * aligned, scales and mins 4-byte aligned.  K must be a multiple of G.
+ * y, x, rows, div, bounds as for bitsmoe_grouped_matmul; bounds NULL (E = 1):
+ * one dense projection of all R rows.
+ * bitsmoe_w4_pack (host arrays): quantizes `rows` rows of K float32 weights
+ * with the packer's rule at 4 bits: s = fp16_rne((max - min) / 15), 1 if that
+ * is 0; m = fp16_rne(min); q = clamp(nearbyint((w - m) / s), 0, 15).
+ * BITSMOE_EBITS for a weight that is not finite or beyond 60000. */
+int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
+                      int div, const void* codes, const void* scales, const void* mins, int G,
+                      const int32_t* bounds, int R, int E, int N, int K, int act, void* y,
+                      int y_dtype, int64_t ldy, bitsmoe_stream_t stream);
+int bitsmoe_w4_pack(const float* w, int64_t rows, int K, int G, uint8_t* codes, uint16_t* scales,
+                    uint16_t* mins);
+
 /* Zero-fills a workspace with a kernel (no memset node), on `stream`. */
 int bitsmoe_workspace_init(void* ws, size_t ws_bytes, bitsmoe_stream_t stream);
 

@@ -40,6 +40,7 @@ def _load():
 _lib = _load()
 
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_i64, _f = ctypes.c_int64, ctypes.c_float
 _pi = ctypes.POINTER(ctypes.c_int)
 _psz = ctypes.POINTER(ctypes.c_size_t)
 
@@ -72,6 +73,25 @@ _SIGS = {
     "bitsmoe_moe_down": ([_vp, _sz, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz,
                           _vp], _i),
     "bitsmoe_ssd_workspace_size": ([_i, _i, _i, _i, _psz], _i),
+    "bitsmoe_moe_route": ([_i, _vp, _i64, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                           _vp], _i),
+    "bitsmoe_moe_route_grad": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i64, _vp], _i),
+    "bitsmoe_moe_group_workspace_size": ([_i, _i, _psz], _i),
+    "bitsmoe_moe_group": ([_vp, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "bitsmoe_grouped_matmul": ([_i, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i,
+                                _i64, _vp], _i),
+    "bitsmoe_grouped_matmul_dx": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i64, _vp],
+                                  _i),
+    "bitsmoe_grouped_matmul_dw": ([_i, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _i, _i, _i, _i,
+                                   _vp, _i, _vp], _i),
+    "bitsmoe_silu_mul": ([_i, _vp, _i64, _vp, _i, _i, _i, _vp, _i64, _vp], _i),
+    "bitsmoe_silu_mul_grad": ([_i, _vp, _i64, _vp, _i64, _vp, _i, _i, _i, _vp, _i64, _vp], _i),
+    "bitsmoe_moe_combine": ([_i, _vp, _i64, _i, _vp, _vp, _i, _i, _i, _vp, _i, _i64, _vp], _i),
+    "bitsmoe_moe_combine_grad": ([_vp, _i, _i64, _i, _vp, _i64, _i, _vp, _vp, _i, _i, _i, _vp,
+                                  _i64, _vp, _vp], _i),
+    "bitsmoe_w4_matmul": ([_i, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i,
+                           _vp, _i, _i64, _vp], _i),
+    "bitsmoe_w4_pack": ([_vp, _i64, _i, _i, _vp, _vp, _vp], _i),
     "bitsmoe_ssd": ([_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _pi, _i, _vp, _sz, _vp], _i),
 }
 FQCM_WS_BYTES = 1024 + 65536 * 24
@@ -368,3 +388,374 @@ def ssd(W, r, max_sweeps=30, ws=None, stream=None):
                             s2.ctypes.data, ctypes.byref(sw), int(max_sweeps), _ptr(ws),
                             _nbytes(ws), _stream(stream)))
     return phi, a, p, s2, sw.value
+
+
+# ------------------------------------------------ the expert layer's operators
+#
+# Routing, products with dense or 4-bit experts, the gated activation and the
+# combine, with their gradients.  Sorted rows: the T*k (token, slot) pairs
+# grouped by expert; `bounds` (E + 1), `order` (row -> pair) and `slot`
+# (pair -> row) come from moe_route or moe_group.  Matrices may have any row
+# stride; their rows are contiguous.  Without `stream` a call runs on the
+# current stream of its tensors' device.
+
+ACT = {None: 0, "silu_mul": 1}
+
+
+def _dtype(t):
+    import torch
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    return code
+
+
+def _matrix(name, t, shape=None):
+    """(pointer, row stride) of a 2-d tensor with contiguous rows."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s must be %s, got %s" % (name, "2-d" if shape is None else
+                                                    "of shape %s" % (shape,), tuple(t.shape)))
+    rows, cols = t.shape
+    step, one = t.stride()
+    if cols > 1 and one != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    # the stride of a single row says nothing
+    return t.data_ptr(), max(step, cols) if rows <= 1 else step
+
+
+def _array(name, t, dtype, shape):
+    """Pointer of a contiguous tensor of that dtype and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError("%s must be %s of shape %s, got %s of %s" % (name, dtype, shape, t.dtype,
+                                                                      tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _same_device(*ts):
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError("a tensor is on %s, not on a GPU" % t.device)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors on %s and %s" % (dev, t.device))
+    return dev
+
+
+def _enqueue(fn, dev, stream, *args):
+    """Calls fn(*args, stream) with the tensors' device as the current one."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _new(shape, dtype, dev, stream, zero=False):
+    """A tensor that belongs to the stream the call runs on."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
+def _scratch(nbytes, dev, stream):
+    import torch
+    return _new(nbytes, torch.uint8, dev, stream) if nbytes else None
+
+
+def moe_group_workspace_size(P, E):
+    out = ctypes.c_size_t(0)
+    _check(_lib.bitsmoe_moe_group_workspace_size(P, E, ctypes.byref(out)))
+    return out.value
+
+
+def _group_buffers(T, k, E, bounds, order, slot, dev, stream):
+    import torch
+    i32 = torch.int32
+    bounds = _new(E + 1, i32, dev, stream) if bounds is None else bounds
+    order = _new(T * k, i32, dev, stream) if order is None else order
+    slot = _new((T, k), i32, dev, stream) if slot is None else slot
+    _array("bounds", bounds, torch.int32, (E + 1,))
+    _array("order", order, torch.int32, (T * k,))
+    _array("slot", slot, torch.int32, (T, k))
+    return bounds, order, slot
+
+
+def moe_group(ids, E, bounds=None, order=None, slot=None, ws=None, stream=None):
+    """(bounds, order, slot) of the pairs of ids (T x k int32) by expert, in
+    rising pair order; pairs with an id outside [0, E) come last, with -1."""
+    import torch
+    T, k = ids.shape
+    dev = _same_device(ids, bounds, order, slot, ws)
+    pi = _array("ids", ids, torch.int32, (T, k))
+    bounds, order, slot = _group_buffers(T, k, E, bounds, order, slot, dev, stream)
+    if ws is None:
+        ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
+    _enqueue(_lib.bitsmoe_moe_group, dev, stream, pi, T * k, E, bounds.data_ptr(),
+             order.data_ptr(), slot.data_ptr(), _ptr(ws), 0 if ws is None else _nbytes(ws))
+    return bounds, order, slot
+
+
+def moe_route(logits, k, ids=None, g=None, renorm=False, scale=1.0, bounds=None, order=None,
+              slot=None, ws=None, stream=None):
+    """(ids T x k int32, g T x k float32) of the k largest logits (T x E) of
+    each token: softmax weights over all experts, or over the chosen ones
+    (renorm), times scale.  With bounds, order and slot the pairs are grouped
+    by expert as well, as by moe_group."""
+    import torch
+    T, E = logits.shape
+    dev = _same_device(logits, ids, g, bounds, order, slot, ws)
+    pl, ld = _matrix("logits", logits)
+    if ids is None:
+        ids = _new((T, k), torch.int32, dev, stream)
+    if g is None:
+        g = _new((T, k), torch.float32, dev, stream)
+    pi, pg = _array("ids", ids, torch.int32, (T, k)), _array("g", g, torch.float32, (T, k))
+    pb = po = ps = None
+    if bounds is not None or order is not None or slot is not None:
+        if bounds is None or order is None or slot is None:
+            raise ValueError("bounds, order and slot go together")
+        pb = _array("bounds", bounds, torch.int32, (E + 1,))
+        po = _array("order", order, torch.int32, (T * k,))
+        ps = _array("slot", slot, torch.int32, (T, k))
+        if ws is None and T * k:
+            ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
+    _enqueue(_lib.bitsmoe_moe_route, dev, stream, _dtype(logits), pl, ld, T, E, k, int(renorm),
+             scale, pi, pg, pb, po, ps, _ptr(ws), 0 if ws is None else _nbytes(ws))
+    return ids, g
+
+
+def moe_route_grad(logits, ids, dg, dlogits=None, renorm=False, scale=1.0, stream=None):
+    """dlogits (T x E, the logits' dtype) from dg (T x k float32) and the ids
+    that moe_route gave for these logits."""
+    import torch
+    T, E = logits.shape
+    k = ids.shape[1]
+    dev = _same_device(logits, ids, dg, dlogits)
+    pl, ld = _matrix("logits", logits)
+    if dlogits is None:
+        dlogits = _new((T, E), logits.dtype, dev, stream)
+    if dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must have the logits' dtype")
+    pd, ldd = _matrix("dlogits", dlogits, (T, E))
+    _enqueue(_lib.bitsmoe_moe_route_grad, dev, stream, _dtype(logits), pl, ld,
+             _array("ids", ids, torch.int32, (T, k)), _array("dg", dg, torch.float32, (T, k)), T,
+             E, k, int(renorm), scale, pd, ldd)
+    return dlogits
+
+
+def _gather(x, rows, div, R):
+    import torch
+    if rows is None:
+        if x.shape[0] < R:
+            raise ValueError("x has %d rows, the sorted layout %d" % (x.shape[0], R))
+        return None, 1
+    return _array("rows", rows, torch.int32, (R,)), div
+
+
+def _bounds(bounds, E):
+    import torch
+    return _array("bounds", bounds, torch.int32, (E + 1,))
+
+
+def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None):
+    """y (R x N) with y[i] = W_e x[i] for the sorted rows i of expert e.
+    w: E x N x K; with act="silu_mul" E x 2N x K (gate rows first) and y =
+    SiLU(gate) * up.  rows (R int32): row i reads x[rows[i] // div].  y has
+    x's dtype, or float32 where it is given so."""
+    import torch
+    E, n2, K = w.shape
+    N = n2 // 2 if act else n2
+    if act not in ACT or (act and n2 % 2):
+        raise ValueError("act=%r with %d rows of w" % (act, n2))
+    R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x.shape[0]
+    dev = _same_device(x, w, bounds, y, rows)
+    px, ldx = _matrix("x", x, (x.shape[0], K))
+    pr, div = _gather(x, rows, div, R)
+    if y is None:
+        y = _new((R, N), x.dtype, dev, stream)
+    py, ldy = _matrix("y", y, (R, N))
+    _enqueue(_lib.bitsmoe_grouped_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div,
+             _array("w", w, x.dtype, (E, n2, K)), _bounds(bounds, E), R, E, N, K, ACT[act], py,
+             _dtype(y), ldy)
+    return y
+
+
+def grouped_matmul_dx(dy, w, bounds, dx=None, stream=None):
+    """dx (R x K) with dx[i] = W_e^T dy[i]: the gradient of grouped_matmul's
+    sorted rows (of a gathered x, moe_combine adds up a token's rows)."""
+    import torch
+    E, N, K = w.shape
+    R = dy.shape[0]
+    dev = _same_device(dy, w, bounds, dx)
+    pd, ldd = _matrix("dy", dy, (R, N))
+    if dx is None:
+        dx = _new((R, K), dy.dtype, dev, stream)
+    px, ldx = _matrix("dx", dx, (R, K))
+    _enqueue(_lib.bitsmoe_grouped_matmul_dx, dev, stream, _dtype(dy), pd, ldd,
+             _array("w", w, dy.dtype, (E, N, K)), _bounds(bounds, E), R, E, N, K, px, _dtype(dx),
+             ldx)
+    return dx
+
+
+def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
+    """dw (E x N x K) with dw_e = sum of dy[i] x[i]^T over the sorted rows of
+    expert e; 0 for an expert without rows.  float32 unless dw is given."""
+    import torch
+    R, N = dy.shape
+    K = x.shape[1]
+    E = bounds.shape[0] - 1
+    dev = _same_device(dy, x, bounds, dw, rows)
+    pd, ldd = _matrix("dy", dy)
+    px, ldx = _matrix("x", x)
+    if x.dtype != dy.dtype:
+        raise ValueError("x and dy must have one dtype")
+    pr, div = _gather(x, rows, div, R)
+    if dw is None:
+        dw = _new((E, N, K), torch.float32, dev, stream)
+    _enqueue(_lib.bitsmoe_grouped_matmul_dw, dev, stream, _dtype(dy), pd, ldd, px, ldx, x.shape[0],
+             pr, div, _bounds(bounds, E), R, E, N, K, _array("dw", dw, dw.dtype, (E, N, K)),
+             _dtype(dw))
+    return dw
+
+
+def silu_mul(a, h=None, bounds=None, stream=None):
+    """h (R x F) = SiLU(gate) * up of rows a = [gate | up] (R x 2F); with
+    bounds only the experts' rows."""
+    import torch
+    R, F2 = a.shape
+    dev = _same_device(a, h, bounds)
+    pa, lda = _matrix("a", a)
+    if F2 % 2:
+        raise ValueError("a has %d columns" % F2)
+    if h is None:
+        h = _new((R, F2 // 2), a.dtype, dev, stream)
+    if h.dtype != a.dtype:
+        raise ValueError("h must have a's dtype")
+    ph, ldh = _matrix("h", h, (R, F2 // 2))
+    E = 0 if bounds is None else bounds.shape[0] - 1
+    _enqueue(_lib.bitsmoe_silu_mul, dev, stream, _dtype(a), pa, lda,
+             None if bounds is None else _bounds(bounds, E), R, E, F2 // 2, ph, ldh)
+    return h
+
+
+def silu_mul_grad(a, dh, da=None, bounds=None, stream=None):
+    """da (R x 2F) from a and dh (R x F); da may be a itself."""
+    import torch
+    R, F2 = a.shape
+    dev = _same_device(a, dh, da, bounds)
+    pa, lda = _matrix("a", a)
+    if F2 % 2:
+        raise ValueError("a has %d columns" % F2)
+    if da is None:
+        da = _new((R, F2), a.dtype, dev, stream)
+    if dh.dtype != a.dtype or da.dtype != a.dtype:
+        raise ValueError("dh and da must have a's dtype")
+    pd, ldd = _matrix("dh", dh, (R, F2 // 2))
+    po, ldo = _matrix("da", da, (R, F2))
+    E = 0 if bounds is None else bounds.shape[0] - 1
+    _enqueue(_lib.bitsmoe_silu_mul_grad, dev, stream, _dtype(a), pa, lda, pd, ldd,
+             None if bounds is None else _bounds(bounds, E), R, E, F2 // 2, po, ldo)
+    return da
+
+
+def moe_combine(y, slot, g=None, out=None, stream=None):
+    """out (T x D) = sum over j of g[t, j] * y[slot[t, j]], in slot order; a
+    slot of -1 has no row.  out has y's dtype, or float32 where given so."""
+    import torch
+    T, k = slot.shape
+    R, D = y.shape
+    dev = _same_device(y, slot, g, out)
+    py, ldy = _matrix("y", y)
+    if out is None:
+        out = _new((T, D), y.dtype, dev, stream)
+    po, ldo = _matrix("out", out, (T, D))
+    _enqueue(_lib.bitsmoe_moe_combine, dev, stream, _dtype(y), py, ldy, R,
+             _array("slot", slot, torch.int32, (T, k)),
+             None if g is None else _array("g", g, torch.float32, (T, k)), T, k, D, po, _dtype(out),
+             ldo)
+    return out
+
+
+def moe_combine_grad(dout, y, slot, g=None, dy=None, dg=None, stream=None):
+    """(dy, dg) of moe_combine: dy[slot[t, j]] = g[t, j] * dout[t] (other rows
+    as they were), dg[t, j] = <dout[t], y[slot[t, j]]>; the slots differ."""
+    import torch
+    T, k = slot.shape
+    R, D = y.shape
+    dev = _same_device(dout, y, slot, g, dy, dg)
+    py, ldy = _matrix("y", y)
+    pd, ldd = _matrix("dout", dout, (T, D))
+    if dy is None:
+        dy = _new((R, D), y.dtype, dev, stream, zero=True)
+    if dg is None:
+        dg = _new((T, k), torch.float32, dev, stream)
+    if dy.dtype != y.dtype:
+        raise ValueError("dy must have y's dtype")
+    pdy, lddy = _matrix("dy", dy, (R, D))
+    _enqueue(_lib.bitsmoe_moe_combine_grad, dev, stream, pd, _dtype(dout), ldd, _dtype(y), py, ldy,
+             R, _array("slot", slot, torch.int32, (T, k)),
+             None if g is None else _array("g", g, torch.float32, (T, k)), T, k, D, pdy, lddy,
+             _array("dg", dg, torch.float32, (T, k)))
+    return dy, dg
+
+
+def w4_pack(w, group=128):
+    """(codes, scales, mins) of dense host weights w (... x K float32), 4 bits
+    with a step and a minimum per `group` inputs."""
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    K = w.shape[-1]
+    if group < 1 or K % group:
+        raise ValueError("K=%d is not a multiple of the group of %d" % (K, group))
+    lead = w.shape[:-1]
+    rows = int(np.prod(lead, dtype=np.int64))
+    codes = np.empty(lead + (K // 2,), np.uint8)
+    scales = np.empty(lead + (K // group,), np.float16)
+    mins = np.empty_like(scales)
+    _check(_lib.bitsmoe_w4_pack(w.ctypes.data, rows, K, group, codes.ctypes.data,
+                                scales.ctypes.data, mins.ctypes.data))
+    return codes, scales, mins
+
+
+def w4_matmul(x, codes, scales, mins=None, y=None, bounds=None, rows=None, div=1, act=None,
+              stream=None):
+    """y (R x N) = W x with 4-bit weights W = mins + scales * codes, per group
+    of K / scales.shape[-1] inputs (mins None: -8 * scales).  codes: E x N x
+    K/2 uint8 (or N x K/2 for one dense projection); bounds, rows, div and act
+    as for grouped_matmul (bounds may be None when E is 1)."""
+    import torch
+    if codes.dim() == 2:
+        codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+        mins = None if mins is None else mins.unsqueeze(0)
+    E, n2, half = codes.shape
+    K, groups = 2 * half, scales.shape[-1]
+    N = n2 // 2 if act else n2
+    if act not in ACT or (act and n2 % 2):
+        raise ValueError("act=%r with %d rows of codes" % (act, n2))
+    if groups < 1 or K % groups:
+        raise ValueError("%d inputs in %d groups" % (K, groups))
+    R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x.shape[0]
+    dev = _same_device(x, codes, scales, mins, y, bounds, rows)
+    px, ldx = _matrix("x", x, (x.shape[0], K))
+    pr, div = _gather(x, rows, div, R)
+    if y is None:
+        y = _new((R, N), x.dtype, dev, stream)
+    py, ldy = _matrix("y", y, (R, N))
+    _enqueue(_lib.bitsmoe_w4_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div,
+             _array("codes", codes, torch.uint8, (E, n2, half)),
+             _array("scales", scales, torch.float16, (E, n2, groups)),
+             None if mins is None else _array("mins", mins, torch.float16, (E, n2, groups)),
+             K // groups, None if bounds is None else _bounds(bounds, E), R, E, N, K, ACT[act], py,
+             _dtype(y), ldy)
+    return y

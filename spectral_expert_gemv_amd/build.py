@@ -19,8 +19,9 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libbitsmoe.so")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["common.cpp", "pack.cpp"]
-HIP_SOURCES = ["bitsmoe.hip", "fused.hip", "one.hip", "grouped.hip", "pack_gpu.hip", "fqcm.hip", "down.hip", "ssd.hip"]
+HOST_SOURCES = ["common.cpp", "pack.cpp", "experts/w4_pack.cpp"]
+HIP_SOURCES = ["bitsmoe.hip", "fused.hip", "one.hip", "grouped.hip", "pack_gpu.hip", "fqcm.hip", "down.hip", "ssd.hip",
+               "experts/route.hip", "experts/act.hip", "experts/gemm.hip", "experts/w4.hip"]
 
 HIP_FLAGS = [
     "-x", "hip", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
@@ -60,11 +61,11 @@ def build(verbose: bool = False) -> str:
     objs = []
     inc = ["-I", INCLUDE, "-I", CSRC]
     for src in HOST_SOURCES:
-        obj = os.path.join(bdir, src + ".o")
+        obj = os.path.join(bdir, src.replace("/", "_") + ".o")
         _run([hipcc] + HOST_FLAGS + inc + ["-c", os.path.join(CSRC, src), "-o", obj], verbose)
         objs.append(obj)
     for src in HIP_SOURCES:
-        obj = os.path.join(bdir, src + ".o")
+        obj = os.path.join(bdir, src.replace("/", "_") + ".o")
         _run([hipcc] + HIP_FLAGS + inc + ["-c", os.path.join(CSRC, src), "-o", obj], verbose)
         objs.append(obj)
     tmp = OUT + ".tmp"
