@@ -141,6 +141,19 @@ __device__ inline Tile find_tile(const int32_t* __restrict__ bounds, int E, int 
   return Tile{0, 0, 0};
 }
 
+// Tiles of up to BM rows of all experts (whole waves call it).
+__device__ inline int count_tiles(const int32_t* __restrict__ bounds, int E, int R, int BM) {
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < E; e += 64) {
+    int lo, hi;
+    expert_rows(bounds, e, R, lo, hi);
+    n += (hi - lo + BM - 1) / BM;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) n += __shfl_xor(n, d, 64);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
 // The most tiles of BM rows that R rows of E experts can make.
 inline long long max_tiles(long long R, long long E, long long BM) {
   return R / BM + (R < E ? R : E);

@@ -4,6 +4,8 @@
 //   dx       dx_i = W_e^T dy_i
 //   dw       dW_e = sum_i dy_i x_i^T
 // fp16 or bf16 operands, float32 accumulators, one rounding at the end.
+#include <type_traits>
+
 #include "experts.h"
 
 namespace bitsmoe {
@@ -150,9 +152,9 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs s) {
 
 // -------------------------------------------------------- tiled, 16-byte rows
 // Work-group tile of TM output rows x TN output columns, WM x WN waves, the
-// contraction in steps of 64.  Every step's two operand tiles are copied
+// contraction in steps of 64 (whole 128-byte lines of a row).  Every step's two operand tiles are copied
 // straight into LDS by 16-byte loads (no registers in between) into one of
-// two buffers, a step ahead of the products.
+// kBufs buffers, kBufs - 1 steps ahead of the products.
 //
 // An operand whose rows run along the contraction lies in LDS as
 // [row][64 elements]: 16-byte piece p of row r at place p ^ (r / 2 % 8), so
@@ -177,7 +179,12 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
                : "v"(src), "s"(lds)
                : "memory");
 }
-__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+// all but the last kLeft copies of the wave have landed
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() {
+  static_assert(kLeft < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);
+}
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
@@ -194,16 +201,16 @@ typedef __attribute__((ext_vector_type(8))) short s16x8;
 // global addresses of the pieces they copy each step.
 template <int B, bool kTr, int NT>
 struct Operand {
-  static constexpr int kCopies = B * kStep * 2 / 16 / NT;
   static constexpr int kBytes = B * kStep * 2;
+  static constexpr int kCopies = kBytes / 16 / NT;
+  static_assert(kCopies * NT * 16 == kBytes, "whole copies");
   const uint8_t* ptr[kCopies];
-  int step[kCopies];  // bytes per step (kTr: unused)
 
   // place of a lane's piece in copy i: line of the tile, and the 16-byte
   // piece of that line it has to fetch
   static __device__ __forceinline__ int line(int i) {
     const int at = i * NT + threadIdx.x;
-    return kTr ? at / (B / 8) : at / 8;
+    return kTr ? at / (B / 8) : at / (kStep / 8);
   }
   static __device__ __forceinline__ int key(int l) {
     return kTr ? (l & 3) | ((l >> 1) & 4) : (l >> 1) & 7;
@@ -214,75 +221,70 @@ struct Operand {
       const int p = at % (B / 8), l = at / (B / 8);
       return (((p >> 1) ^ key(l)) << 1) | (p & 1);
     }
-    return (at % 8) ^ key(at / 8);
+    return (at % (kStep / 8)) ^ key(at / (kStep / 8));
   }
-  // LDS byte offset of the wave's piece run of copy i
-  static __device__ __forceinline__ uint32_t dest(uint32_t base, int i) {
-    return base + (uint32_t)__builtin_amdgcn_readfirstlane((i * NT + (threadIdx.x & ~63)) * 16);
+  // LDS address of the wave's piece run of copy i
+  static __device__ __forceinline__ uint32_t dest(uint32_t base, int wv, int i) {
+    return base + (uint32_t)(i * NT + wv * 64) * 16;
   }
 
-  // 8 consecutive contraction elements (32 s + 8 (lane / 16) ..) of row or
-  // column r + lane % 16
-  template <class T>
-  static __device__ __forceinline__ typename Vec8<T>::type frag(uint32_t base, int r, int s) {
+  // A lane's offset in the tile for the matrix-core piece of rows (columns)
+  // r0 .. r0 + 15, r0 a multiple of 16, and the piece itself, 16 g rows on: 8
+  // consecutive contraction elements (8 (lane / 16) ..) of row or column
+  // r0 + 16 g + lane % 16.  Both layouts' keys depend on the lane alone; in
+  // the transposed one the block's index enters by xor.
+  static __device__ __forceinline__ uint32_t lane_offset(int r0) {
     const int lane = threadIdx.x & 63;
+    if (kTr) {
+      const int i = lane & 15, c = 8 * (lane >> 4) + (i >> 2);
+      return c * (B * 2) + (((r0 >> 4) ^ key(c)) << 5) + (i & 3) * 8;
+    }
+    const int l = lane & 15;
+    return (r0 + l) * (kStep * 2) + (((lane >> 4) ^ key(l)) << 4);
+  }
+  // (half: which 32 of the step's contraction)
+  template <class T>
+  static __device__ __forceinline__ typename Vec8<T>::type frag(uint32_t at, int g, int half) {
     if constexpr (kTr) {
       typedef __attribute__((address_space(3))) s16x4 lds_s4;
-      const int g = lane >> 4, i = lane & 15;
       s16x8 v;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = 32 * s + 8 * g + 4 * h + (i >> 2);
-        const int unit = (r >> 4) ^ key(c);
+      for (int h = 0; h < 2; ++h) {  // (contraction + 4 has the same key)
         const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s4*)(uintptr_t)(base + c * (B * 2) + unit * 32 + (i & 3) * 8));
+            (lds_s4*)(uintptr_t)((at ^ (g << 5)) + (h * 4 + half * 32) * (B * 2)));
         v[4 * h] = t[0], v[4 * h + 1] = t[1], v[4 * h + 2] = t[2], v[4 * h + 3] = t[3];
       }
       return __builtin_bit_cast(typename Vec8<T>::type, v);
     } else {
-      const int row = r + (lane & 15), p = 4 * s + (lane >> 4);
       typedef __attribute__((address_space(3))) const s16x8 lds_s8;
       return __builtin_bit_cast(typename Vec8<T>::type,
-                                *(lds_s8*)(uintptr_t)(base + row * (kStep * 2) +
-                                                      ((p ^ key(row)) << 4)));
+                                *(lds_s8*)(uintptr_t)((at ^ (half << 6)) + g * 16 * (kStep * 2)));
     }
   }
 };
 
-template <class T, class O, int MODE, int TM, int TN, int WM, int WN, bool ACT>
-__global__ __launch_bounds__(64 * WM* WN) void k_mm_tile(MmArgs s, int mtiles_cap) {
+// Tile `id` of mt x nt in the order that keeps the 32 work-groups of an XCD on
+// shared operand rows (in its L2): 4 row tiles by 8 column tiles, then the
+// next columns.
+__device__ __forceinline__ void tile_place(uint32_t id, int mt, int nt, int& m, int& n) {
+  const uint32_t g = id / (4u * nt), r = id - g * (4u * nt);
+  const uint32_t gm = min(4, mt - (int)g * 4);
+  m = g * 4 + r % gm;
+  n = r / gm;
+}
+
+// Output rows m0 .. m0 + mn and columns n0 .. n0 + nn of expert e, with the
+// contraction c0 .. c0 + cn.
+template <class T, class O, int MODE, int TM, int TN, int WM, int WN, int kBufs, bool ACT>
+__device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, int m0, int mn,
+                                        int n0, int nn, int c0, int cn) {
   constexpr int NT = 64 * WM * WN;
   constexpr int MI = TM / WM / 16, NI = TN / WN / 16;  // 16 x 16 tiles of a wave
   constexpr bool kTrA = MODE == kDw, kTrB = MODE != kFwd;
   typedef Operand<TM, kTrA, NT> OpA;
   typedef Operand<TN, kTrB, NT> OpB;
   constexpr uint32_t kBuf = OpA::kBytes + OpB::kBytes;
-  __shared__ __align__(128) uint8_t lds[2 * kBuf];
-  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int cols = MODE == kFwd ? s.N : s.K;  // output columns
-  constexpr int kCols = ACT ? TN / 2 : TN;    // of them per tile
-  const int ntn = (cols + kCols - 1) / kCols;
-  int e, m0, mn, c0, cn, nt;
-  if (MODE == kDw) {
-    const int ntm = (s.N + TM - 1) / TM;
-    const int per = ntm * ntn;
-    int b = blockIdx.x;
-    e = b / per;
-    b -= e * per;
-    m0 = (b / ntn) * TM, mn = min(TM, s.N - m0), nt = b % ntn;
-    int hi;
-    expert_rows(s.bounds, e, s.R, c0, hi);
-    cn = hi - c0;
-  } else {
-    const Tile t = find_tile(s.bounds, s.E, s.R, blockIdx.x % mtiles_cap, TM);
-    if (t.n == 0) return;
-    nt = blockIdx.x / mtiles_cap;
-    e = t.e, m0 = t.row0, mn = t.n;
-    c0 = 0, cn = MODE == kFwd ? s.K : s.N;
-  }
-  const int n0 = nt * kCols, nn = min(kCols, cols - n0);
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // addresses of the pieces of step 0
   OpA a;
@@ -291,17 +293,17 @@ __global__ __launch_bounds__(64 * WM* WN) void k_mm_tile(MmArgs s, int mtiles_ca
   const uint8_t* Bp = (const uint8_t*)s.b;
   if (MODE != kDw) Bp += (size_t)e * (ACT ? 2 : 1) * s.N * s.K * 2;
   const int64_t lda = s.lda * 2, ldb = MODE == kDw ? s.ldb * 2 : (int64_t)s.K * 2;
+  uint32_t nan_rows = 0;  // bit i: copy i's row of A lies outside x
 #pragma unroll
   for (int i = 0; i < OpA::kCopies; ++i) {
     const int l = OpA::line(i), p = OpA::piece(i);
-    a.step[i] = kStep * 2;
     if (kTrA) {
       a.ptr[i] = A + (int64_t)(c0 + l) * lda + (int64_t)(m0 + min(8 * p, mn - 8)) * 2;
     } else {
       const int row = m0 + min(l, mn - 1);
       const int xr = MODE == kFwd ? x_row(s, row) : row;
       a.ptr[i] = A + (int64_t)xr * lda + p * 16;
-      if (xr < 0) a.ptr[i] = (const uint8_t*)(g_pad + 4), a.step[i] = 0;
+      if (xr < 0) a.ptr[i] = (const uint8_t*)(g_pad + 4), nan_rows |= 1u << i;
     }
   }
 #pragma unroll
@@ -316,63 +318,145 @@ __global__ __launch_bounds__(64 * WM* WN) void k_mm_tile(MmArgs s, int mtiles_ca
       b.ptr[i] = Bp + (int64_t)(MODE == kDw ? 0 : l) * ldb + (int64_t)(n0 + min(8 * p, nn - 8)) * 2;
     }
   }
-  // dw: rows of x of the next step (-1: outside x)
-  int xr[MODE == kDw ? OpB::kCopies : 1];
-  auto fetch_rows = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < (MODE == kDw ? OpB::kCopies : 1); ++i)
-      xr[i] = c + OpB::line(i) < cn ? x_row(s, c0 + c + OpB::line(i)) : 0;
-  };
-  if (MODE == kDw) fetch_rows(0);
 
-  // copies of the step at contraction index c into the buffer at `buf`;
-  // pieces past the end of the contraction are 0
-  auto stage = [&](int c, uint32_t buf) {
-    const bool whole = c + kStep <= cn;
+  // The row of x in line l (of 64 lanes at most two lines) of a step of dw,
+  // read through the scalar cache: a vector load would make its reader wait
+  // for the copies in flight.
+  auto dw_row = [&](int i, int c) -> int {
+    constexpr int kPer = 64 / (TN / 8);  // lines of a wave's copy
+    static_assert(MODE != kDw || kPer == 1 || kPer == 2 || kPer == 4, "lines per copy");
+    const int l0 = (i * NT + wv * 64) / (TN / 8);
+    const int l = OpB::line(i) - l0;
+    int r = -1;
 #pragma unroll
-    for (int i = 0; i < OpA::kCopies; ++i) {
+    for (int u = 0; u < kPer; ++u) {
+      const int at = c + l0 + u;
+      int v = c0 + at;
+      if (s.rows) {
+        typedef __attribute__((address_space(4))) const int32_t cint;
+        v = at < cn ? ((cint*)(uintptr_t)s.rows)[v] : -1;
+        v = v < 0 ? -1 : v / s.div;
+        v = v < s.x_rows ? v : -1;
+      }
+      if (l == u) r = v;
+    }
+    return r;
+  };
+
+  // Piece i of the copies of the step at contraction index c into the buffer
+  // at `buf` (A's pieces first).  Pieces past the end of the contraction are
+  // 0; steps past it are copied too (as 0), so that the counts of copies in
+  // flight stay the same.
+  auto stage_piece = [&](int i, int c, bool whole, uint32_t buf) {
+    if (i < OpA::kCopies) {
       const uint8_t* p = a.ptr[i];
       if (!whole && c + (kTrA ? OpA::line(i) : 8 * OpA::piece(i)) >= cn) p = (const uint8_t*)g_pad;
-      copy16(p, OpA::dest(buf, i));
-      a.ptr[i] += kTrA ? (int64_t)kStep * lda : (int64_t)a.step[i];
-    }
-#pragma unroll
-    for (int i = 0; i < OpB::kCopies; ++i) {
+      copy16(p, OpA::dest(buf, wv, i));
+      if (kTrA)
+        a.ptr[i] += (int64_t)kStep * lda;
+      else
+        a.ptr[i] += (nan_rows >> i) & 1 ? 0 : kStep * 2;
+    } else {
+      i -= OpA::kCopies;
       const uint8_t* p = b.ptr[i];
       if (MODE == kDw) {
-        p = xr[i] < 0 ? (const uint8_t*)(g_pad + 4) : p + (int64_t)xr[i] * ldb;
+        const int r = dw_row(i, c);
+        p = r < 0 ? (const uint8_t*)(g_pad + 4) : p + (int64_t)r * ldb;
       }
       if (!whole && c + (kTrB ? OpB::line(i) : 8 * OpB::piece(i)) >= cn) p = (const uint8_t*)g_pad;
-      copy16(p, OpB::dest(buf + OpA::kBytes, i));
+      copy16(p, OpB::dest(buf + OpA::kBytes, wv, i));
       if (MODE == kFwd) b.ptr[i] += kStep * 2;
       if (MODE == kDx) b.ptr[i] += (int64_t)kStep * ldb;
     }
   };
-
+  constexpr int kPieces = OpA::kCopies + OpB::kCopies;
+  // A step is two halves of MI groups of NI products with one A piece; the LDS reads run
+  // kAhead groups before the products, across the steps' border.  There (group
+  // kSwitch) the wave waits for its copies of the next step, meets the
+  // others, and starts to copy a later step into the buffer that nobody reads
+  // any more; the last groups' products run meanwhile.
+  constexpr int kAhead = 3, kGroups = kStep / 32 * MI, kSwitch = kGroups - kAhead;
+  static_assert(MI % (kAhead + 1) == 0 && kStep == 64, "turns of the registers");
+  typedef typename Vec8<T>::type Frag;
   const int wm = (wv / WN) * (TM / WM), wn = (wv % WN) * (TN / WN);
+  // (buffers start at multiples of 1024 bytes, so adding one keeps the xor)
+  const uint32_t off_a = OpA::lane_offset(wm), off_b = OpA::kBytes + OpB::lane_offset(wn);
   f32x4 acc[MI][NI] = {};
-  uint32_t cur = base;
-  if (cn > 0) stage(0, cur);
-  for (int c = 0; c < cn; c += kStep) {
-    if (MODE == kDw && c + kStep < cn) fetch_rows(c + kStep);
-    wait_copies();
-    lds_barrier();  // this step's copies are in, and nobody reads the other buffer any more
-    const uint32_t next = base + (cur == base ? kBuf : 0u);
-    if (c + kStep < cn) stage(c + kStep, next);
+  Frag fa[kAhead + 1], fb[2][NI];
+  auto read_a = [&](int g, uint32_t at) {  // (at: the lane's own address)
+    fa[g % (kAhead + 1)] = OpA::template frag<T>(at, g % MI, g / MI);
+  };
+  // B pieces of one half of a step, the first of them or the others
+  auto read_b = [&](int half, int part, uint32_t at) {
 #pragma unroll
-    for (int k = 0; k < kStep / 32; ++k) {
-      typename Vec8<T>::type fa[MI], fb[NI];
+    for (int j = 0; j < NI; ++j)
+      if (j * 2 / NI == part) fb[half][j] = OpB::template frag<T>(at, j, half);
+  };
+  uint32_t cur = base, at_a = base + off_a, at_b = base + off_b;
+  // kind 0: the step copied meanwhile is whole; 1: it may not be; 2: there is
+  // no next step
+  auto step = [&](int c, auto kind_) {
+    constexpr int kKind = decltype(kind_)::value;
+    constexpr bool kLast = kKind == 2;
+    const uint32_t nxt = cur + kBuf == base + kBufs * kBuf ? base : cur + kBuf;
+    uint32_t next_a = nxt + off_a, next_b = nxt + off_b;
+    asm("" : "+v"(next_a), "+v"(next_b));  // one register and immediate offsets each
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (!kLast && g == kSwitch) {
+        wait_copies<(kBufs - 2) * kPieces>();
+        lds_barrier();
+      }
+      if (!kLast || g + kAhead < kGroups) {
+        const int ahead = (g + kAhead) % kGroups;
+        const bool here = g + kAhead < kGroups;
+        if (ahead % MI == 0) read_b(ahead / MI, 0, here ? at_b : next_b);
+        read_a(ahead, here ? at_a : next_a);
+        if (ahead % MI == 1) read_b(ahead / MI, 1, here ? at_b : next_b);
+      }
+      if (!kLast && g >= kSwitch) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if (i * kAhead / kPieces == g - kSwitch)
+            stage_piece(i, c + kBufs * kStep, kKind == 0, cur);
+      }
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        fb[j] = OpB::template frag<T>(cur + OpA::kBytes, wn + 16 * j, k);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = OpA::template frag<T>(cur, wm + 16 * i, k);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16(fb[j], fa[i], acc[i][j]);
+        acc[g % MI][j] = mfma16(fb[g / MI][j], fa[g % (kAhead + 1)], acc[g % MI][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    cur = next;
+    cur = nxt, at_a = next_a, at_b = next_b;
+  };
+  if (cn > 0) {
+#pragma unroll 1
+    for (int i = 0; i < kBufs; ++i)
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) stage_piece(j, i * kStep, false, base + i * kBuf);
+    wait_copies<(kBufs - 1) * kPieces>();
+    lds_barrier();
+    int c = 0;
+    using std::integral_constant;
+    if (wm < mn) {
+      read_b(0, 0, at_b);
+      read_a(0, at_a);
+      read_b(0, 1, at_b);
+      read_a(1, at_a);
+      read_a(2, at_a);
+      for (; c + (kBufs + 1) * kStep <= cn; c += kStep) step(c, integral_constant<int, 0>{});
+#pragma unroll 1
+      for (; c + kStep < cn; c += kStep) step(c, integral_constant<int, 1>{});
+      step(c, integral_constant<int, 2>{});
+    } else {  // a wave past the tile's rows only copies
+#pragma unroll 1
+      for (; c + kStep < cn; c += kStep) {
+        wait_copies<(kBufs - 2) * kPieces>();
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) stage_piece(i, c + kBufs * kStep, false, cur);
+        cur = cur + kBuf == base + kBufs * kBuf ? base : cur + kBuf;
+      }
+    }
+    wait_copies<0>();  // nothing is written into this work-group's LDS after its end
   }
 
   // the products were formed transposed: lane % 16 is the output row, and a
@@ -401,6 +485,65 @@ __global__ __launch_bounds__(64 * WM* WN) void k_mm_tile(MmArgs s, int mtiles_ca
         *reinterpret_cast<O4*>(row + n) = o;
       }
     }
+  }
+}
+
+// One work-group per tile: first the whole rounds of the chip's compute units
+// with 256 x 256 tiles, then what is left, cut into 128 x 128 tiles if it
+// would fill at most half a round (see kSplitMost).
+constexpr int kUnits = 256;       // compute units of an MI355X, one work-group each (its LDS)
+constexpr int kTile = 256;        // rows and columns of a tile
+constexpr int kSplitMost = 128;   // left-over tiles that are cut in four
+constexpr int kBufs = 2;
+
+template <class T, class O, int MODE, bool ACT>
+__global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
+  constexpr uint32_t kLds = 2 * kTile * kStep * 2 * kBufs;
+  __shared__ __align__(1024) uint8_t lds[kLds];
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const int cols = MODE == kFwd ? s.N : s.K;     // output columns
+  constexpr int kCols = ACT ? kTile / 2 : kTile; // of them per tile
+  const int ntn = (cols + kCols - 1) / kCols, ntm = (s.N + kTile - 1) / kTile;
+  const int mt = MODE == kDw ? s.E * ntm : count_tiles(s.bounds, s.E, s.R, kTile);
+  const uint32_t total = (uint32_t)mt * ntn, left = total % kUnits;
+  const uint32_t whole = left <= kSplitMost ? total - left : total;
+  // Work-group b runs on XCD b % 8, and every XCD takes one run of tiles.
+  uint32_t b = blockIdx.x, id;
+  int part = -1;
+  const uint32_t run = (whole + 7) / 8;
+  if (b < run * 8) {
+    id = (b & 7) * run + (b >> 3);
+    if (id >= whole) return;
+  } else {
+    b -= run * 8;
+    const uint32_t run4 = ((total - whole) * 4 + 7) / 8;
+    const uint32_t id4 = (b & 7) * run4 + (b >> 3);
+    if ((b >> 3) >= run4 || id4 >= (total - whole) * 4) return;
+    id = whole + id4 / 4;
+    part = id4 & 3;
+  }
+  int e, m0, mn, c0, cn, mi, ni;
+  tile_place(id, mt, ntn, mi, ni);
+  if (MODE == kDw) {
+    e = mi / ntm;
+    m0 = (mi - e * ntm) * kTile, mn = min(kTile, s.N - m0);
+    int hi;
+    expert_rows(s.bounds, e, s.R, c0, hi);
+    cn = hi - c0;
+  } else {
+    const Tile t = find_tile(s.bounds, s.E, s.R, mi, kTile);
+    e = t.e, m0 = t.row0, mn = t.n;
+    c0 = 0, cn = MODE == kFwd ? s.K : s.N;
+  }
+  int n0 = ni * kCols, nn = min(kCols, cols - n0);
+  if (part < 0) {
+    mm_tile<T, O, MODE, kTile, kTile, 2, 4, kBufs, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
+  } else {
+    const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
+    mn = min(kTile / 2, mn - pm), nn = min(kCols / 2, nn - pn);
+    if (mn <= 0 || nn <= 0) return;
+    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, kBufs, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
+                                                                nn, c0, cn);
   }
 }
 
@@ -433,13 +576,6 @@ int mm_check(int dtype, int o_dtype, int R, int E, int N, int K, const int32_t* 
 int rows_check(const int32_t* rows, int div, int x_rows, int R) {
   if (rows ? (div < 1 || x_rows < 0) : x_rows < R)
     return fail(BITSMOE_ESHAPE, "div=%d, %d rows of x for R=%d", div, x_rows, R);
-  return BITSMOE_OK;
-}
-
-int row_grid(int R, int E, int tile, unsigned* out) {
-  const long long n = max_tiles(R, E, tile);
-  if (n > 65535 * 16ll) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);
-  *out = (unsigned)n;
   return BITSMOE_OK;
 }
 
@@ -477,21 +613,21 @@ int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
   with_types(dtype, o_dtype, [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
-    constexpr int TM = 256, TN = 256, WM = 2, WN = 4;
-    const int cols = MODE == kFwd ? s.N : s.K, per = s.act ? TN / 2 : TN;
+    const int cols = MODE == kFwd ? s.N : s.K, per = s.act ? kTile / 2 : kTile;
     const long long ntn = (cols + per - 1) / per;
-    const long long mt = MODE == kDw ? (long long)s.E * ((s.N + TM - 1) / TM) : max_tiles(s.R, s.E, TM);
-    if (mt * ntn > 0x7FFFFFFFll) {
+    const long long mt =
+        MODE == kDw ? (long long)s.E * ((s.N + kTile - 1) / kTile) : max_tiles(s.R, s.E, kTile);
+    if (mt * ntn > 0x1FFFFFFFll) {
       rc = fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", s.R, s.E, s.N, s.K);
       return;
     }
-    const dim3 grid((unsigned)(mt * ntn));
+    // enough for any split of at most mt * ntn tiles into whole and cut ones
+    const long long cut = mt * ntn < kSplitMost ? mt * ntn : kSplitMost;
+    const dim3 grid((unsigned)((mt * ntn + 7) / 8 * 8 + cut * 3 + 8));
     if (MODE == kFwd && s.act)
-      hipLaunchKernelGGL((k_mm_tile<T, O, MODE, TM, TN, WM, WN, MODE == kFwd>), grid,
-                         dim3(64 * WM * WN), 0, st, s, (int)mt);
+      hipLaunchKernelGGL((k_mm_tile<T, O, MODE, MODE == kFwd>), grid, dim3(512), 0, st, s);
     else
-      hipLaunchKernelGGL((k_mm_tile<T, O, MODE, TM, TN, WM, WN, false>), grid, dim3(64 * WM * WN),
-                         0, st, s, (int)mt);
+      hipLaunchKernelGGL((k_mm_tile<T, O, MODE, false>), grid, dim3(512), 0, st, s);
     rc = launched("grouped_matmul");
   });
   return rc;
