@@ -154,7 +154,7 @@ __global__ __launch_bounds__(256) void k_mm_any(MmArgs s) {
 // Work-group tile of TM output rows x TN output columns, WM x WN waves, the
 // contraction in steps of 64 (whole 128-byte lines of a row).  Every step's two operand tiles are copied
 // straight into LDS by 16-byte loads (no registers in between) into one of
-// kBufs buffers, kBufs - 1 steps ahead of the products.
+// two buffers, a step ahead of the products.
 //
 // An operand whose rows run along the contraction lies in LDS as
 // [row][64 elements]: 16-byte piece p of row r at place p ^ (r / 2 % 8), so
@@ -182,8 +182,8 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
 // all but the last kLeft copies of the wave have landed
 template <int kLeft>
 __device__ __forceinline__ void wait_copies() {
-  static_assert(kLeft < 64, "vmcnt field");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);
+  static_assert(kLeft < 16, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | kLeft);
 }
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -275,7 +275,7 @@ __device__ __forceinline__ void tile_place(uint32_t id, int mt, int nt, int& m, 
 
 // Output rows m0 .. m0 + mn and columns n0 .. n0 + nn of expert e, with the
 // contraction c0 .. c0 + cn.
-template <class T, class O, int MODE, int TM, int TN, int WM, int WN, int kBufs, bool ACT>
+template <class T, class O, int MODE, int TM, int TN, int WM, int WN, bool ACT>
 __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, int m0, int mn,
                                         int n0, int nn, int c0, int cn) {
   constexpr int NT = 64 * WM * WN;
@@ -345,13 +345,13 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 
   // Piece i of the copies of the step at contraction index c into the buffer
   // at `buf` (A's pieces first).  Pieces past the end of the contraction are
-  // 0; steps past it are copied too (as 0), so that the counts of copies in
-  // flight stay the same.
+  // 0, and so are steps past it.
   auto stage_piece = [&](int i, int c, bool whole, uint32_t buf) {
     if (i < OpA::kCopies) {
       const uint8_t* p = a.ptr[i];
       if (!whole && c + (kTrA ? OpA::line(i) : 8 * OpA::piece(i)) >= cn) p = (const uint8_t*)g_pad;
-      copy16(p, OpA::dest(buf, wv, i));
+      // (rows past the tile's are not copied: nobody uses what lies there)
+      if (kTrA || whole || i * (NT / 8) < mn) copy16(p, OpA::dest(buf, wv, i));
       if (kTrA)
         a.ptr[i] += (int64_t)kStep * lda;
       else
@@ -398,13 +398,13 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   auto step = [&](int c, auto kind_) {
     constexpr int kKind = decltype(kind_)::value;
     constexpr bool kLast = kKind == 2;
-    const uint32_t nxt = cur + kBuf == base + kBufs * kBuf ? base : cur + kBuf;
+    const uint32_t nxt = cur == base ? base + kBuf : base;
     uint32_t next_a = nxt + off_a, next_b = nxt + off_b;
     asm("" : "+v"(next_a), "+v"(next_b));  // one register and immediate offsets each
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       if (!kLast && g == kSwitch) {
-        wait_copies<(kBufs - 2) * kPieces>();
+        wait_copies<0>();
         lds_barrier();
       }
       if (!kLast || g + kAhead < kGroups) {
@@ -418,7 +418,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
           if (i * kAhead / kPieces == g - kSwitch)
-            stage_piece(i, c + kBufs * kStep, kKind == 0, cur);
+            stage_piece(i, c + 2 * kStep, kKind == 0, cur);
       }
 #pragma unroll
       for (int j = 0; j < NI; ++j)
@@ -428,11 +428,15 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
     cur = nxt, at_a = next_a, at_b = next_b;
   };
   if (cn > 0) {
+    const bool full = kTrA || mn > TM - NT / 8;  // every copy has rows
 #pragma unroll 1
-    for (int i = 0; i < kBufs; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) stage_piece(j, i * kStep, false, base + i * kBuf);
-    wait_copies<(kBufs - 1) * kPieces>();
+    if (full)
+      wait_copies<kPieces>();  // the first step's
+    else
+      wait_copies<0>();
     lds_barrier();
     int c = 0;
     using std::integral_constant;
@@ -442,18 +446,19 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
       read_b(0, 1, at_b);
       read_a(1, at_a);
       read_a(2, at_a);
-      for (; c + (kBufs + 1) * kStep <= cn; c += kStep) step(c, integral_constant<int, 0>{});
+      if (full)
+        for (; c + 3 * kStep <= cn; c += kStep) step(c, integral_constant<int, 0>{});
 #pragma unroll 1
       for (; c + kStep < cn; c += kStep) step(c, integral_constant<int, 1>{});
       step(c, integral_constant<int, 2>{});
     } else {  // a wave past the tile's rows only copies
 #pragma unroll 1
       for (; c + kStep < cn; c += kStep) {
-        wait_copies<(kBufs - 2) * kPieces>();
+        wait_copies<0>();
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) stage_piece(i, c + kBufs * kStep, false, cur);
-        cur = cur + kBuf == base + kBufs * kBuf ? base : cur + kBuf;
+        for (int i = 0; i < kPieces; ++i) stage_piece(i, c + 2 * kStep, false, cur);
+        cur = cur == base ? base + kBuf : base;
       }
     }
     wait_copies<0>();  // nothing is written into this work-group's LDS after its end
@@ -494,11 +499,10 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 constexpr int kUnits = 256;       // compute units of an MI355X, one work-group each (its LDS)
 constexpr int kTile = 256;        // rows and columns of a tile
 constexpr int kSplitMost = 128;   // left-over tiles that are cut in four
-constexpr int kBufs = 2;
 
 template <class T, class O, int MODE, bool ACT>
 __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
-  constexpr uint32_t kLds = 2 * kTile * kStep * 2 * kBufs;
+  constexpr uint32_t kLds = 2 * kTile * kStep * 2 * 2;
   __shared__ __align__(1024) uint8_t lds[kLds];
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const int cols = MODE == kFwd ? s.N : s.K;     // output columns
@@ -537,12 +541,12 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   }
   int n0 = ni * kCols, nn = min(kCols, cols - n0);
   if (part < 0) {
-    mm_tile<T, O, MODE, kTile, kTile, 2, 4, kBufs, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
+    mm_tile<T, O, MODE, kTile, kTile, 2, 4, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
   } else {
     const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
     mn = min(kTile / 2, mn - pm), nn = min(kCols / 2, nn - pn);
     if (mn <= 0 || nn <= 0) return;
-    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, kBufs, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
+    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
                                                                 nn, c0, cn);
   }
 }
