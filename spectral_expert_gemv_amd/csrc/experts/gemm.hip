@@ -551,6 +551,119 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   }
 }
 
+// ------------------------------------------------- few rows per expert, forward
+// Reads every weight once, straight into registers.  A work-group takes up to
+// 64 sorted rows of one expert and 32 rows of its weights (with the
+// activation 16 of the gate and the same 16 of the up half); its four waves
+// split the inputs in turns of 64, a whole 128-byte line of each weight row,
+// and add up their sums through LDS.  The weights are the products' first
+// operand, so that 16 rows of x fill the other side of one matrix-core
+// instruction; rows of x past the tile's repeat the last one.
+constexpr int kFewRows = 64, kFewCols = 32, kFewWaves = 4;
+
+template <class T, class O, bool ACT, int MB>
+__device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* lds) {
+  typedef typename Vec8<T>::type V;
+  constexpr int U = MB == 1 ? 4 : 2;  // turns whose loads are in flight together
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * (ACT ? kFewCols / 2 : kFewCols);
+  const T* w[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t row = ACT ? (int64_t)b * s.N + min(n0 + r, s.N - 1) : min(n0 + 16 * b + r, s.N - 1);
+    w[b] = (const T*)s.b + ((int64_t)t.e * (ACT ? 2 : 1) * s.N + row) * s.K + 8 * q;
+  }
+  const T* x[MB];
+  bool bad[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) {
+    const int xr = x_row(s, t.row0 + min(16 * m + r, t.n - 1));
+    bad[m] = xr < 0;
+    x[m] = (const T*)s.a + (int64_t)max(xr, 0) * s.lda + 8 * q;
+  }
+  f32x4 acc[MB][2] = {};
+  auto turn = [&](int k0, auto whole_) {  // inputs k0 .. and every kFewWaves * 64 on, U times
+    constexpr bool whole = decltype(whole_)::value;
+    V vw[U][2][2], vx[U][MB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = k0 + u * kFewWaves * 64 + 32 * h;
+        const bool in = whole || k + 8 * q < s.K;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          vw[u][b][h] = *reinterpret_cast<const V*>(in ? (const void*)(w[b] + k) : (const void*)g_pad);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+          vx[u][m][h] = *reinterpret_cast<const V*>(in ? (const void*)(x[m] + k) : (const void*)g_pad);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) acc[m][b] = mfma16(vw[u][b][h], vx[u][m][h], acc[m][b]);
+  };
+  constexpr int kTurn = U * kFewWaves * 64;
+  int k = wv * 64;
+  for (; k + kTurn - kFewWaves * 64 + 64 <= s.K; k += kTurn) turn(k, std::true_type{});
+  if (k < s.K) turn(k, std::false_type{});
+
+  // sums of the four waves: [wave][tile of 16 x 16][lane]
+  f32x4* part = (f32x4*)lds;
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) part[(wv * MB * 2 + m * 2 + b) * 64 + lane] = acc[m][b];
+  __syncthreads();
+  O* Y = (O*)s.y;
+  for (int i = wv; i < (ACT ? MB : MB * 2); i += kFewWaves) {
+    const int m = ACT ? i : i >> 1;
+    f32x4 v[2];
+#pragma unroll
+    for (int b = 0; b < (ACT ? 2 : 1); ++b) {
+      const int at = ACT ? m * 2 + b : i;
+      v[b] = part[at * 64 + lane];
+#pragma unroll
+      for (int o = 1; o < kFewWaves; ++o) {
+        const f32x4 p = part[(o * MB * 2 + at) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[b][j] += p[j];
+      }
+    }
+    const int n = n0 + (ACT ? 0 : 16 * (i & 1)) + 4 * q;
+    bool nan = false;
+#pragma unroll
+    for (int u = 0; u < MB; ++u) nan = u == m ? bad[u] : nan;
+    if (16 * m + r >= t.n || n >= s.N) continue;  // (N is a multiple of 8)
+    typedef __attribute__((ext_vector_type(4))) O O4;
+    O4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = ACT ? gated(v[0][j], v[1][j]) : v[0][j];
+      o[j] = (O)(nan ? __builtin_nanf("") : f);
+    }
+    *reinterpret_cast<O4*>(Y + (int64_t)(t.row0 + 16 * m + r) * s.ldy + n) = o;
+  }
+}
+
+template <class T, class O, bool ACT>
+__global__ __launch_bounds__(64 * kFewWaves, 4) void k_mm_few(MmArgs s) {
+  __shared__ float lds[kFewWaves * 8 * 64 * 4];
+  const Tile t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kFewRows);
+  if (t.n == 0) return;
+  if (t.n <= 16)
+    few_rows<T, O, ACT, 1>(s, t, lds);
+  else if (t.n <= 32)
+    few_rows<T, O, ACT, 2>(s, t, lds);
+  else
+    few_rows<T, O, ACT, 4>(s, t, lds);
+}
+
 template <class F>
 void with_types(int dtype, int o_dtype, F f) {
   if (dtype == BITSMOE_F16) {
@@ -610,6 +723,10 @@ bool tiled(const MmArgs& s, int mode, int o_dtype) {
          rows16(s.b, mode == kDw ? s.ldb : s.K) && rows16(s.y, mode == kDw ? s.K : s.ldy);
 }
 
+// Up to this many rows per expert on average the forward product is bound by
+// the weights' bytes.
+constexpr int kFewMean = 32;
+
 template <int MODE>
 int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
   if (!tiled(s, MODE, o_dtype)) return launch_any<MODE>(s, dtype, o_dtype, st);
@@ -617,6 +734,19 @@ int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
   with_types(dtype, o_dtype, [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
+    if constexpr (MODE == kFwd) {
+      const long long tiles = max_tiles(s.R, s.E, kFewRows);
+      if (s.R <= (long long)kFewMean * s.E && tiles <= 65535) {
+        const int per = s.act ? kFewCols / 2 : kFewCols;
+        const dim3 grid((unsigned)((s.N + per - 1) / per), (unsigned)tiles);
+        if (s.act)
+          hipLaunchKernelGGL((k_mm_few<T, O, true>), grid, dim3(64 * kFewWaves), 0, st, s);
+        else
+          hipLaunchKernelGGL((k_mm_few<T, O, false>), grid, dim3(64 * kFewWaves), 0, st, s);
+        rc = launched("grouped_matmul");
+        return;
+      }
+    }
     const int cols = MODE == kFwd ? s.N : s.K, per = s.act ? kTile / 2 : kTile;
     const long long ntn = (cols + per - 1) / per;
     const long long mt =
