@@ -4,6 +4,8 @@
 // SiLU(gate) * up of the two halves of the rows.  Per group
 //   sum_c W x = s (sum_c q x) + m (sum_c x),
 // so the codes enter the products as small whole numbers, exactly.
+#include <type_traits>
+
 #include "experts.h"
 
 namespace bitsmoe {
@@ -32,7 +34,8 @@ __device__ inline int w4_row(const W4Args& s, int i) {
   return r < s.x_rows ? r : -1;
 }
 
-// A wave per (row, output): lanes along the inputs, 8 codes at a time.
+// A wave per (row, output): lanes along the inputs, 8 codes at a time.  For
+// rows of x that are not 16-byte aligned.
 template <class T, class O>
 __global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
   const int lane = threadIdx.x & 63;
@@ -71,6 +74,429 @@ __global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
   }
 }
 
+// ------------------------------------------------------------ 16-byte rows
+// A work-group takes up to 32 rows of one expert and 32 rows of its weights
+// (with the activation 16 of the gate and the same 16 of the up half); its
+// four waves split the inputs in turns of 128 and add up through LDS.  Every
+// code is read once per work-group, 16 bytes (32 inputs of one row) a lane.
+//
+// In a turn lane (r, q) loads the codes of row r, inputs 32 q .. 32 q + 31.
+// One matrix-core step takes 32 inputs, 8 a lane, that have to lie in one
+// group: a 4 x 4 transpose of the words between the four lanes of a row (two
+// row swaps each way) gives lane (r, q) the inputs 32 s + 8 q .. of step s.
+// A word's eight codes become eight fp16 (bf16) values 16 + q, exactly, by a
+// shift and an and-or per pair (q goes into the mantissa of 16.0), in the
+// order 0 4 1 5 2 6 3 7; x is put into that order.  Per group
+//   y += s (sum (16 + q) x) + (m - 16 s) (sum x),
+// where sum x comes from one more matrix-core step with ones.  x is the first
+// operand, so a lane's sums all belong to its own row of weights, whose s and
+// m it holds.  All sums are float32.
+constexpr int kRows = 32, kCols = 32, kWaves = 4, kTurn = 128;
+
+template <class T>
+struct Magic;
+template <>
+struct Magic<f16> {
+  static constexpr int kShift = 6;  // q in mantissa bits 6 .. 9 of 16.0
+  static constexpr uint32_t kMask = 0x03C003C0u, kOr = 0x4C004C00u, kOne = 0x3C003C00u;
+};
+template <>
+struct Magic<bf16> {
+  static constexpr int kShift = 3;  // bits 3 .. 6
+  static constexpr uint32_t kMask = 0x00780078u, kOr = 0x41804180u, kOne = 0x3F803F80u;
+};
+
+// 8 codes of a word as 16 + q, order 0 4 1 5 2 6 3 7
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::type codes8(uint32_t w) {
+  typedef Magic<T> M;
+  uint4 o;
+  auto put = [&](int n) {
+    const int sh = M::kShift - 4 * n;
+    const uint32_t v = sh >= 0 ? w << (sh > 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
+    return (v & M::kMask) | M::kOr;
+  };
+  o.x = put(0), o.y = put(1), o.z = put(2), o.w = put(3);
+  return __builtin_bit_cast(typename Vec8<T>::type, o);
+}
+
+// x in the same order
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::type order8(uint4 v) {
+  uint4 o;
+  o.x = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
+  o.y = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
+  o.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
+  o.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
+  return __builtin_bit_cast(typename Vec8<T>::type, o);
+}
+
+// d[j] of lane row q <- d[q] of lane row j
+__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
+  typedef __attribute__((ext_vector_type(2))) uint32_t u2;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const u2 t = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(d[j], d[j + 2], false, false));
+    d[j] = t[0], d[j + 2] = t[1];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const u2 t = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(d[j], d[j + 1], false, false));
+    d[j] = t[0], d[j + 1] = t[1];
+  }
+}
+
+// the 128 / G float16 values of a turn's groups, from an address that is only
+// 2-byte aligned
+template <int N>
+struct Halves {
+  f16 v[N];
+};
+template <int N>
+__device__ __forceinline__ Halves<N> load_halves(const f16* p) {
+  Halves<N> h;
+  __builtin_memcpy(&h, p, sizeof(h));
+  return h;
+}
+
+template <class T, class O, int G, bool ACT, int MB>
+__device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* lds) {
+  constexpr int U = MB == 1 ? 2 : 1;  // turns whose loads are in flight together
+  constexpr int NG = kTurn / G;                      // groups of a turn
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * (ACT ? kCols / 2 : kCols);
+  const int groups = s.K / G;
+  const uint8_t* codes[2];
+  int64_t group0[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t row = (int64_t)t.e * (ACT ? 2 : 1) * s.N +
+                        (ACT ? (int64_t)b * s.N + min(n0 + r, s.N - 1) : min(n0 + 16 * b + r, s.N - 1));
+    codes[b] = s.codes + row * (s.K / 2) + 16 * q;
+    group0[b] = row * groups;
+  }
+  const T* x[MB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+    x[m] = (const T*)s.x + (int64_t)max(w4_row(s, t.row0 + min(16 * m + r, t.n - 1)), 0) * s.ldx + 8 * q;
+  const uint4 ones = {Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne};
+  const typename Vec8<T>::type one8 = __builtin_bit_cast(typename Vec8<T>::type, ones);
+
+  f32x4 acc[MB][2] = {};
+  auto turns = [&](int k0, auto whole_) {  // inputs k0 .., U turns kWaves * kTurn apart
+    constexpr bool whole = decltype(whole_)::value;
+    uint4 vc[U][2], vx[U][MB][4];
+    Halves<NG> vs[U][2], vm[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kWaves * kTurn;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        vc[u][b] = uint4{0, 0, 0, 0};
+        if (whole || k + 32 * q < s.K) vc[u][b] = *reinterpret_cast<const uint4*>(codes[b] + k / 2);
+        // past the end the row's last groups: x is 0 there
+        if (whole) {
+          vs[u][b] = load_halves<NG>(s.scales + group0[b] + k / G);
+          if (s.mins) vm[u][b] = load_halves<NG>(s.mins + group0[b] + k / G);
+        } else {
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const int64_t at = group0[b] + min(k / G + g, groups - 1);
+            vs[u][b].v[g] = s.scales[at];
+            if (s.mins) vm[u][b].v[g] = s.mins[at];
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vx[u][m][i] = uint4{0, 0, 0, 0};
+          if (whole || k + 32 * i < s.K)
+            vx[u][m][i] = *reinterpret_cast<const uint4*>(x[m] + k + 32 * i);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t d[2][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        d[b][0] = vc[u][b].x, d[b][1] = vc[u][b].y, d[b][2] = vc[u][b].z, d[b][3] = vc[u][b].w;
+        transpose4(d[b]);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4 sum[MB][2] = {}, sx[MB] = {};
+#pragma unroll
+        for (int i = 0; i < 4 / NG; ++i) {
+          const int st = g * (4 / NG) + i;
+          typename Vec8<T>::type w[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) w[b] = codes8<T>(d[b][st]);
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            const typename Vec8<T>::type v = order8<T>(vx[u][m][st]);
+            sx[m] = mfma16(v, one8, sx[m]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) sum[m][b] = mfma16(v, w[b], sum[m][b]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float sc = (float)vs[u][b].v[g];
+          const float mn = s.mins ? fmaf(-16.f, sc, (float)vm[u][b].v[g]) : -24.f * sc;
+#pragma unroll
+          for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[m][b][j] = fmaf(sc, sum[m][b][j], fmaf(mn, sx[m][j], acc[m][b][j]));
+        }
+      }
+    }
+  };
+  int k = wv * kTurn;
+  for (; k + (U - 1) * kWaves * kTurn + kTurn <= s.K; k += U * kWaves * kTurn) turns(k, std::true_type{});
+  if (k < s.K) turns(k, std::false_type{});
+
+  // sums of the four waves: [wave][tile of 16 x 16][lane]
+  f32x4* part = (f32x4*)lds;
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) part[(wv * MB * 2 + m * 2 + b) * 64 + lane] = acc[m][b];
+  __syncthreads();
+  for (int i = wv; i < (ACT ? MB : MB * 2); i += kWaves) {
+    const int m = ACT ? i : i >> 1;
+    f32x4 v[2];
+#pragma unroll
+    for (int b = 0; b < (ACT ? 2 : 1); ++b) {
+      const int at = ACT ? m * 2 + b : i;
+      v[b] = part[at * 64 + lane];
+#pragma unroll
+      for (int o = 1; o < kWaves; ++o) {
+        const f32x4 p = part[(o * MB * 2 + at) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[b][j] += p[j];
+      }
+    }
+    const int n = n0 + (ACT ? 0 : 16 * (i & 1)) + r;
+    if (n >= s.N) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 16 * m + 4 * q + j;
+      if (row >= t.n) continue;
+      float o = ACT ? gated(v[0][j], v[1][j]) : v[0][j];
+      if (s.rows && w4_row(s, t.row0 + row) < 0) o = __builtin_nanf("");
+      ((O*)s.y)[(int64_t)(t.row0 + row) * s.ldy + n] = from_f32<O>(o);
+    }
+  }
+}
+
+// ---------------------------------------------------------- one or two rows
+// A wave takes 8 rows of the weights (with the activation 4 of the gate and
+// the same 4 of the up half) and all their inputs: 32 inputs of one row per
+// lane and 16-byte load, `lanes` lanes per row (64 from 1024 inputs on), so
+// that 64 / lanes rows are read by one load; four loads' codes are in use
+// while the next four are in flight.  x lies in LDS, in the codes' order and
+// so that a read is contiguous over the lanes, with its sums per 32 inputs
+// (which lie in one group), and two products are added per v_dot2.  The
+// decode of 8 codes is 8 instructions however few rows there are, and here
+// nothing but one sum per row is exchanged between lanes.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c, f16) {
+  typedef __attribute__((ext_vector_type(2))) _Float16 h2;
+  return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
+}
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c, bf16) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 h2;
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, false));
+}
+// sum over runs of `lanes` lanes (8, 16, 32 or 64), in every lane
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  typedef __attribute__((ext_vector_type(2))) uint32_t u2;
+  v = dpp_add<0xB1>(v);   // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E>(v);   // quad_perm [2,3,0,1]
+  v = dpp_add<0x141>(v);  // row_half_mirror
+  if (lanes >= 16) v = dpp_add<0x140>(v);  // row_mirror
+  if (lanes >= 32) {
+    const uint32_t u = __float_as_uint(v);
+    const u2 t = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(u, u, false, false));
+    v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+  }
+  if (lanes >= 64) {
+    const uint32_t u = __float_as_uint(v);
+    const u2 t = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+    v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+  }
+  return v;
+}
+
+constexpr int kVecRows = 2;  // rows of x the vector path takes
+constexpr int kOuts = 8;     // rows of the weights per wave
+
+constexpr int kBatch = 4;    // loads whose rows are summed together
+constexpr int kVecInputs = 16384;  // rows x inputs of x that the LDS holds
+constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kVecRows * 4;
+
+template <class T, class O, bool ACT, int M>
+__device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* lds) {
+  typedef Magic<T> Mg;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int log_lanes = s.K <= 256 ? 3 : s.K <= 512 ? 4 : s.K <= 1024 ? 5 : 6;
+  const int lanes = 1 << log_lanes, sub = 64 >> log_lanes;  // lanes per row, rows per load
+  const int at = lane & (lanes - 1), which = lane >> log_lanes;
+  const int chunks = (s.K + 32 * lanes - 1) >> (5 + log_lanes);
+  constexpr int kN = ACT ? kOuts / 2 : kOuts;
+  const int n0 = blockIdx.x * (ACT ? kCols / 2 : kCols) + wv * kN;
+  const int groups = s.K / s.G;
+  uint4* xs = (uint4*)lds;                                   // [m][chunk][piece][lane]
+  float* sums = (float*)(lds + kVecInputs * 2);              // [m][chunk][lane]
+  float* mine = (float*)(lds + kVecInputs * 2 + kVecInputs / 32 * 4) + wv * kOuts * M;
+
+  // the wave's rows, clamped to the last one
+  const int64_t first = (int64_t)t.e * (ACT ? 2 : 1) * s.N + min(n0, s.N - 1);
+  const int most = max(s.N - 1 - n0, 0);
+  const uint8_t* codes = s.codes + first * (s.K / 2);
+  const int64_t group0 = first * groups;
+  struct Loads {
+    uint4 c[kBatch];
+    f16 s[kBatch], m[kBatch];
+  };
+  auto load = [&](int batch, int chunk, Loads& l) {
+    const int k = 32 * ((chunk << log_lanes) + at);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = (batch * kBatch + i) * sub + which;
+      l.c[i] = uint4{0, 0, 0, 0};
+      l.s[i] = l.m[i] = (f16)0.f;
+      if (j < kOuts && k < s.K) {
+        const int64_t row = min(ACT ? j & 3 : j, most) + (ACT && (j & 4) ? (int64_t)s.N : 0);
+        l.c[i] = *reinterpret_cast<const uint4*>(codes + row * (s.K / 2) + k / 2);
+        l.s[i] = s.scales[group0 + row * groups + k / s.G];
+        if (s.mins) l.m[i] = s.mins[group0 + row * groups + k / s.G];
+      }
+    }
+  };
+  Loads now, next;
+  load(0, 0, now);
+
+  // x into LDS, 0 past its end; 8 inputs a thread, a lane's 32 in 4 neighbours
+  const int pieces = chunks << (log_lanes + 2);
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const T* x = (const T*)s.x + (int64_t)max(w4_row(s, t.row0 + min(m, t.n - 1)), 0) * s.ldx;
+    for (int p = tid; p < pieces; p += 64 * kWaves) {
+      uint4 v = uint4{0, 0, 0, 0};
+      if (8 * p < s.K) v = *reinterpret_cast<const uint4*>(x + 8 * p);
+      const uint4 o = __builtin_bit_cast(uint4, order8<T>(v));
+      const int a = (p >> 2) & (lanes - 1), c = p >> (log_lanes + 2);
+      xs[(((m * chunks + c) * 4 + (p & 3)) << log_lanes) + a] = o;
+      float f = dot2(o.x, Mg::kOne, 0.f, T{});
+      f = dot2(o.y, Mg::kOne, f, T{});
+      f = dot2(o.z, Mg::kOne, f, T{});
+      f = dot2(o.w, Mg::kOne, f, T{});
+      f = dpp_add<0x4E>(dpp_add<0xB1>(f));  // the four neighbours' sum
+      if ((p & 3) == 0) sums[((m * chunks + c) << log_lanes) + a] = f;
+    }
+  }
+  __syncthreads();
+
+  const int batches = sub * kBatch >= kOuts ? 1 : kOuts / (sub * kBatch);
+  float acc[kBatch][M];
+  for (int batch = 0, chunk = 0; batch < batches;) {
+    const bool last = chunk + 1 == chunks;
+    const int nb = last ? batch + 1 : batch, nc = last ? 0 : chunk + 1;
+    if (nb < batches) load(nb, nc, next);
+    if (chunk == 0) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[i][m] = 0.f;
+    }
+    float d[kBatch][M] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 v[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] = xs[(((m * chunks + chunk) * 4 + j) << log_lanes) + at];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t w = j == 0 ? now.c[i].x : j == 1 ? now.c[i].y : j == 2 ? now.c[i].z : now.c[i].w;
+        const uint4 c = __builtin_bit_cast(uint4, codes8<T>(w));
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          d[i][m] = dot2(c.x, v[m].x, d[i][m], T{});
+          d[i][m] = dot2(c.y, v[m].y, d[i][m], T{});
+          d[i][m] = dot2(c.z, v[m].z, d[i][m], T{});
+          d[i][m] = dot2(c.w, v[m].w, d[i][m], T{});
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const float sx = sums[((m * chunks + chunk) << log_lanes) + at];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float sc = (float)now.s[i];
+        const float mn = s.mins ? fmaf(-16.f, sc, (float)now.m[i]) : -24.f * sc;
+        acc[i][m] = fmaf(sc, d[i][m], fmaf(mn, sx, acc[i][m]));
+      }
+    }
+    if (last) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = (batch * kBatch + i) * sub + which;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const float v = lanes_sum(acc[i][m], lanes);
+          if (at == 0 && j < kOuts) mine[j * M + m] = v;
+        }
+      }
+    }
+    now = next;
+    batch = nb, chunk = nc;
+  }
+  __syncthreads();
+  if (lane < kN * M) {
+    const int j = lane % kN, m = lane / kN;
+    if (m < t.n && n0 + j < s.N) {
+      float o = mine[j * M + m];
+      if (ACT) o = gated(o, mine[(j + kN) * M + m]);
+      if (s.rows && w4_row(s, t.row0 + m) < 0) o = __builtin_nanf("");
+      ((O*)s.y)[(int64_t)(t.row0 + m) * s.ldy + n0 + j] = from_f32<O>(o);
+    }
+  }
+}
+
+template <class T, class O, int G, bool ACT>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_w4_rows(W4Args s) {
+  __shared__ __align__(16) uint8_t lds[kVecLds];
+  static_assert(kVecLds >= kWaves * 4 * 64 * 16, "sums of the waves");
+  Tile t;
+  if (s.bounds) {
+    t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kRows);
+  } else {
+    t.e = 0, t.row0 = blockIdx.y * kRows, t.n = min(kRows, s.R - t.row0);
+  }
+  if (t.n <= 0) return;
+  // (a whole number of turns of 64 lanes x 32 inputs)
+  const bool vec = t.n <= kVecRows && t.n * ((s.K + 2047) & ~2047) <= kVecInputs;
+  if (vec && t.n == 1)
+    w4_vec<T, O, ACT, 1>(s, t, lds);
+  else if (vec)
+    w4_vec<T, O, ACT, 2>(s, t, lds);
+  else if (t.n <= 16)
+    w4_rows<T, O, G, ACT, 1>(s, t, (float*)lds);
+  else
+    w4_rows<T, O, G, ACT, 2>(s, t, (float*)lds);
+}
+
 }  // namespace
 }  // namespace experts
 }  // namespace bitsmoe
@@ -104,11 +530,32 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
     return fail(BITSMOE_EINVAL, "codes must be 16-byte aligned, scales and mins 4-byte aligned");
   W4Args s{x, ldx, rows, div, x_rows, (const uint8_t*)codes, (const f16*)scales, (const f16*)mins,
            bounds, R, E, N, K, G, y, ldy, act};
-  const dim3 grid((unsigned)((N + 3) / 4), (unsigned)R);
-  if (R > 65535) return fail(BITSMOE_ESHAPE, "R=%d", R);
+  const hipStream_t st = (hipStream_t)stream;
+  const bool wide = ((uintptr_t)x & 15u) == 0 && ldx % 8 == 0;
+  const long long tiles = !wide ? R : bounds ? max_tiles(R, E, kRows) : ((long long)R + kRows - 1) / kRows;
+  if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);
+  const int per = !wide ? 4 : act ? kCols / 2 : kCols;
+  const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)tiles);
   auto go = [&](auto t, auto o) {
-    hipLaunchKernelGGL((k_w4_any<decltype(t), decltype(o)>), grid, dim3(256), 0,
-                       (hipStream_t)stream, s);
+    using T = decltype(t);
+    using O = decltype(o);
+    if (!wide) {
+      hipLaunchKernelGGL((k_w4_any<T, O>), grid, dim3(256), 0, st, s);
+      return;
+    }
+    auto rows_of = [&](auto g) {
+      constexpr int kG = decltype(g)::value;
+      if (act)
+        hipLaunchKernelGGL((k_w4_rows<T, O, kG, true>), grid, dim3(64 * kWaves), 0, st, s);
+      else
+        hipLaunchKernelGGL((k_w4_rows<T, O, kG, false>), grid, dim3(64 * kWaves), 0, st, s);
+    };
+    if (G == 32)
+      rows_of(std::integral_constant<int, 32>{});
+    else if (G == 64)
+      rows_of(std::integral_constant<int, 64>{});
+    else
+      rows_of(std::integral_constant<int, 128>{});
   };
   if (dtype == BITSMOE_F16) {
     if (y_dtype == BITSMOE_F32)
