@@ -399,12 +399,15 @@ def ssd(W, r, max_sweeps=30, ws=None, stream=None):
 # stride; their rows are contiguous.  Without `stream` a call runs on the
 # current stream of its tensors' device.
 
+import torch  # noqa: E402  (after the library: see _load)
+
 ACT = {None: 0, "silu_mul": 1}
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _dtype(t):
-    import torch
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError("unsupported dtype %s" % t.dtype)
     return code
@@ -412,20 +415,20 @@ def _dtype(t):
 
 def _matrix(name, t, shape=None):
     """(pointer, row stride) of a 2-d tensor with contiguous rows."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    have = t.shape
+    if len(have) != 2 or (shape is not None and have != shape):
         raise ValueError("%s must be %s, got %s" % (name, "2-d" if shape is None else
-                                                    "of shape %s" % (shape,), tuple(t.shape)))
-    rows, cols = t.shape
+                                                    "of shape %s" % (shape,), tuple(have)))
     step, one = t.stride()
-    if cols > 1 and one != 1:
+    if one != 1 and have[1] > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
     # the stride of a single row says nothing
-    return t.data_ptr(), max(step, cols) if rows <= 1 else step
+    return t.data_ptr(), max(step, have[1]) if have[0] <= 1 else step
 
 
 def _array(name, t, dtype, shape):
     """Pointer of a contiguous tensor of that dtype and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s of shape %s, got %s of %s" % (name, dtype, shape, t.dtype,
                                                                       tuple(t.shape)))
     if not t.is_contiguous():
@@ -433,34 +436,36 @@ def _array(name, t, dtype, shape):
     return t.data_ptr()
 
 
-def _same_device(*ts):
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError("a tensor is on %s, not on a GPU" % t.device)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors on %s and %s" % (dev, t.device))
-    return dev
+def _same_device(first, *rest):
+    """The index of the tensors' one GPU."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("a tensor is on %s, not on a GPU" % first.device)
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors on %s and %s" % (first.device, t.device))
+    return index
 
 
-def _enqueue(fn, dev, stream, *args):
+def _enqueue(fn, index, stream, *args):
     """Calls fn(*args, stream) with the tensors' device as the current one."""
-    import torch
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _enqueue(fn, index, stream, *args)
+    if stream is None:
+        # (the handle alone: a Stream object would take most of a call's time)
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
-def _new(shape, dtype, dev, stream, zero=False):
+def _new(shape, dtype, index, stream, zero=False):
     """A tensor that belongs to the stream the call runs on."""
-    import torch
     make = torch.zeros if zero else torch.empty
+    dev = torch.device("cuda", index)
     if stream is None:
         return make(shape, dtype=dtype, device=dev)
     if isinstance(stream, int):
@@ -470,7 +475,6 @@ def _new(shape, dtype, dev, stream, zero=False):
 
 
 def _scratch(nbytes, dev, stream):
-    import torch
     return _new(nbytes, torch.uint8, dev, stream) if nbytes else None
 
 
@@ -481,24 +485,22 @@ def moe_group_workspace_size(P, E):
 
 
 def _group_buffers(T, k, E, bounds, order, slot, dev, stream):
-    import torch
-    i32 = torch.int32
+    i32 = _I32
     bounds = _new(E + 1, i32, dev, stream) if bounds is None else bounds
     order = _new(T * k, i32, dev, stream) if order is None else order
     slot = _new((T, k), i32, dev, stream) if slot is None else slot
-    _array("bounds", bounds, torch.int32, (E + 1,))
-    _array("order", order, torch.int32, (T * k,))
-    _array("slot", slot, torch.int32, (T, k))
+    _array("bounds", bounds, _I32, (E + 1,))
+    _array("order", order, _I32, (T * k,))
+    _array("slot", slot, _I32, (T, k))
     return bounds, order, slot
 
 
 def moe_group(ids, E, bounds=None, order=None, slot=None, ws=None, stream=None):
     """(bounds, order, slot) of the pairs of ids (T x k int32) by expert, in
     rising pair order; pairs with an id outside [0, E) come last, with -1."""
-    import torch
     T, k = ids.shape
     dev = _same_device(ids, bounds, order, slot, ws)
-    pi = _array("ids", ids, torch.int32, (T, k))
+    pi = _array("ids", ids, _I32, (T, k))
     bounds, order, slot = _group_buffers(T, k, E, bounds, order, slot, dev, stream)
     if ws is None:
         ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
@@ -513,22 +515,21 @@ def moe_route(logits, k, ids=None, g=None, renorm=False, scale=1.0, bounds=None,
     each token: softmax weights over all experts, or over the chosen ones
     (renorm), times scale.  With bounds, order and slot the pairs are grouped
     by expert as well, as by moe_group."""
-    import torch
     T, E = logits.shape
     dev = _same_device(logits, ids, g, bounds, order, slot, ws)
     pl, ld = _matrix("logits", logits)
     if ids is None:
-        ids = _new((T, k), torch.int32, dev, stream)
+        ids = _new((T, k), _I32, dev, stream)
     if g is None:
-        g = _new((T, k), torch.float32, dev, stream)
-    pi, pg = _array("ids", ids, torch.int32, (T, k)), _array("g", g, torch.float32, (T, k))
+        g = _new((T, k), _F32, dev, stream)
+    pi, pg = _array("ids", ids, _I32, (T, k)), _array("g", g, _F32, (T, k))
     pb = po = ps = None
     if bounds is not None or order is not None or slot is not None:
         if bounds is None or order is None or slot is None:
             raise ValueError("bounds, order and slot go together")
-        pb = _array("bounds", bounds, torch.int32, (E + 1,))
-        po = _array("order", order, torch.int32, (T * k,))
-        ps = _array("slot", slot, torch.int32, (T, k))
+        pb = _array("bounds", bounds, _I32, (E + 1,))
+        po = _array("order", order, _I32, (T * k,))
+        ps = _array("slot", slot, _I32, (T, k))
         if ws is None and T * k:
             ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
     _enqueue(_lib.bitsmoe_moe_route, dev, stream, _dtype(logits), pl, ld, T, E, k, int(renorm),
@@ -539,7 +540,6 @@ def moe_route(logits, k, ids=None, g=None, renorm=False, scale=1.0, bounds=None,
 def moe_route_grad(logits, ids, dg, dlogits=None, renorm=False, scale=1.0, stream=None):
     """dlogits (T x E, the logits' dtype) from dg (T x k float32) and the ids
     that moe_route gave for these logits."""
-    import torch
     T, E = logits.shape
     k = ids.shape[1]
     dev = _same_device(logits, ids, dg, dlogits)
@@ -550,23 +550,21 @@ def moe_route_grad(logits, ids, dg, dlogits=None, renorm=False, scale=1.0, strea
         raise ValueError("dlogits must have the logits' dtype")
     pd, ldd = _matrix("dlogits", dlogits, (T, E))
     _enqueue(_lib.bitsmoe_moe_route_grad, dev, stream, _dtype(logits), pl, ld,
-             _array("ids", ids, torch.int32, (T, k)), _array("dg", dg, torch.float32, (T, k)), T,
+             _array("ids", ids, _I32, (T, k)), _array("dg", dg, _F32, (T, k)), T,
              E, k, int(renorm), scale, pd, ldd)
     return dlogits
 
 
 def _gather(x, rows, div, R):
-    import torch
     if rows is None:
         if x.shape[0] < R:
             raise ValueError("x has %d rows, the sorted layout %d" % (x.shape[0], R))
         return None, 1
-    return _array("rows", rows, torch.int32, (R,)), div
+    return _array("rows", rows, _I32, (R,)), div
 
 
 def _bounds(bounds, E):
-    import torch
-    return _array("bounds", bounds, torch.int32, (E + 1,))
+    return _array("bounds", bounds, _I32, (E + 1,))
 
 
 def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None):
@@ -574,7 +572,6 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None
     w: E x N x K; with act="silu_mul" E x 2N x K (gate rows first) and y =
     SiLU(gate) * up.  rows (R int32): row i reads x[rows[i] // div].  y has
     x's dtype, or float32 where it is given so."""
-    import torch
     E, n2, K = w.shape
     N = n2 // 2 if act else n2
     if act not in ACT or (act and n2 % 2):
@@ -595,7 +592,6 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None
 def grouped_matmul_dx(dy, w, bounds, dx=None, stream=None):
     """dx (R x K) with dx[i] = W_e^T dy[i]: the gradient of grouped_matmul's
     sorted rows (of a gathered x, moe_combine adds up a token's rows)."""
-    import torch
     E, N, K = w.shape
     R = dy.shape[0]
     dev = _same_device(dy, w, bounds, dx)
@@ -612,7 +608,6 @@ def grouped_matmul_dx(dy, w, bounds, dx=None, stream=None):
 def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
     """dw (E x N x K) with dw_e = sum of dy[i] x[i]^T over the sorted rows of
     expert e; 0 for an expert without rows.  float32 unless dw is given."""
-    import torch
     R, N = dy.shape
     K = x.shape[1]
     E = bounds.shape[0] - 1
@@ -623,7 +618,7 @@ def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
         raise ValueError("x and dy must have one dtype")
     pr, div = _gather(x, rows, div, R)
     if dw is None:
-        dw = _new((E, N, K), torch.float32, dev, stream)
+        dw = _new((E, N, K), _F32, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul_dw, dev, stream, _dtype(dy), pd, ldd, px, ldx, x.shape[0],
              pr, div, _bounds(bounds, E), R, E, N, K, _array("dw", dw, dw.dtype, (E, N, K)),
              _dtype(dw))
@@ -633,7 +628,6 @@ def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
 def silu_mul(a, h=None, bounds=None, stream=None):
     """h (R x F) = SiLU(gate) * up of rows a = [gate | up] (R x 2F); with
     bounds only the experts' rows."""
-    import torch
     R, F2 = a.shape
     dev = _same_device(a, h, bounds)
     pa, lda = _matrix("a", a)
@@ -652,7 +646,6 @@ def silu_mul(a, h=None, bounds=None, stream=None):
 
 def silu_mul_grad(a, dh, da=None, bounds=None, stream=None):
     """da (R x 2F) from a and dh (R x F); da may be a itself."""
-    import torch
     R, F2 = a.shape
     dev = _same_device(a, dh, da, bounds)
     pa, lda = _matrix("a", a)
@@ -673,7 +666,6 @@ def silu_mul_grad(a, dh, da=None, bounds=None, stream=None):
 def moe_combine(y, slot, g=None, out=None, stream=None):
     """out (T x D) = sum over j of g[t, j] * y[slot[t, j]], in slot order; a
     slot of -1 has no row.  out has y's dtype, or float32 where given so."""
-    import torch
     T, k = slot.shape
     R, D = y.shape
     dev = _same_device(y, slot, g, out)
@@ -682,8 +674,8 @@ def moe_combine(y, slot, g=None, out=None, stream=None):
         out = _new((T, D), y.dtype, dev, stream)
     po, ldo = _matrix("out", out, (T, D))
     _enqueue(_lib.bitsmoe_moe_combine, dev, stream, _dtype(y), py, ldy, R,
-             _array("slot", slot, torch.int32, (T, k)),
-             None if g is None else _array("g", g, torch.float32, (T, k)), T, k, D, po, _dtype(out),
+             _array("slot", slot, _I32, (T, k)),
+             None if g is None else _array("g", g, _F32, (T, k)), T, k, D, po, _dtype(out),
              ldo)
     return out
 
@@ -691,7 +683,6 @@ def moe_combine(y, slot, g=None, out=None, stream=None):
 def moe_combine_grad(dout, y, slot, g=None, dy=None, dg=None, stream=None):
     """(dy, dg) of moe_combine: dy[slot[t, j]] = g[t, j] * dout[t] (other rows
     as they were), dg[t, j] = <dout[t], y[slot[t, j]]>; the slots differ."""
-    import torch
     T, k = slot.shape
     R, D = y.shape
     dev = _same_device(dout, y, slot, g, dy, dg)
@@ -700,14 +691,14 @@ def moe_combine_grad(dout, y, slot, g=None, dy=None, dg=None, stream=None):
     if dy is None:
         dy = _new((R, D), y.dtype, dev, stream, zero=True)
     if dg is None:
-        dg = _new((T, k), torch.float32, dev, stream)
+        dg = _new((T, k), _F32, dev, stream)
     if dy.dtype != y.dtype:
         raise ValueError("dy must have y's dtype")
     pdy, lddy = _matrix("dy", dy, (R, D))
     _enqueue(_lib.bitsmoe_moe_combine_grad, dev, stream, pd, _dtype(dout), ldd, _dtype(y), py, ldy,
-             R, _array("slot", slot, torch.int32, (T, k)),
-             None if g is None else _array("g", g, torch.float32, (T, k)), T, k, D, pdy, lddy,
-             _array("dg", dg, torch.float32, (T, k)))
+             R, _array("slot", slot, _I32, (T, k)),
+             None if g is None else _array("g", g, _F32, (T, k)), T, k, D, pdy, lddy,
+             _array("dg", dg, _F32, (T, k)))
     return dy, dg
 
 
@@ -734,7 +725,6 @@ def w4_matmul(x, codes, scales, mins=None, y=None, bounds=None, rows=None, div=1
     of K / scales.shape[-1] inputs (mins None: -8 * scales).  codes: E x N x
     K/2 uint8 (or N x K/2 for one dense projection); bounds, rows, div and act
     as for grouped_matmul (bounds may be None when E is 1)."""
-    import torch
     if codes.dim() == 2:
         codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
         mins = None if mins is None else mins.unsqueeze(0)
