@@ -16,7 +16,7 @@ namespace experts {
 namespace {
 
 constexpr int kMaxSlots = 64;
-constexpr int kMaxExperts = 2048;  // counters of 4 waves in 64 KB of LDS
+constexpr int kMaxExperts = 2048;
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;  // order_key(-inf); 0 is below it
 
 // Unsigned key in the order of the floats (-0 made +0, so the two tie).
@@ -65,11 +65,10 @@ __device__ inline float reduce_sum(float v) {
 // load of all lanes is contiguous.  A choice is the largest key of the lanes'
 // own largest ones, then the lowest expert that has it.
 template <class T, int L, int V>
-__global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int64_t ld, int T_,
-                                               int E, int k, int renorm, float scale,
-                                               int32_t* __restrict__ ids, float* __restrict__ g) {
+__device__ __forceinline__ int32_t route_token(const T* __restrict__ logits, int64_t ld, int64_t t0,
+                                            int T_, int E, int k, int renorm, float scale,
+                                            int32_t* __restrict__ ids, float* __restrict__ g) {
   const int l = threadIdx.x & (L - 1);
-  const int64_t t0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
   const bool live = t0 < T_;
   const int64_t t = live ? t0 : T_ - 1;  // (whole waves stay in the reductions)
   uint32_t key[V];
@@ -119,6 +118,15 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
     ids[t * k + l] = bad ? -1 : my_id;
     g[t * k + l] = bad ? __builtin_nanf("") : my_id >= 0 ? scale * (my_e / total) : 0.f;
   }
+  return bad ? -1 : my_id;  // the l-th choice
+}
+
+template <class T, int L, int V>
+__global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int64_t ld, int T_,
+                                               int E, int k, int renorm, float scale,
+                                               int32_t* __restrict__ ids, float* __restrict__ g) {
+  route_token<T, L, V>(logits, ld, ((int64_t)blockIdx.x * 256 + threadIdx.x) / L, T_, E, k, renorm,
+                       scale, ids, g);
 }
 
 // With w = softmax over all experts and q_i = scale dg_j at i = id_j (0
@@ -199,12 +207,18 @@ __device__ inline uint64_t same_id(int id, int bits) {
   return m;
 }
 
+constexpr int kIdBatch = 8;  // turns of 64 ids loaded before the first is used
+
 // counts of one wave's run [p0, p1) into cnt[E + 1] (LDS, zeroed)
 __device__ inline void count_run(const int32_t* __restrict__ ids, int p0, int p1, int E,
                                  uint32_t* cnt) {
-  for (int p = p0 + (int)(threadIdx.x & 63); p < p1; p += 64) {
-    const int id = ids[p];
-    atomicAdd(&cnt[id >= 0 && id < E ? id : E], 1u);
+  for (int b = p0 + (int)(threadIdx.x & 63); b < p1; b += 64 * kIdBatch) {
+    int id[kIdBatch];
+#pragma unroll
+    for (int u = 0; u < kIdBatch; ++u) id[u] = b + 64 * u < p1 ? ids[b + 64 * u] : 0;
+#pragma unroll
+    for (int u = 0; u < kIdBatch; ++u)
+      if (b + 64 * u < p1) atomicAdd(&cnt[id[u] >= 0 && id[u] < E ? id[u] : E], 1u);
   }
 }
 
@@ -213,25 +227,27 @@ __device__ inline void place_run(const int32_t* __restrict__ ids, int p0, int p1
                                  uint32_t* cur, int32_t* __restrict__ order,
                                  int32_t* __restrict__ slot) {
   const int lane = threadIdx.x & 63;
-  for (int b = p0; b < p1; b += 64) {
-    const int p = b + lane;
-    int id = -1;
-    if (p < p1) {
-      id = ids[p];
-      id = id >= 0 && id < E ? id : E;
+  for (int b = p0; b < p1; b += 64 * kIdBatch) {
+    int ids_[kIdBatch];
+#pragma unroll
+    for (int u = 0; u < kIdBatch; ++u) ids_[u] = b + 64 * u + lane < p1 ? ids[b + 64 * u + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < kIdBatch; ++u) {
+      const int p = b + 64 * u + lane;
+      const int id = ids_[u] >= 0 && ids_[u] < E ? ids_[u] : E;
+      const bool live = p < p1;
+      const uint64_t m = same_id(id, bits) & __ballot(live);
+      if (live) {
+        const uint32_t rank = (uint32_t)__popcll(m & ((1ull << lane) - 1));
+        const uint32_t base = cur[id];
+        order[base + rank] = id < E ? p : -1;
+        slot[p] = id < E ? (int32_t)(base + rank) : -1;
+        if (rank + 1 == (uint32_t)__popcll(m)) cur[id] = base + rank + 1;
+      }
+      // (LDS operations of one wave complete in order: the reads of `cur`
+      // above are done before the next 64 pairs' reads)
+      __builtin_amdgcn_wave_barrier();
     }
-    // lanes past the end have all bits set; p < p1 tells them from an id
-    uint64_t m = same_id(id, bits) & __ballot(p < p1);
-    if (p < p1) {
-      const uint32_t rank = (uint32_t)__popcll(m & ((1ull << lane) - 1));
-      const uint32_t base = cur[id];
-      order[base + rank] = id < E ? p : -1;
-      slot[p] = id < E ? (int32_t)(base + rank) : -1;
-      if (rank + 1 == (uint32_t)__popcll(m)) cur[id] = base + rank + 1;
-    }
-    // (LDS operations of one wave complete in order: the reads of `cur`
-    // above are done before the next 64 pairs' reads)
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -255,11 +271,10 @@ __device__ inline uint32_t block_scan(uint32_t v, uint32_t* buf, int nw) {
 // All pairs in one work-group of 16 waves: dynamic LDS 16 (E + 1) words of
 // counters, then 16 of scan totals.
 constexpr int kOneWaves = 16;
-__global__ __launch_bounds__(64 * kOneWaves) void k_group_one(const int32_t* __restrict__ ids,
-                                                              int P, int E, int bits,
-                                                              int32_t* __restrict__ bounds,
-                                                              int32_t* __restrict__ order,
-                                                              int32_t* __restrict__ slot) {
+__device__ __forceinline__ void group_one(const int32_t* __restrict__ ids, int P, int E, int bits,
+                                          int32_t* __restrict__ bounds,
+                                          int32_t* __restrict__ order,
+                                          int32_t* __restrict__ slot) {
   extern __shared__ uint32_t lds[];
   uint32_t* buf = lds + kOneWaves * (E + 1);
   const int tid = threadIdx.x, wv = tid >> 6, n = 64 * kOneWaves;
@@ -295,59 +310,125 @@ __global__ __launch_bounds__(64 * kOneWaves) void k_group_one(const int32_t* __r
   place_run(ids, p0, p1, E, bits, mine, order, slot);
 }
 
-// Many pairs: every wave of the grid counts its run into ws[unit][E + 1] ...
-constexpr int kGridWaves = 4;
-__global__ __launch_bounds__(64 * kGridWaves) void k_group_count(const int32_t* __restrict__ ids,
-                                                                 int P, int E, int per,
-                                                                 uint32_t* __restrict__ ws) {
+__global__ __launch_bounds__(64 * kOneWaves) void k_group_one(const int32_t* __restrict__ ids,
+                                                              int P, int E, int bits,
+                                                              int32_t* __restrict__ bounds,
+                                                              int32_t* __restrict__ order,
+                                                              int32_t* __restrict__ slot) {
+  group_one(ids, P, E, bits, bounds, order, slot);
+}
+
+// Up to 4 tokens and 64 pairs: one wave, nothing but registers.  Lane p holds
+// pair p's id; a place is the number of pairs with a lower id, or the same
+// and a lower index.
+template <class T, int V>
+__global__ __launch_bounds__(64) void k_route_group_wave(
+    const T* __restrict__ logits, int64_t ld, int T_, int E, int k, int renorm, float scale,
+    int32_t* __restrict__ ids, float* __restrict__ g, int32_t* __restrict__ bounds,
+    int32_t* __restrict__ order, int32_t* __restrict__ slot) {
+  const int lane = threadIdx.x, P = T_ * k;
+  int id = route_token<T, 16, V>(logits, ld, lane / 16, T_, E, k, renorm, scale, ids, g);
+  id = __shfl(id, min(lane / k * 16 + lane % k, 63), 64);
+  id = id >= 0 ? id : E;
+  int at = 0;
+  for (int p = 0; p < P; ++p) {
+    const int o = __builtin_amdgcn_readlane(id, p);
+    at += o < id || (o == id && p < lane);
+  }
+  if (lane < P) {
+    order[at] = id < E ? lane : -1;
+    slot[lane] = id < E ? at : -1;
+  }
+  for (int e0 = 0; e0 <= E; e0 += 64) {
+    int n = 0;
+    for (int p = 0; p < P; ++p) n += __builtin_amdgcn_readlane(id, p) < e0 + lane;
+    if (e0 + lane <= E) bounds[e0 + lane] = n;
+  }
+}
+
+// Few tokens (at most kOneTokens): routing and grouping in one work-group, 64
+// tokens at a time, which saves a launch.
+constexpr int kOneTokens = 128;
+template <class T, int V>
+__global__ __launch_bounds__(64 * kOneWaves) void k_route_group_one(
+    const T* __restrict__ logits, int64_t ld, int T_, int E, int k, int renorm, float scale,
+    int32_t* ids, float* __restrict__ g, int bits, int32_t* __restrict__ bounds,
+    int32_t* __restrict__ order, int32_t* __restrict__ slot) {
+  for (int t0 = 0; t0 < T_; t0 += 64 * kOneWaves / 16)
+    route_token<T, 16, V>(logits, ld, t0 + (int)threadIdx.x / 16, T_, E, k, renorm, scale, ids, g);
+  __threadfence_block();  // (group_one starts with a barrier)
+  group_one(ids, T_ * k, E, bits, bounds, order, slot);
+}
+
+// Many pairs: every wave of the grid counts its run into runs[unit][E + 1],
+// the work-group's sums go to blocks[block][E + 1] ...
+__global__ __launch_bounds__(512) void k_group_count(const int32_t* __restrict__ ids, int P, int E,
+                                                     int per, uint32_t* __restrict__ runs,
+                                                     uint32_t* __restrict__ blocks) {
   extern __shared__ uint32_t lds[];
-  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int unit = blockIdx.x * kGridWaves + wv;
+  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+  const int unit = blockIdx.x * nw + wv;
   uint32_t* mine = lds + wv * (E + 1);
   for (int i = lane; i <= E; i += 64) mine[i] = 0;
   __syncthreads();
   const int p0 = (int)min((int64_t)P, (int64_t)unit * per), p1 = (int)min((int64_t)P, (int64_t)p0 + per);
   count_run(ids, p0, p1, E, mine);
   __syncthreads();
-  for (int i = lane; i <= E; i += 64) ws[(size_t)unit * (E + 1) + i] = mine[i];
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+    uint32_t sum = 0;
+    for (int w = 0; w < nw; ++w) {
+      const uint32_t c = lds[w * (E + 1) + e];
+      runs[(size_t)(blockIdx.x * nw + w) * (E + 1) + e] = c;
+      sum += c;
+    }
+    blocks[(size_t)blockIdx.x * (E + 1) + e] = sum;
+  }
 }
 
-// ... and places it after the pairs of lower experts and of earlier units,
-// whose counts every work-group adds up for itself.
-__global__ __launch_bounds__(64 * kGridWaves) void k_group_place(
-    const int32_t* __restrict__ ids, int P, int E, int bits, int per, int units,
-    const uint32_t* __restrict__ ws, int32_t* __restrict__ bounds, int32_t* __restrict__ order,
-    int32_t* __restrict__ slot) {
+// ... and places it after the pairs of lower experts, of earlier work-groups,
+// whose sums every work-group adds up for itself, 16 in flight, and of the
+// earlier waves of its own.
+__global__ __launch_bounds__(512) void k_group_place(
+    const int32_t* __restrict__ ids, int P, int E, int bits, int per,
+    const uint32_t* __restrict__ runs, const uint32_t* __restrict__ blocks,
+    int32_t* __restrict__ bounds, int32_t* __restrict__ order, int32_t* __restrict__ slot) {
   extern __shared__ uint32_t lds[];
-  uint32_t* buf = lds + kGridWaves * (E + 1);
-  const int tid = threadIdx.x, wv = tid >> 6, n = 64 * kGridWaves;
-  const int u0 = blockIdx.x * kGridWaves;
+  const int tid = threadIdx.x, wv = tid >> 6, n = blockDim.x, nw = n >> 6;
+  const int nb = gridDim.x, b0 = blockIdx.x;
+  uint32_t* buf = lds + nw * (E + 1);
   uint32_t before = 0;
   for (int e0 = 0; e0 <= E; e0 += n) {
     const int e = e0 + tid;
-    uint32_t sum = 0, earlier = 0;
+    uint32_t sum = 0, earlier = 0, c[16], own[8];
     if (e <= E) {
-      for (int u = 0; u < units; ++u) {
-        const uint32_t c = ws[(size_t)u * (E + 1) + e];
-        if (u == u0) earlier = sum;
-        sum += c;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) own[w] = w < nw ? runs[(size_t)(b0 * nw + w) * (E + 1) + e] : 0;
+      for (int u = 0; u < nb; u += 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[i] = u + i < nb ? blocks[(size_t)(u + i) * (E + 1) + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          earlier += u + i < b0 ? c[i] : 0;
+          sum += c[i];
+        }
       }
     }
-    const uint32_t ex = before + block_scan(sum, buf, kGridWaves);
+    const uint32_t ex = before + block_scan(sum, buf, nw);
     if (e <= E) {
-      if (blockIdx.x == 0) bounds[e] = (int32_t)ex;
+      if (b0 == 0) bounds[e] = (int32_t)ex;
       uint32_t at = ex + earlier;
-      for (int w = 0; w < kGridWaves; ++w) {
-        lds[w * (E + 1) + e] = at;
-        if (u0 + w < units) at += ws[(size_t)(u0 + w) * (E + 1) + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w < nw) lds[w * (E + 1) + e] = at;
+        at += own[w];
       }
     }
-    if (tid == n - 1) buf[kGridWaves] = ex + sum;
+    if (tid == n - 1) buf[nw] = ex + sum;
     __syncthreads();
-    before = buf[kGridWaves];
+    before = buf[nw];
     __syncthreads();
   }
-  const int unit = u0 + wv;
+  const int unit = b0 * nw + wv;
   const int p0 = (int)min((int64_t)P, (int64_t)unit * per), p1 = (int)min((int64_t)P, (int64_t)p0 + per);
   place_run(ids, p0, p1, E, bits, lds + wv * (E + 1), order, slot);
 }
@@ -362,17 +443,19 @@ int id_bits(int E) {
 // the LDS up to 512 experts (33 KB).
 bool group_in_one(int P, int E) { return P <= 4096 && E <= 512; }
 
-// Pairs a wave of the grid: whole groups of 64, at most 256 waves (so that
-// the per-unit counts stay in L2), at least 256 pairs.
-int group_per(int P) {
-  long long per = ((long long)P + 255) / 256;
+// Waves per work-group of the grid: their counters take at most 33 KB.
+int grid_waves(int E) { return E <= 1024 ? 8 : 4; }
+// Pairs a wave of the grid: whole groups of 64, at least 256, and at most
+// about 64 work-groups, whose sums every work-group reads.
+int group_per(int P, int E) {
+  const long long most = 64 * grid_waves(E);
+  long long per = (P + most - 1) / most;
   per = (per + 63) / 64 * 64;
   return (int)(per < 256 ? 256 : per);
 }
-int group_units(int P) {
-  const long long per = group_per(P);
-  const long long u = ((long long)P + per - 1) / per;
-  return (int)((u + kGridWaves - 1) / kGridWaves * kGridWaves);
+int group_blocks(int P, int E) {
+  const long long run = (long long)group_per(P, E) * grid_waves(E);
+  return (int)((P + run - 1) / run);
 }
 
 int group_check(int P, int E) {
@@ -382,7 +465,7 @@ int group_check(int P, int E) {
 }
 
 size_t group_ws(int P, int E) {
-  return group_in_one(P, E) ? 0 : (size_t)group_units(P) * (E + 1) * 4;
+  return group_in_one(P, E) ? 0 : (size_t)group_blocks(P, E) * (grid_waves(E) + 1) * (E + 1) * 4;
 }
 
 int run_group(const int32_t* ids, int P, int E, int32_t* bounds, int32_t* order, int32_t* slot,
@@ -394,14 +477,15 @@ int run_group(const int32_t* ids, int P, int E, int32_t* bounds, int32_t* order,
                        order, slot);
     return launched("moe_group");
   }
-  const int per = group_per(P), units = group_units(P);
-  const size_t lds = ((size_t)kGridWaves * (E + 1) + kGridWaves + 1) * 4;
-  hipLaunchKernelGGL(k_group_count, dim3(units / kGridWaves), dim3(64 * kGridWaves), lds, st, ids,
-                     P, E, per, (uint32_t*)ws);
+  const int per = group_per(P, E), nb = group_blocks(P, E), nw = grid_waves(E);
+  const size_t lds = ((size_t)nw * (E + 1) + nw + 1) * 4;
+  uint32_t* runs = (uint32_t*)ws;
+  uint32_t* blocks = runs + (size_t)nb * nw * (E + 1);
+  hipLaunchKernelGGL(k_group_count, dim3(nb), dim3(64 * nw), lds, st, ids, P, E, per, runs, blocks);
   int rc = launched("moe_group count");
   if (rc) return rc;
-  hipLaunchKernelGGL(k_group_place, dim3(units / kGridWaves), dim3(64 * kGridWaves), lds, st, ids,
-                     P, E, bits, per, units, (const uint32_t*)ws, bounds, order, slot);
+  hipLaunchKernelGGL(k_group_place, dim3(nb), dim3(64 * nw), lds, st, ids, P, E, bits, per,
+                     (const uint32_t*)runs, (const uint32_t*)blocks, bounds, order, slot);
   return launched("moe_group place");
 }
 
@@ -481,11 +565,28 @@ int bitsmoe_moe_route(int dtype, const void* logits, int64_t ld, int T, int E, i
       return fail(BITSMOE_ENOSPC, "ws_bytes=%zu < %zu", ws_bytes, group_ws(T * k, E));
     if ((uintptr_t)ws & 3u) return fail(BITSMOE_EINVAL, "misaligned workspace");
   }
+  // few tokens: one launch for both
+  const bool one = grouped && T && T <= kOneTokens && E <= 256 && k <= 16 && group_in_one(T * k, E);
   if (T) {
     auto go = [&](auto tag) {
       using X = decltype(tag);
       with_shape(E, k, [&](auto l, auto v) {
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
+        if constexpr (L == 16) {
+          if (one && T <= 4 && T * k <= 64) {
+            hipLaunchKernelGGL((k_route_group_wave<X, V>), dim3(1), dim3(64), 0,
+                               (hipStream_t)stream, (const X*)logits, ld, T, E, k, renorm, scale,
+                               ids, g, bounds, order, slot);
+            return;
+          }
+          if (one) {
+            const size_t lds = ((size_t)kOneWaves * (E + 1) + kOneWaves + 1) * 4;
+            hipLaunchKernelGGL((k_route_group_one<X, V>), dim3(1), dim3(64 * kOneWaves), lds,
+                               (hipStream_t)stream, (const X*)logits, ld, T, E, k, renorm, scale,
+                               ids, g, id_bits(E), bounds, order, slot);
+            return;
+          }
+        }
         hipLaunchKernelGGL((k_route<X, L, V>), dim3((unsigned)(((int64_t)T * L + 255) / 256)),
                            dim3(256), 0, (hipStream_t)stream, (const X*)logits, ld, T, E, k,
                            renorm, scale, ids, g);
@@ -499,7 +600,7 @@ int bitsmoe_moe_route(int dtype, const void* logits, int64_t ld, int T, int E, i
       go(bf16{});
     if ((st = launched("moe_route"))) return st;
   }
-  if (grouped) return run_group(ids, T * k, E, bounds, order, slot, ws, (hipStream_t)stream);
+  if (grouped && !one) return run_group(ids, T * k, E, bounds, order, slot, ws, (hipStream_t)stream);
   return BITSMOE_OK;
 }
 
