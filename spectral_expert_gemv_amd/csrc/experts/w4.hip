@@ -25,6 +25,7 @@ struct W4Args {
   void* y;
   int64_t ldy;
   int act;
+  int turns;  // blocks of kCols weight rows of a work-group: 1 or kWaves
 };
 
 __device__ inline int w4_row(const W4Args& s, int i) {
@@ -74,11 +75,13 @@ __global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
   }
 }
 
-// ------------------------------------------------------------ 16-byte rows
-// A work-group takes up to 32 rows of one expert and 32 rows of its weights
-// (with the activation 16 of the gate and the same 16 of the up half); its
-// four waves split the inputs in turns of 128 and add up through LDS.  Every
-// code is read once per work-group, 16 bytes (32 inputs of one row) a lane.
+// ------------------------------------------------------- three rows and more
+// A work-group takes up to 32 rows of one expert and a block of 32 rows of its
+// weights (with the activation 16 of the gate and the same 16 of the up
+// half), whose inputs its four waves split in turns of 128, adding up through
+// LDS; or, when there is enough work, a block for each of its waves.  Every
+// code is read once per tile of rows, 16 bytes (32 inputs of one row) a lane,
+// a stage of turns ahead of its use.
 //
 // In a turn lane (r, q) loads the codes of row r, inputs 32 q .. 32 q + 31.
 // One matrix-core step takes 32 inputs, 8 a lane, that have to lie in one
@@ -150,32 +153,28 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
 // 2-byte aligned
 template <int N>
 struct Halves {
-  f16 v[N];
+  typedef _Float16 type __attribute__((ext_vector_type(N)));
+  typedef type loose __attribute__((aligned(2)));
 };
 template <int N>
-__device__ __forceinline__ Halves<N> load_halves(const f16* p) {
-  Halves<N> h;
-  __builtin_memcpy(&h, p, sizeof(h));
-  return h;
+__device__ __forceinline__ typename Halves<N>::type load_halves(const f16* p) {
+  return *reinterpret_cast<const typename Halves<N>::loose*>(p);
 }
 
-template <class T, class O, int G, bool ACT, int MB>
+// U: turns of a stage; the loads of one are in flight during the products of
+// the one before
+template <class T, class O, int G, bool ACT, int MB, int U>
 __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* lds) {
-  constexpr int U = MB == 1 ? 2 : 1;  // turns whose loads are in flight together
-  constexpr int NG = kTurn / G;                      // groups of a turn
+  constexpr int NG = kTurn / G;  // groups of a turn
+  constexpr int kPer = ACT ? kCols / 2 : kCols;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * (ACT ? kCols / 2 : kCols);
   const int groups = s.K / G;
-  const uint8_t* codes[2];
-  int64_t group0[2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int64_t row = (int64_t)t.e * (ACT ? 2 : 1) * s.N +
-                        (ACT ? (int64_t)b * s.N + min(n0 + r, s.N - 1) : min(n0 + 16 * b + r, s.N - 1));
-    codes[b] = s.codes + row * (s.K / 2) + 16 * q;
-    group0[b] = row * groups;
-  }
+  // One block of columns for the work-group, whose waves split the inputs, or
+  // one for each of its waves.
+  const int parts = s.turns == 1 ? kWaves : 1, part = s.turns == 1 ? wv : 0;
+  const int n0 = (s.turns == 1 ? blockIdx.x : blockIdx.x * kWaves + wv) * kPer;
+  const int stages = (s.K + kTurn * parts * U - 1) / (kTurn * parts * U);
   const T* x[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
@@ -183,46 +182,61 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
   const uint4 ones = {Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne};
   const typename Vec8<T>::type one8 = __builtin_bit_cast(typename Vec8<T>::type, ones);
 
-  f32x4 acc[MB][2] = {};
-  auto turns = [&](int k0, auto whole_) {  // inputs k0 .., U turns kWaves * kTurn apart
-    constexpr bool whole = decltype(whole_)::value;
-    uint4 vc[U][2], vx[U][MB][4];
-    Halves<NG> vs[U][2], vm[U][2];
+  struct Stage {
+    uint4 c[U][2], x[U][MB][4];
+    typename Halves<NG>::type s[U][2], m[U][2];
+  };
+  const uint8_t* codes[2];
+  const f16 *scales[2], *mins[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int64_t row =
+        (int64_t)t.e * (ACT ? 2 : 1) * s.N +
+        (ACT ? (int64_t)b * s.N + min(n0 + r, s.N - 1) : min(n0 + 16 * b + r, s.N - 1));
+    codes[b] = s.codes + row * (s.K / 2);
+    scales[b] = s.scales + row * groups;
+    mins[b] = s.mins + row * groups;
+  }
+  // Turn u of stage st starts at input ((st U + u) parts + part) kTurn.  Past
+  // the end x is 0, and codes and groups are the row's last ones.
+  auto load = [&](int st, Stage& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kWaves * kTurn;
+      const int k = ((st * U + u) * parts + part) * kTurn;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        vc[u][b] = uint4{0, 0, 0, 0};
-        if (whole || k + 32 * q < s.K) vc[u][b] = *reinterpret_cast<const uint4*>(codes[b] + k / 2);
-        // past the end the row's last groups: x is 0 there
-        if (whole) {
-          vs[u][b] = load_halves<NG>(s.scales + group0[b] + k / G);
-          if (s.mins) vm[u][b] = load_halves<NG>(s.mins + group0[b] + k / G);
+        v.c[u][b] = *reinterpret_cast<const uint4*>(codes[b] + min(k + 32 * q, s.K - 32) / 2);
+        if (k + kTurn <= s.K) {
+          v.s[u][b] = load_halves<NG>(scales[b] + k / G);
+          if (s.mins) v.m[u][b] = load_halves<NG>(mins[b] + k / G);
         } else {
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const int64_t at = group0[b] + min(k / G + g, groups - 1);
-            vs[u][b].v[g] = s.scales[at];
-            if (s.mins) vm[u][b].v[g] = s.mins[at];
+            const int at = min(k / G + g, groups - 1);
+            v.s[u][b][g] = scales[b][at];
+            if (s.mins) v.m[u][b][g] = mins[b][at];
           }
         }
       }
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+      for (int i = 0; i < 4; ++i) {
+        const bool in = k + 32 * i < s.K;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vx[u][m][i] = uint4{0, 0, 0, 0};
-          if (whole || k + 32 * i < s.K)
-            vx[u][m][i] = *reinterpret_cast<const uint4*>(x[m] + k + 32 * i);
+        for (int m = 0; m < MB; ++m) {
+          v.x[u][m][i] = uint4{0, 0, 0, 0};
+          if (in) v.x[u][m][i] = *reinterpret_cast<const uint4*>(x[m] + k + 32 * i);
         }
+      }
     }
+  };
+  f32x4 acc[MB][2] = {};
+  auto add = [&](const Stage& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t d[2][4];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        d[b][0] = vc[u][b].x, d[b][1] = vc[u][b].y, d[b][2] = vc[u][b].z, d[b][3] = vc[u][b].w;
+        d[b][0] = v.c[u][b].x, d[b][1] = v.c[u][b].y, d[b][2] = v.c[u][b].z, d[b][3] = v.c[u][b].w;
         transpose4(d[b]);
       }
 #pragma unroll
@@ -236,16 +250,16 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
           for (int b = 0; b < 2; ++b) w[b] = codes8<T>(d[b][st]);
 #pragma unroll
           for (int m = 0; m < MB; ++m) {
-            const typename Vec8<T>::type v = order8<T>(vx[u][m][st]);
-            sx[m] = mfma16(v, one8, sx[m]);
+            const typename Vec8<T>::type xv = order8<T>(v.x[u][m][st]);
+            sx[m] = mfma16(xv, one8, sx[m]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) sum[m][b] = mfma16(v, w[b], sum[m][b]);
+            for (int b = 0; b < 2; ++b) sum[m][b] = mfma16(xv, w[b], sum[m][b]);
           }
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float sc = (float)vs[u][b].v[g];
-          const float mn = s.mins ? fmaf(-16.f, sc, (float)vm[u][b].v[g]) : -24.f * sc;
+          const float sc = (float)v.s[u][b][g];
+          const float mn = s.mins ? fmaf(-16.f, sc, (float)v.m[u][b][g]) : -24.f * sc;
 #pragma unroll
           for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -255,42 +269,75 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
       }
     }
   };
-  int k = wv * kTurn;
-  for (; k + (U - 1) * kWaves * kTurn + kTurn <= s.K; k += U * kWaves * kTurn) turns(k, std::true_type{});
-  if (k < s.K) turns(k, std::false_type{});
+  Stage va, vb;
+  load(0, va);
+  for (int i = 0; i < stages; i += 2) {
+    if (i + 1 < stages) load(i + 1, vb);
+    add(va);
+    if (i + 1 == stages) break;
+    if (i + 2 < stages) load(i + 2, va);
+    add(vb);
+  }
 
-  // sums of the four waves: [wave][tile of 16 x 16][lane]
-  f32x4* part = (f32x4*)lds;
-#pragma unroll
-  for (int m = 0; m < MB; ++m)
-#pragma unroll
-    for (int b = 0; b < 2; ++b) part[(wv * MB * 2 + m * 2 + b) * 64 + lane] = acc[m][b];
-  __syncthreads();
-  for (int i = wv; i < (ACT ? MB : MB * 2); i += kWaves) {
-    const int m = ACT ? i : i >> 1;
-    f32x4 v[2];
-#pragma unroll
-    for (int b = 0; b < (ACT ? 2 : 1); ++b) {
-      const int at = ACT ? m * 2 + b : i;
-      v[b] = part[at * 64 + lane];
-#pragma unroll
-      for (int o = 1; o < kWaves; ++o) {
-        const f32x4 p = part[(o * MB * 2 + at) * 64 + lane];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[b][j] += p[j];
-      }
-    }
-    const int n = n0 + (ACT ? 0 : 16 * (i & 1)) + r;
-    if (n >= s.N) continue;
+  // tile i of the MB x 2 (with the activation: of the MB pairs)
+  auto put = [&](int m, int b, const f32x4& g, const f32x4& u) {
+    const int n = n0 + (ACT ? 0 : 16 * b) + r;
+    if (n >= s.N) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = 16 * m + 4 * q + j;
       if (row >= t.n) continue;
-      float o = ACT ? gated(v[0][j], v[1][j]) : v[0][j];
+      float o = ACT ? gated(g[j], u[j]) : g[j];
       if (s.rows && w4_row(s, t.row0 + row) < 0) o = __builtin_nanf("");
       ((O*)s.y)[(int64_t)(t.row0 + row) * s.ldy + n] = from_f32<O>(o);
     }
+  };
+  if (parts == 1) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int b = 0; b < (ACT ? 1 : 2); ++b) put(m, b, acc[m][b], acc[m][1]);
+    return;
   }
+  // the four waves' sums, [wave][tile of 16 x 16][lane]
+  f32x4* sums = (f32x4*)lds;
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) sums[(wv * MB * 2 + m * 2 + b) * 64 + lane] = acc[m][b];
+  __syncthreads();
+  for (int i = wv; i < (ACT ? MB : MB * 2); i += kWaves) {
+    f32x4 v[2];
+#pragma unroll
+    for (int b = 0; b < (ACT ? 2 : 1); ++b) {
+      const int at = ACT ? i * 2 + b : i;
+      v[b] = sums[at * 64 + lane];
+#pragma unroll
+      for (int o = 1; o < kWaves; ++o) {
+        const f32x4 p = sums[(o * MB * 2 + at) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[b][j] += p[j];
+      }
+    }
+    put(ACT ? i : i >> 1, i & 1, v[0], v[1]);
+  }
+}
+
+__device__ __forceinline__ Tile w4_tile(const W4Args& s, int rows) {
+  if (s.bounds) return find_tile(s.bounds, s.E, s.R, blockIdx.y, rows);
+  const int row0 = blockIdx.y * rows;
+  return Tile{0, row0, min(rows, s.R - row0)};
+}
+
+template <class T, class O, int G, bool ACT>
+__global__ __launch_bounds__(64 * kWaves, 2) void k_w4_mm(W4Args s) {
+  __shared__ __align__(16) float lds[kWaves * 4 * 64 * 4];
+  const Tile t = w4_tile(s, kRows);
+  if (t.n <= 0) return;
+  if (t.n <= 16)
+    w4_rows<T, O, G, ACT, 1, 2>(s, t, lds);
+  else
+    w4_rows<T, O, G, ACT, 2, 1>(s, t, lds);
 }
 
 // ---------------------------------------------------------- one or two rows
@@ -338,11 +385,12 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 }
 
 constexpr int kVecRows = 2;  // rows of x the vector path takes
-constexpr int kOuts = 8;     // rows of the weights per wave
-
+constexpr int kOuts = 8;     // rows of the weights per wave and block
+constexpr int kMostTurns = 4;
 constexpr int kBatch = 4;    // loads whose rows are summed together
+constexpr int kEnoughGroups = 4096;
 constexpr int kVecInputs = 16384;  // rows x inputs of x that the LDS holds
-constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kVecRows * 4;
+constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kMostTurns * kVecRows * 4;
 
 template <class T, class O, bool ACT, int M>
 __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* lds) {
@@ -353,17 +401,23 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
   const int at = lane & (lanes - 1), which = lane >> log_lanes;
   const int chunks = (s.K + 32 * lanes - 1) >> (5 + log_lanes);
   constexpr int kN = ACT ? kOuts / 2 : kOuts;
-  const int n0 = blockIdx.x * (ACT ? kCols / 2 : kCols) + wv * kN;
+  const int outs = kOuts * s.turns;
+  const int n0 = (blockIdx.x * kWaves + wv) * kN * s.turns;
   const int groups = s.K / s.G;
   uint4* xs = (uint4*)lds;                                   // [m][chunk][piece][lane]
   float* sums = (float*)(lds + kVecInputs * 2);              // [m][chunk][lane]
-  float* mine = (float*)(lds + kVecInputs * 2 + kVecInputs / 32 * 4) + wv * kOuts * M;
+  float* mine = (float*)(lds + kVecInputs * 2 + kVecInputs / 32 * 4) + wv * outs * M;
 
   // the wave's rows, clamped to the last one
   const int64_t first = (int64_t)t.e * (ACT ? 2 : 1) * s.N + min(n0, s.N - 1);
   const int most = max(s.N - 1 - n0, 0);
   const uint8_t* codes = s.codes + first * (s.K / 2);
-  const int64_t group0 = first * groups;
+  const uint8_t* codes_up = codes + (int64_t)s.N * (s.K / 2);
+  const f16* scales = s.scales + first * groups;
+  const f16* scales_up = scales + (int64_t)s.N * groups;
+  const f16* mins = s.mins + first * groups;
+  const f16* mins_up = mins + (int64_t)s.N * groups;
+  const int log_g = s.G == 32 ? 5 : s.G == 64 ? 6 : 7;
   struct Loads {
     uint4 c[kBatch];
     f16 s[kBatch], m[kBatch];
@@ -375,11 +429,14 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
       const int j = (batch * kBatch + i) * sub + which;
       l.c[i] = uint4{0, 0, 0, 0};
       l.s[i] = l.m[i] = (f16)0.f;
-      if (j < kOuts && k < s.K) {
-        const int64_t row = min(ACT ? j & 3 : j, most) + (ACT && (j & 4) ? (int64_t)s.N : 0);
-        l.c[i] = *reinterpret_cast<const uint4*>(codes + row * (s.K / 2) + k / 2);
-        l.s[i] = s.scales[group0 + row * groups + k / s.G];
-        if (s.mins) l.m[i] = s.mins[group0 + row * groups + k / s.G];
+      if (j < outs && k < s.K) {
+        // (the rows of a wave lie within 2^25 bytes and 2^21 groups)
+        const int wr = min(ACT ? (j >> 3) * 4 + (j & 3) : j, most);
+        const bool up = ACT && (j & 4);
+        const int g = wr * groups + (k >> log_g);
+        l.c[i] = *reinterpret_cast<const uint4*>((up ? codes_up : codes) + wr * (s.K / 2) + k / 2);
+        l.s[i] = (up ? scales_up : scales)[g];
+        if (s.mins) l.m[i] = (up ? mins_up : mins)[g];
       }
     }
   };
@@ -407,7 +464,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
   }
   __syncthreads();
 
-  const int batches = sub * kBatch >= kOuts ? 1 : kOuts / (sub * kBatch);
+  const int batches = (outs + sub * kBatch - 1) / (sub * kBatch);
   float acc[kBatch][M];
   for (int batch = 0, chunk = 0; batch < batches;) {
     const bool last = chunk + 1 == chunks;
@@ -455,7 +512,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           const float v = lanes_sum(acc[i][m], lanes);
-          if (at == 0 && j < kOuts) mine[j * M + m] = v;
+          if (at == 0 && j < outs) mine[j * M + m] = v;
         }
       }
     }
@@ -463,38 +520,34 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
     batch = nb, chunk = nc;
   }
   __syncthreads();
-  if (lane < kN * M) {
-    const int j = lane % kN, m = lane / kN;
+  static_assert(kOuts * kMostTurns * kVecRows <= 64, "an output per lane");
+  if (lane < kN * s.turns * M) {
+    const int j = lane / M, m = lane % M;
     if (m < t.n && n0 + j < s.N) {
-      float o = mine[j * M + m];
-      if (ACT) o = gated(o, mine[(j + kN) * M + m]);
+      float o = mine[(ACT ? (j >> 2) * 8 + (j & 3) : j) * M + m];
+      if (ACT) o = gated(o, mine[((j >> 2) * 8 + 4 + (j & 3)) * M + m]);
       if (s.rows && w4_row(s, t.row0 + m) < 0) o = __builtin_nanf("");
       ((O*)s.y)[(int64_t)(t.row0 + m) * s.ldy + n0 + j] = from_f32<O>(o);
     }
   }
 }
 
+// Up to 16 rows of an expert: by v_dot2 or on the matrix cores.
+constexpr int kFewRows = 16;
 template <class T, class O, int G, bool ACT>
-__global__ __launch_bounds__(64 * kWaves, 4) void k_w4_rows(W4Args s) {
+__global__ __launch_bounds__(64 * kWaves, 3) void k_w4_few(W4Args s) {
   __shared__ __align__(16) uint8_t lds[kVecLds];
-  static_assert(kVecLds >= kWaves * 4 * 64 * 16, "sums of the waves");
-  Tile t;
-  if (s.bounds) {
-    t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kRows);
-  } else {
-    t.e = 0, t.row0 = blockIdx.y * kRows, t.n = min(kRows, s.R - t.row0);
-  }
+  static_assert(kVecLds >= kWaves * 2 * 64 * 16, "sums of the waves");
+  const Tile t = w4_tile(s, kFewRows);
   if (t.n <= 0) return;
-  // (a whole number of turns of 64 lanes x 32 inputs)
+  // (x of the tile in LDS, in whole turns of 64 lanes x 32 inputs)
   const bool vec = t.n <= kVecRows && t.n * ((s.K + 2047) & ~2047) <= kVecInputs;
   if (vec && t.n == 1)
     w4_vec<T, O, ACT, 1>(s, t, lds);
   else if (vec)
     w4_vec<T, O, ACT, 2>(s, t, lds);
-  else if (t.n <= 16)
-    w4_rows<T, O, G, ACT, 1>(s, t, (float*)lds);
   else
-    w4_rows<T, O, G, ACT, 2>(s, t, (float*)lds);
+    w4_rows<T, O, G, ACT, 1, 1>(s, t, (float*)lds);
 }
 
 }  // namespace
@@ -529,12 +582,20 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   if (((uintptr_t)codes & 15u) || ((uintptr_t)scales & 3u) || ((uintptr_t)mins & 3u))
     return fail(BITSMOE_EINVAL, "codes must be 16-byte aligned, scales and mins 4-byte aligned");
   W4Args s{x, ldx, rows, div, x_rows, (const uint8_t*)codes, (const f16*)scales, (const f16*)mins,
-           bounds, R, E, N, K, G, y, ldy, act};
+           bounds, R, E, N, K, G, y, ldy, act, 1};
   const hipStream_t st = (hipStream_t)stream;
   const bool wide = ((uintptr_t)x & 15u) == 0 && ldx % 8 == 0;
-  const long long tiles = !wide ? R : bounds ? max_tiles(R, E, kRows) : ((long long)R + kRows - 1) / kRows;
+  const bool few = R <= (long long)kFewRows * E;
+  const int rows_tile = !wide ? 1 : few ? kFewRows : kRows;
+  const long long tiles =
+      bounds ? max_tiles(R, E, rows_tile) : ((long long)R + rows_tile - 1) / rows_tile;
   if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);
-  const int per = !wide ? 4 : act ? kCols / 2 : kCols;
+  int per = !wide ? 4 : act ? kCols / 2 : kCols;
+  // a block per wave once there are enough work-groups to fill the chip
+  // several times over: finding the rows and bringing in x is done once for
+  // four blocks, and the waves have no sums to exchange
+  if (wide && tiles * ((N + per * kWaves - 1) / (per * kWaves)) >= kEnoughGroups) s.turns = kWaves;
+  per *= s.turns;
   const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)tiles);
   auto go = [&](auto t, auto o) {
     using T = decltype(t);
@@ -543,12 +604,17 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
       hipLaunchKernelGGL((k_w4_any<T, O>), grid, dim3(256), 0, st, s);
       return;
     }
+    const dim3 block(64 * kWaves);
     auto rows_of = [&](auto g) {
       constexpr int kG = decltype(g)::value;
-      if (act)
-        hipLaunchKernelGGL((k_w4_rows<T, O, kG, true>), grid, dim3(64 * kWaves), 0, st, s);
+      if (few && act)
+        hipLaunchKernelGGL((k_w4_few<T, O, kG, true>), grid, block, 0, st, s);
+      else if (few)
+        hipLaunchKernelGGL((k_w4_few<T, O, kG, false>), grid, block, 0, st, s);
+      else if (act)
+        hipLaunchKernelGGL((k_w4_mm<T, O, kG, true>), grid, block, 0, st, s);
       else
-        hipLaunchKernelGGL((k_w4_rows<T, O, kG, false>), grid, dim3(64 * kWaves), 0, st, s);
+        hipLaunchKernelGGL((k_w4_mm<T, O, kG, false>), grid, block, 0, st, s);
     };
     if (G == 32)
       rows_of(std::integral_constant<int, 32>{});
