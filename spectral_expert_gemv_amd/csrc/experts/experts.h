@@ -83,16 +83,31 @@ __device__ inline void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<f32x4*>(p)[1] = b;
 }
 
+// 1 / (1 + exp(-g)).  exp2 of the product with log2(e), whose rounding error
+// and low part are put back by one multiplication, and the hardware's
+// reciprocal: each within a step of float32, a third of the instructions of
+// an exact exp and division (products with the activation, 24576 rows of 64
+// experts: 361 -> 351 us).
+// (The maximum turns the NaN of inf - inf into a factor that leaves 0 or inf.)
+__device__ inline float sigmoid(float g) {
+#pragma clang fp contract(off)
+  constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596299112661746887e-8f;
+  const float t = g * kHi;
+  const float lo = fmaxf(fmaf(g, kLo, fmaf(g, kHi, -t)), -1.0f);
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182464599609375f, 1.0f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 // SiLU(g) * u, and its derivative with respect to g and u times dh.  No
 // contraction, so that the bits do not depend on which kernel (by alignment)
 // evaluates them.
 __device__ inline float gated(float g, float u) {
 #pragma clang fp contract(off)
-  return g / (1.0f + expf(-g)) * u;
+  return g * sigmoid(g) * u;
 }
 __device__ inline void gated_grad(float g, float u, float dh, float& dg, float& du) {
 #pragma clang fp contract(off)
-  const float s = 1.0f / (1.0f + expf(-g));
+  const float s = sigmoid(g);
   // 1 + g (1 - s) as written loses nothing: both terms are of order 1 where it matters
   dg = dh * u * (s * (1.0f + g * (1.0f - s)));
   du = dh * (g * s);

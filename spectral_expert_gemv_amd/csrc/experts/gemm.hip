@@ -511,15 +511,17 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   const int mt = MODE == kDw ? s.E * ntm : count_tiles(s.bounds, s.E, s.R, kTile);
   const uint32_t total = (uint32_t)mt * ntn, left = total % kUnits;
   const uint32_t whole = left <= kSplitMost ? total - left : total;
-  // Work-group b runs on XCD b % 8, and every XCD takes one run of tiles.
+  // Work-group b runs on XCD b % 8, and every XCD takes 32 consecutive tiles of
+  // a round, which share operand rows in its L2.  (One long run per XCD would
+  // leave those with the small experts' part tiles idle at the end.)
   uint32_t b = blockIdx.x, id;
   int part = -1;
-  const uint32_t run = (whole + 7) / 8;
-  if (b < run * 8) {
-    id = (b & 7) * run + (b >> 3);
+  const uint32_t rounds = (whole + kUnits - 1) / kUnits;
+  if (b < rounds * kUnits) {
+    id = b / kUnits * kUnits + (b & 7) * (kUnits / 8) + b % kUnits / 8;
     if (id >= whole) return;
   } else {
-    b -= run * 8;
+    b -= rounds * kUnits;
     const uint32_t run4 = ((total - whole) * 4 + 7) / 8;
     const uint32_t id4 = (b & 7) * run4 + (b >> 3);
     if ((b >> 3) >= run4 || id4 >= (total - whole) * 4) return;
@@ -755,9 +757,9 @@ int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
       rc = fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", s.R, s.E, s.N, s.K);
       return;
     }
-    // enough for any split of at most mt * ntn tiles into whole and cut ones
+    // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
     const long long cut = mt * ntn < kSplitMost ? mt * ntn : kSplitMost;
-    const dim3 grid((unsigned)((mt * ntn + 7) / 8 * 8 + cut * 3 + 8));
+    const dim3 grid((unsigned)((mt * ntn + kUnits - 1) / kUnits * kUnits + cut * 4 + 8));
     if (MODE == kFwd && s.act)
       hipLaunchKernelGGL((k_mm_tile<T, O, MODE, MODE == kFwd>), grid, dim3(512), 0, st, s);
     else
