@@ -273,6 +273,9 @@ __device__ __forceinline__ void tile_place(uint32_t id, int mt, int nt, int& m, 
   n = r / gm;
 }
 
+constexpr int kTile = 256;                          // rows and columns of a tile
+constexpr uint32_t kLds = 2 * 2 * kTile * kStep * 2;  // two buffers of two operands
+
 // Output rows m0 .. m0 + mn and columns n0 .. n0 + nn of expert e, with the
 // contraction c0 .. c0 + cn.
 template <class T, class O, int MODE, int TM, int TN, int WM, int WN, bool ACT>
@@ -464,31 +467,57 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
     wait_copies<0>();  // nothing is written into this work-group's LDS after its end
   }
 
-  // the products were formed transposed: lane % 16 is the output row, and a
-  // lane holds 4 consecutive columns 4 (lane / 16) .. of each 16 x 16 tile
+  // The products were formed transposed: lane % 16 is the output row, and a
+  // lane holds 4 consecutive columns 4 (lane / 16) .. of each 16 x 16 tile.
+  // Stored like that a store would touch 16 rows with 32 (64) bytes each; so
+  // the tile goes through LDS, as far as it fits at a time, and leaves as
+  // whole rows, 16 bytes a lane.  16-byte piece p of LDS row r lies at
+  // p ^ (r % 16), which spreads 16 rows' writes over the banks.
+  constexpr int kOut = ACT ? TN / 2 : TN;                         // columns
+  constexpr int kPassRows = kLds / (kOut * (int)sizeof(O)) < TM ? kLds / (kOut * (int)sizeof(O)) : TM;
+  constexpr int kPasses = TM / kPassRows, kI = MI / kPasses;       // 16-row blocks of a wave per pass
+  constexpr int kRowPieces = kOut * (int)sizeof(O) / 16;
+  constexpr int kKey = kRowPieces < 16 ? kRowPieces - 1 : 15;
+  static_assert(kPassRows * kPasses == TM && kI * kPasses == MI, "whole passes");
   O* Y = (O*)s.y;
   const int64_t ldy = MODE == kDw ? s.K : s.ldy;
   if (MODE == kDw) Y += (size_t)e * s.N * s.K;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = wm + 16 * i + (lane & 15);
-    if (m >= mn) continue;
-    O* row = Y + (int64_t)(m0 + m) * ldy + n0;
+  for (int pass = 0; pass < kPasses; ++pass) {
+    // (nobody reads the operands, or the pass before, any more)
+    lds_barrier();
 #pragma unroll
-    for (int j = 0; j < NI; j += ACT ? 2 : 1) {
-      const int n = (ACT ? (wn + 16 * j) / 2 : wn + 16 * j) + 4 * (lane >> 4);
-      f32x4 v = acc[i][j];
-      if constexpr (ACT) {
+    for (int i = 0; i < kI; ++i) {
+      const int row = (wv / WN) * (kPassRows / WM) + 16 * i + (lane & 15);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = gated(v[q], acc[i][j + 1][q]);
-      }
-      if (n + 4 <= nn) {  // (columns are a multiple of 8, rows 16-byte aligned)
+      for (int j = 0; j < NI; j += ACT ? 2 : 1) {
+        f32x4 v = acc[pass * kI + i][j];
+        if constexpr (ACT) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = gated(v[q], acc[pass * kI + i][j + 1][q]);
+        }
         typedef __attribute__((ext_vector_type(4))) O O4;
         O4 o;
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] = (O)v[q];
-        *reinterpret_cast<O4*>(row + n) = o;
+        const int at = ((ACT ? (wn + 16 * j) / 2 : wn + 16 * j) + 4 * (lane >> 4)) * (int)sizeof(O);
+        typedef __attribute__((address_space(3))) O4 lds_o4;
+        *(lds_o4*)(uintptr_t)(base + row * (kOut * (int)sizeof(O)) +
+                              ((((at >> 4) ^ (row & kKey)) << 4) | (at & 15))) = o;
       }
+    }
+    lds_barrier();
+#pragma unroll 4
+    for (int at = threadIdx.x; at < kPassRows * kRowPieces; at += NT) {
+      const int row = at / kRowPieces, piece = at % kRowPieces;
+      // the output row behind LDS row `row` of this pass
+      const int m = row / (kPassRows / WM) * (TM / WM) + pass * (kPassRows / WM) + row % (kPassRows / WM);
+      typedef __attribute__((address_space(3))) const s16x8 lds_s8;
+      const s16x8 v = *(lds_s8*)(uintptr_t)(base + row * (kOut * (int)sizeof(O)) +
+                                            ((piece ^ (row & kKey)) << 4));
+      const int n = piece * (16 / (int)sizeof(O));
+      if (m < mn && n < nn)  // (columns are a multiple of 8)
+        *reinterpret_cast<s16x8*>(Y + (int64_t)(m0 + m) * ldy + n0 + n) = v;
     }
   }
 }
@@ -497,12 +526,10 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 // with 256 x 256 tiles, then what is left, cut into 128 x 128 tiles if it
 // would fill at most half a round (see kSplitMost).
 constexpr int kUnits = 256;       // compute units of an MI355X, one work-group each (its LDS)
-constexpr int kTile = 256;        // rows and columns of a tile
 constexpr int kSplitMost = 128;   // left-over tiles that are cut in four
 
 template <class T, class O, int MODE, bool ACT>
 __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
-  constexpr uint32_t kLds = 2 * kTile * kStep * 2 * 2;
   __shared__ __align__(1024) uint8_t lds[kLds];
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   const int cols = MODE == kFwd ? s.N : s.K;     // output columns
