@@ -372,18 +372,31 @@ int bitsmoe_moe_group(const int32_t* ids, int P, int E, int32_t* bounds, int32_t
  *                                written: 0 for an expert without rows)
  * rows (may be NULL): sorted row i reads row rows[i] / div of x, which has
  * x_rows rows (the order of the pairs with div = k reads tokens); an index
- * outside them makes the products NaN.  Without rows, x_rows >= R. */
+ * outside them makes the products NaN.  Without rows, x_rows >= R.
+ * Rows that are not whole 16-byte pieces (an odd N or K, a stride or pointer
+ * that is not aligned) are first copied into ws, padded: at least
+ * bitsmoe_grouped_matmul_workspace_size() bytes, 256-byte aligned, 0 for
+ * aligned operands (ws may then be NULL).  op says which call it is for; a, lda,
+ * a_rows are x (dx, dw: dy), b, ldb, b_rows are w (dw: x), of which only the
+ * alignment is looked at (w: ldb and b_rows are not). */
+#define BITSMOE_GROUPED_FORWARD 0
+#define BITSMOE_GROUPED_DX      1
+#define BITSMOE_GROUPED_DW      2
+int bitsmoe_grouped_matmul_workspace_size(int op, const void* a, int64_t lda, int64_t a_rows,
+                                          const void* b, int64_t ldb, int64_t b_rows, int R, int E,
+                                          int N, int K, int act, size_t* bytes);
 int bitsmoe_grouped_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
                            int div, const void* w, const int32_t* bounds, int R, int E, int N,
-                           int K, int act, void* y, int y_dtype, int64_t ldy,
-                           bitsmoe_stream_t stream);
+                           int K, int act, void* y, int y_dtype, int64_t ldy, void* ws,
+                           size_t ws_bytes, bitsmoe_stream_t stream);
 int bitsmoe_grouped_matmul_dx(int dtype, const void* dy, int64_t lddy, const void* w,
                               const int32_t* bounds, int R, int E, int N, int K, void* dx,
-                              int dx_dtype, int64_t lddx, bitsmoe_stream_t stream);
+                              int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes,
+                              bitsmoe_stream_t stream);
 int bitsmoe_grouped_matmul_dw(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                               int x_rows, const int32_t* rows, int div, const int32_t* bounds,
-                              int R, int E, int N, int K, void* dw, int dw_dtype,
-                              bitsmoe_stream_t stream);
+                              int R, int E, int N, int K, void* dw, int dw_dtype, void* ws,
+                              size_t ws_bytes, bitsmoe_stream_t stream);
 
 /* Gated activation of rows a = [gate | up] (R rows of 2F): h = SiLU(gate) up;
  * its gradient da (R rows of 2F) from dh.  bounds (may be NULL, with E): only

@@ -78,12 +78,14 @@ _SIGS = {
     "bitsmoe_moe_route_grad": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i64, _vp], _i),
     "bitsmoe_moe_group_workspace_size": ([_i, _i, _psz], _i),
     "bitsmoe_moe_group": ([_vp, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "bitsmoe_grouped_matmul_workspace_size": ([_i, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _i,
+                                               _i, _i, _psz], _i),
     "bitsmoe_grouped_matmul": ([_i, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i,
-                                _i64, _vp], _i),
-    "bitsmoe_grouped_matmul_dx": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i64, _vp],
-                                  _i),
+                                _i64, _vp, _sz, _vp], _i),
+    "bitsmoe_grouped_matmul_dx": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i64, _vp,
+                                   _sz, _vp], _i),
     "bitsmoe_grouped_matmul_dw": ([_i, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _i, _i, _i, _i,
-                                   _vp, _i, _vp], _i),
+                                   _vp, _i, _vp, _sz, _vp], _i),
     "bitsmoe_silu_mul": ([_i, _vp, _i64, _vp, _i, _i, _i, _vp, _i64, _vp], _i),
     "bitsmoe_silu_mul_grad": ([_i, _vp, _i64, _vp, _i64, _vp, _i, _i, _i, _vp, _i64, _vp], _i),
     "bitsmoe_moe_combine": ([_i, _vp, _i64, _i, _vp, _vp, _i, _i, _i, _vp, _i, _i64, _vp], _i),
@@ -567,7 +569,18 @@ def _bounds(bounds, E):
     return _array("bounds", bounds, _I32, (E + 1,))
 
 
-def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None):
+def _matmul_scratch(op, pa, lda, a_rows, pb, ldb, b_rows, R, E, N, K, act, ws, index, stream):
+    """The workspace of a product, or None: the given one, or one for operands
+    whose rows are not whole 16-byte pieces."""
+    if ws is not None or not ((pa | pb) & 15 or (lda | ldb | N | K) & 7):
+        return ws
+    out = ctypes.c_size_t(0)
+    _check(_lib.bitsmoe_grouped_matmul_workspace_size(op, pa, lda, a_rows, pb, ldb, b_rows, R, E, N,
+                                                      K, act, ctypes.byref(out)))
+    return _scratch(out.value, index, stream)
+
+
+def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, ws=None, stream=None):
     """y (R x N) with y[i] = W_e x[i] for the sorted rows i of expert e.
     w: E x N x K; with act="silu_mul" E x 2N x K (gate rows first) and y =
     SiLU(gate) * up.  rows (R int32): row i reads x[rows[i] // div].  y has
@@ -583,13 +596,15 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, stream=None
     if y is None:
         y = _new((R, N), x.dtype, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
-    _enqueue(_lib.bitsmoe_grouped_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div,
-             _array("w", w, x.dtype, (E, n2, K)), _bounds(bounds, E), R, E, N, K, ACT[act], py,
-             _dtype(y), ldy)
+    pw, code = _array("w", w, x.dtype, (E, n2, K)), ACT[act]
+    ws = _matmul_scratch(0, px, ldx, x.shape[0], pw, K, 0, R, E, N, K, code, ws, dev, stream)
+    _enqueue(_lib.bitsmoe_grouped_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div, pw,
+             _bounds(bounds, E), R, E, N, K, code, py, _dtype(y), ldy, _ptr(ws),
+             0 if ws is None else _nbytes(ws))
     return y
 
 
-def grouped_matmul_dx(dy, w, bounds, dx=None, stream=None):
+def grouped_matmul_dx(dy, w, bounds, dx=None, ws=None, stream=None):
     """dx (R x K) with dx[i] = W_e^T dy[i]: the gradient of grouped_matmul's
     sorted rows (of a gathered x, moe_combine adds up a token's rows)."""
     E, N, K = w.shape
@@ -599,13 +614,15 @@ def grouped_matmul_dx(dy, w, bounds, dx=None, stream=None):
     if dx is None:
         dx = _new((R, K), dy.dtype, dev, stream)
     px, ldx = _matrix("dx", dx, (R, K))
-    _enqueue(_lib.bitsmoe_grouped_matmul_dx, dev, stream, _dtype(dy), pd, ldd,
-             _array("w", w, dy.dtype, (E, N, K)), _bounds(bounds, E), R, E, N, K, px, _dtype(dx),
-             ldx)
+    pw = _array("w", w, dy.dtype, (E, N, K))
+    ws = _matmul_scratch(1, pd, ldd, R, pw, K, 0, R, E, N, K, 0, ws, dev, stream)
+    _enqueue(_lib.bitsmoe_grouped_matmul_dx, dev, stream, _dtype(dy), pd, ldd, pw,
+             _bounds(bounds, E), R, E, N, K, px, _dtype(dx), ldx, _ptr(ws),
+             0 if ws is None else _nbytes(ws))
     return dx
 
 
-def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
+def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, ws=None, stream=None):
     """dw (E x N x K) with dw_e = sum of dy[i] x[i]^T over the sorted rows of
     expert e; 0 for an expert without rows.  float32 unless dw is given."""
     R, N = dy.shape
@@ -619,9 +636,11 @@ def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, stream=None):
     pr, div = _gather(x, rows, div, R)
     if dw is None:
         dw = _new((E, N, K), _F32, dev, stream)
+    ws = _matmul_scratch(2, pd, ldd, R, px, ldx, x.shape[0], R, E, N, K, 0, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul_dw, dev, stream, _dtype(dy), pd, ldd, px, ldx, x.shape[0],
              pr, div, _bounds(bounds, E), R, E, N, K, _array("dw", dw, dw.dtype, (E, N, K)),
-             _dtype(dw))
+             _dtype(dw), _ptr(ws),
+             0 if ws is None else _nbytes(ws))
     return dw
 
 

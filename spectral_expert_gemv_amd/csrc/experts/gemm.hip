@@ -18,14 +18,15 @@ struct MmArgs {
   const void* a;   // forward: x; dx, dw: dy
   int64_t lda;
   const void* b;   // forward, dx: w; dw: x
-  int64_t ldb;     // dw: row stride of x
+  int64_t ldb;     // their row strides (w: of all experts' rows)
   const int32_t* rows;  // forward, dw: x row of sorted row i is rows[i] / div
   int div, x_rows;
   const int32_t* bounds;
   int R, E, N, K;  // W_e is (act ? 2 N : N) x K
   void* y;
-  int64_t ldy;
+  int64_t ldy;     // dw: K
   int act;
+  int y16;         // rows of y are whole 16-byte pieces
 };
 
 // The row of x behind sorted row i; -1: an index outside x, whose products
@@ -37,117 +38,30 @@ __device__ inline int x_row(const MmArgs& s, int i) {
   return r < s.x_rows ? r : -1;
 }
 
-// ------------------------------------------------------------ any layout
-// 64 x 64 tiles, 4 waves of 32 x 32, 32 of the contraction per step.  Both
-// operands are staged element by element with every index checked, so any
-// size, stride and alignment is served; shapes with 16-byte rows take the
-// kernels below.
-constexpr int kAnyTile = 64, kAnyStep = 32, kAnyLd = kAnyStep + 8;
-
-template <class T, class O, int MODE>
-__global__ __launch_bounds__(256) void k_mm_any(MmArgs s) {
-  __shared__ T la[kAnyTile][kAnyLd], lb[kAnyTile][kAnyLd];
-  __shared__ int lrow[kAnyTile];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const T* A = (const T*)s.a;
-  const T* B = (const T*)s.b;
-  const T nan = (T)__builtin_nanf("");
-  // m, n: output row and column, c: contraction
-  int m0, mn, n0, nn, c0, cn, e;
-  if (MODE == kDw) {
-    e = blockIdx.z;
-    int lo, hi;
-    expert_rows(s.bounds, e, s.R, lo, hi);
-    m0 = blockIdx.y * kAnyTile, mn = min(kAnyTile, s.N - m0);
-    n0 = blockIdx.x * kAnyTile, nn = min(kAnyTile, s.K - n0);
-    c0 = lo, cn = hi - lo;
-  } else {
-    const Tile t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kAnyTile);
-    if (t.n == 0) return;
-    e = t.e;
-    m0 = t.row0, mn = t.n;
-    const int per = MODE == kFwd && s.act ? kAnyTile / 2 : kAnyTile;
-    const int cols = MODE == kFwd ? s.N : s.K;
-    n0 = blockIdx.x * per, nn = min(per, cols - n0);
-    c0 = 0, cn = MODE == kFwd ? s.K : s.N;
-    if (tid < kAnyTile) lrow[tid] = tid < mn ? (MODE == kFwd ? x_row(s, m0 + tid) : m0 + tid) : 0;
+// Rows of `cols` elements of 2 bytes, at any stride and alignment, to rows of
+// whole 16-byte pieces, 0 past the end: what the tiled kernel wants of an
+// operand that is not like that.
+__global__ __launch_bounds__(256) void k_mm_pad(const uint16_t* __restrict__ src, int64_t ld,
+                                                int64_t rows, int cols, uint4* __restrict__ dst) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  typedef u4 loose __attribute__((aligned(2)));
+  const int per = (cols + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const uint16_t* p = src + r * ld + c;
+    u4 v = {0, 0, 0, 0};
+    if (c + 8 <= cols) {
+      v = *reinterpret_cast<const loose*>(p);
+    } else {
+      uint16_t e[8] = {};
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) e[j] = p[j];
+      __builtin_memcpy(&v, e, 16);
+    }
+    dst[i] = __builtin_bit_cast(uint4, v);
   }
-  const T* W = MODE == kDw ? nullptr : B + (size_t)e * (s.act ? 2 : 1) * s.N * s.K;
-  f32x4 acc[2][2] = {};
-  __syncthreads();
-  for (int c = 0; c < cn; c += kAnyStep) {
-    if (MODE == kDw) {
-      if (tid < kAnyStep) lrow[tid] = c + tid < cn ? x_row(s, c0 + c + tid) : 0;
-      __syncthreads();
-    }
-    for (int i = tid; i < kAnyTile * kAnyStep; i += 256) {
-      // the inner index runs along the operand's contiguous axis
-      const int ci = MODE == kDw ? i / kAnyTile : i % kAnyStep;
-      const int mi = MODE == kDw ? i % kAnyTile : i / kAnyStep;
-      T v = (T)0.f;
-      if (mi < mn && c + ci < cn) {
-        if (MODE == kDw)
-          v = A[(int64_t)(c0 + c + ci) * s.lda + m0 + mi];
-        else
-          v = lrow[mi] < 0 ? nan : A[(int64_t)lrow[mi] * s.lda + c + ci];
-      }
-      la[mi][ci] = v;
-    }
-    for (int i = tid; i < kAnyTile * kAnyStep; i += 256) {
-      const int ci = MODE == kFwd ? i % kAnyStep : i / kAnyTile;
-      const int ni = MODE == kFwd ? i / kAnyStep : i % kAnyTile;
-      T v = (T)0.f;
-      if (c + ci < cn) {
-        if (MODE == kFwd) {
-          // with the activation, blocks of 16 columns alternate gate and up
-          const int col = s.act ? (ni >> 5) * 16 + (ni & 15) : ni;
-          const int up = s.act ? (ni >> 4) & 1 : 0;
-          if (col < nn) v = W[((int64_t)up * s.N + n0 + col) * s.K + c + ci];
-        } else if (ni < nn) {
-          if (MODE == kDx)
-            v = W[(int64_t)(c + ci) * s.K + n0 + ni];
-          else
-            v = lrow[ci] < 0 ? nan : B[(int64_t)lrow[ci] * s.ldb + n0 + ni];
-        }
-      }
-      lb[ni][ci] = v;
-    }
-    __syncthreads();
-    const int r = lane & 15, q = (lane >> 4) * 8;
-    typename Vec8<T>::type fa[2], fb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fa[i] = *reinterpret_cast<const typename Vec8<T>::type*>(&la[(wv >> 1) * 32 + i * 16 + r][q]);
-      fb[i] = *reinterpret_cast<const typename Vec8<T>::type*>(&lb[(wv & 1) * 32 + i * 16 + r][q]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma16(fa[i], fb[j], acc[i][j]);
-    __syncthreads();
-  }
-  // D: column lane % 16, rows 4 (lane / 16) + v
-  O* Y = (O*)s.y;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int mi = (wv >> 1) * 32 + i * 16 + (lane >> 4) * 4 + v;
-        int ni = (wv & 1) * 32 + j * 16 + (lane & 15);
-        float o = acc[i][j][v];
-        if (MODE == kFwd && s.act) {
-          if (j) continue;
-          ni = (wv & 1) * 16 + (lane & 15);
-          o = gated(acc[i][0][v], acc[i][1][v]);
-        }
-        if (mi >= mn || ni >= nn) continue;
-        if (MODE == kDw)
-          Y[((int64_t)e * s.N + m0 + mi) * s.K + n0 + ni] = from_f32<O>(o);
-        else
-          Y[(int64_t)(m0 + mi) * s.ldy + n0 + ni] = from_f32<O>(o);
-      }
 }
 
 // -------------------------------------------------------- tiled, 16-byte rows
@@ -294,14 +208,14 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   OpB b;
   const uint8_t* A = (const uint8_t*)s.a;
   const uint8_t* Bp = (const uint8_t*)s.b;
-  if (MODE != kDw) Bp += (size_t)e * (ACT ? 2 : 1) * s.N * s.K * 2;
-  const int64_t lda = s.lda * 2, ldb = MODE == kDw ? s.ldb * 2 : (int64_t)s.K * 2;
+  const int64_t lda = s.lda * 2, ldb = s.ldb * 2;
+  if (MODE != kDw) Bp += (int64_t)e * (ACT ? 2 : 1) * s.N * ldb;
   uint32_t nan_rows = 0;  // bit i: copy i's row of A lies outside x
 #pragma unroll
   for (int i = 0; i < OpA::kCopies; ++i) {
     const int l = OpA::line(i), p = OpA::piece(i);
     if (kTrA) {
-      a.ptr[i] = A + (int64_t)(c0 + l) * lda + (int64_t)(m0 + min(8 * p, mn - 8)) * 2;
+      a.ptr[i] = A + (int64_t)(c0 + l) * lda + (int64_t)(m0 + min(8 * p, ((mn + 7) & ~7) - 8)) * 2;
     } else {
       const int row = m0 + min(l, mn - 1);
       const int xr = MODE == kFwd ? x_row(s, row) : row;
@@ -318,7 +232,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
       const int64_t row = n0 + min(col, nn - 1) + (ACT && (l & 16) ? s.N : 0);
       b.ptr[i] = Bp + row * ldb + p * 16;
     } else {
-      b.ptr[i] = Bp + (int64_t)(MODE == kDw ? 0 : l) * ldb + (int64_t)(n0 + min(8 * p, nn - 8)) * 2;
+      b.ptr[i] = Bp + (int64_t)(MODE == kDw ? 0 : l) * ldb + (int64_t)(n0 + min(8 * p, ((nn + 7) & ~7) - 8)) * 2;
     }
   }
 
@@ -480,7 +394,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   constexpr int kKey = kRowPieces < 16 ? kRowPieces - 1 : 15;
   static_assert(kPassRows * kPasses == TM && kI * kPasses == MI, "whole passes");
   O* Y = (O*)s.y;
-  const int64_t ldy = MODE == kDw ? s.K : s.ldy;
+  const int64_t ldy = s.ldy;
   if (MODE == kDw) Y += (size_t)e * s.N * s.K;
 #pragma unroll
   for (int pass = 0; pass < kPasses; ++pass) {
@@ -515,9 +429,18 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
       typedef __attribute__((address_space(3))) const s16x8 lds_s8;
       const s16x8 v = *(lds_s8*)(uintptr_t)(base + row * (kOut * (int)sizeof(O)) +
                                             ((piece ^ (row & kKey)) << 4));
-      const int n = piece * (16 / (int)sizeof(O));
-      if (m < mn && n < nn)  // (columns are a multiple of 8)
-        *reinterpret_cast<s16x8*>(Y + (int64_t)(m0 + m) * ldy + n0 + n) = v;
+      constexpr int kPer = 16 / (int)sizeof(O);
+      const int n = piece * kPer;
+      O* y = Y + (int64_t)(m0 + m) * ldy + n0 + n;
+      if (m < mn && s.y16 && n + kPer <= nn) {
+        *reinterpret_cast<s16x8*>(y) = v;
+      } else if (m < mn) {
+        typedef __attribute__((ext_vector_type(kPer))) O On;
+        const On o = __builtin_bit_cast(On, v);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (n + j < nn) y[j] = o[j];
+      }
     }
   }
 }
@@ -590,6 +513,25 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
 // instruction; rows of x past the tile's repeat the last one.
 constexpr int kFewRows = 64, kFewCols = 32, kFewWaves = 4;
 
+// 8 elements from an address of any element's alignment (the hardware takes
+// it), 0 from the `left`-th on
+template <class V, class T>
+__device__ __forceinline__ V few_load(const T* p, int left) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  typedef u4 loose __attribute__((aligned(2)));
+  u4 v = {0, 0, 0, 0};
+  if (left >= 8) {
+    v = *reinterpret_cast<const loose*>(p);
+  } else if (left > 0) {
+    V e = {};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < left) e[j] = p[j];
+    return e;
+  }
+  return __builtin_bit_cast(V, v);
+}
+
 template <class T, class O, bool ACT, int MB>
 __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* lds) {
   typedef typename Vec8<T>::type V;
@@ -601,7 +543,7 @@ __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* 
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int64_t row = ACT ? (int64_t)b * s.N + min(n0 + r, s.N - 1) : min(n0 + 16 * b + r, s.N - 1);
-    w[b] = (const T*)s.b + ((int64_t)t.e * (ACT ? 2 : 1) * s.N + row) * s.K + 8 * q;
+    w[b] = (const T*)s.b + ((int64_t)t.e * (ACT ? 2 : 1) * s.N + row) * s.ldb + 8 * q;
   }
   const T* x[MB];
   bool bad[MB];
@@ -620,13 +562,11 @@ __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = k0 + u * kFewWaves * 64 + 32 * h;
-        const bool in = whole || k + 8 * q < s.K;
+        const int left = whole ? 8 : s.K - (k + 8 * q);  // inputs of this lane
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          vw[u][b][h] = *reinterpret_cast<const V*>(in ? (const void*)(w[b] + k) : (const void*)g_pad);
+        for (int b = 0; b < 2; ++b) vw[u][b][h] = few_load<V>(w[b] + k, left);
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-          vx[u][m][h] = *reinterpret_cast<const V*>(in ? (const void*)(x[m] + k) : (const void*)g_pad);
+        for (int m = 0; m < MB; ++m) vx[u][m][h] = few_load<V>(x[m] + k, left);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -668,7 +608,7 @@ __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* 
     bool nan = false;
 #pragma unroll
     for (int u = 0; u < MB; ++u) nan = u == m ? bad[u] : nan;
-    if (16 * m + r >= t.n || n >= s.N) continue;  // (N is a multiple of 8)
+    if (16 * m + r >= t.n) continue;
     typedef __attribute__((ext_vector_type(4))) O O4;
     O4 o;
 #pragma unroll
@@ -676,7 +616,14 @@ __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* 
       const float f = ACT ? gated(v[0][j], v[1][j]) : v[0][j];
       o[j] = (O)(nan ? __builtin_nanf("") : f);
     }
-    *reinterpret_cast<O4*>(Y + (int64_t)(t.row0 + 16 * m + r) * s.ldy + n) = o;
+    O* y = Y + (int64_t)(t.row0 + 16 * m + r) * s.ldy + n;
+    if (s.y16 && n + 4 <= s.N) {
+      *reinterpret_cast<O4*>(y) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < s.N) y[j] = o[j];
+    }
   }
 }
 
@@ -725,64 +672,89 @@ int rows_check(const int32_t* rows, int div, int x_rows, int R) {
   return BITSMOE_OK;
 }
 
-template <int MODE>
-int launch_any(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
-  dim3 grid;
-  if (MODE == kDw) {
-    grid = dim3((unsigned)((s.K + kAnyTile - 1) / kAnyTile),
-                (unsigned)((s.N + kAnyTile - 1) / kAnyTile), (unsigned)s.E);
-  } else {
-    const int per = MODE == kFwd && s.act ? kAnyTile / 2 : kAnyTile;
-    const int cols = MODE == kFwd ? s.N : s.K;
-    const long long tiles = max_tiles(s.R, s.E, kAnyTile);
-    if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", s.R, s.E);
-    grid = dim3((unsigned)((cols + per - 1) / per), (unsigned)tiles);
-  }
-  with_types(dtype, o_dtype, [&](auto t, auto o) {
-    hipLaunchKernelGGL((k_mm_any<decltype(t), decltype(o), MODE>), grid, dim3(256), 0, st, s);
-  });
-  return launched("grouped_matmul");
-}
-
 bool rows16(const void* p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
 
-// The tiled kernel serves rows of whole 16-byte pieces.
-bool tiled(const MmArgs& s, int mode, int o_dtype) {
-  return s.N % 8 == 0 && s.K % 8 == 0 && rows16(s.a, s.lda) &&
-         rows16(s.b, mode == kDw ? s.ldb : s.K) && rows16(s.y, mode == kDw ? s.K : s.ldy);
+// Up to this many rows per expert on average the forward product is bound by
+// the weights' bytes (64 experts of 1536 x 2048, us by the few-rows and the
+// tiled kernel: 32 rows 111 and 128, 64 rows 148 and 131); so it is with up to
+// 128 rows while there are few 256 x 256 tiles (one expert of 4096 x 4096, 128
+// rows: 31 and 42).
+constexpr int kFewMean = 48, kFewMeanSmall = 128, kFewTiles = 64;
+
+bool few(const MmArgs& s) {
+  const long long tiles = (long long)((s.N + kTile - 1) / kTile) * s.E * ((s.R / s.E + kTile - 1) / kTile);
+  return s.R <= (long long)(tiles <= kFewTiles ? kFewMeanSmall : kFewMean) * s.E &&
+         max_tiles(s.R, s.E, kFewRows) <= 65535;
 }
 
-// Up to this many rows per expert on average the forward product is bound by
-// the weights' bytes.
-constexpr int kFewMean = 32;
+// What of the operands the tiled kernel cannot read in place: rows that are
+// not whole 16-byte pieces, along the contraction or across it.
+struct Pad {
+  bool a, b;
+  size_t a_bytes, b_bytes;
+};
+Pad pad_of(const MmArgs& s, int mode, int64_t a_rows) {
+  Pad p{};
+  if (mode == kFwd && few(s)) return p;
+  const int ac = mode == kFwd ? s.K : s.N, bc = s.K;
+  const int64_t b_rows = mode == kDw ? s.x_rows : (int64_t)s.E * s.N * (s.act ? 2 : 1);
+  p.a = ac % 8 != 0 || !rows16(s.a, s.lda);
+  p.b = bc % 8 != 0 || !rows16(s.b, s.ldb);
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  p.a_bytes = p.a ? al((size_t)a_rows * ((ac + 7) / 8) * 16) : 0;
+  p.b_bytes = p.b ? al((size_t)b_rows * ((bc + 7) / 8) * 16) : 0;
+  return p;
+}
+
+int pad_rows(const void*& src, int64_t& ld, int64_t rows, int cols, void* dst, hipStream_t st) {
+  const int64_t pieces = rows * ((cols + 7) / 8);
+  if (pieces) {
+    const int64_t blocks = (pieces + 255) / 256;
+    hipLaunchKernelGGL(k_mm_pad, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, st,
+                       (const uint16_t*)src, ld, rows, cols, (uint4*)dst);
+  }
+  src = dst;
+  ld = (cols + 7) / 8 * 8;
+  return launched("grouped_matmul rows");
+}
 
 template <int MODE>
-int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
-  if (!tiled(s, MODE, o_dtype)) return launch_any<MODE>(s, dtype, o_dtype, st);
+int launch_mm(MmArgs s, int dtype, int o_dtype, int64_t a_rows, void* ws, size_t ws_bytes,
+              hipStream_t st) {
+  s.y16 = rows16(s.y, s.ldy);
+  const Pad p = pad_of(s, MODE, a_rows);
+  if (p.a_bytes + p.b_bytes > ws_bytes || (p.a_bytes + p.b_bytes && !ws))
+    return fail(BITSMOE_ENOSPC, "ws_bytes=%zu < %zu (operands that are not 16-byte rows)", ws_bytes,
+                p.a_bytes + p.b_bytes);
+  if (p.a_bytes + p.b_bytes && ((uintptr_t)ws & 255u))
+    return fail(BITSMOE_EINVAL, "misaligned workspace (256 bytes)");
+  const int cols = MODE == kFwd ? s.N : s.K, per = s.act ? kTile / 2 : kTile;
+  const long long ntn = (cols + per - 1) / per;
+  const long long mt =
+      MODE == kDw ? (long long)s.E * ((s.N + kTile - 1) / kTile) : max_tiles(s.R, s.E, kTile);
+  if (mt * ntn > 0x1FFFFFFFll)
+    return fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", s.R, s.E, s.N, s.K);
   int rc = BITSMOE_OK;
+  if (p.a &&
+      (rc = pad_rows(s.a, s.lda, a_rows, MODE == kFwd ? s.K : s.N, ws, st)))
+    return rc;
+  if (p.b && (rc = pad_rows(s.b, s.ldb,
+                            MODE == kDw ? s.x_rows : (int64_t)s.E * s.N * (s.act ? 2 : 1), s.K,
+                            (uint8_t*)ws + p.a_bytes, st)))
+    return rc;
   with_types(dtype, o_dtype, [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
     if constexpr (MODE == kFwd) {
-      const long long tiles = max_tiles(s.R, s.E, kFewRows);
-      if (s.R <= (long long)kFewMean * s.E && tiles <= 65535) {
-        const int per = s.act ? kFewCols / 2 : kFewCols;
-        const dim3 grid((unsigned)((s.N + per - 1) / per), (unsigned)tiles);
+      if (few(s)) {
+        const int fp = s.act ? kFewCols / 2 : kFewCols;
+        const dim3 grid((unsigned)((s.N + fp - 1) / fp), (unsigned)max_tiles(s.R, s.E, kFewRows));
         if (s.act)
           hipLaunchKernelGGL((k_mm_few<T, O, true>), grid, dim3(64 * kFewWaves), 0, st, s);
         else
           hipLaunchKernelGGL((k_mm_few<T, O, false>), grid, dim3(64 * kFewWaves), 0, st, s);
-        rc = launched("grouped_matmul");
         return;
       }
-    }
-    const int cols = MODE == kFwd ? s.N : s.K, per = s.act ? kTile / 2 : kTile;
-    const long long ntn = (cols + per - 1) / per;
-    const long long mt =
-        MODE == kDw ? (long long)s.E * ((s.N + kTile - 1) / kTile) : max_tiles(s.R, s.E, kTile);
-    if (mt * ntn > 0x1FFFFFFFll) {
-      rc = fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", s.R, s.E, s.N, s.K);
-      return;
     }
     // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
     const long long cut = mt * ntn < kSplitMost ? mt * ntn : kSplitMost;
@@ -791,9 +763,8 @@ int launch_mm(const MmArgs& s, int dtype, int o_dtype, hipStream_t st) {
       hipLaunchKernelGGL((k_mm_tile<T, O, MODE, MODE == kFwd>), grid, dim3(512), 0, st, s);
     else
       hipLaunchKernelGGL((k_mm_tile<T, O, MODE, false>), grid, dim3(512), 0, st, s);
-    rc = launched("grouped_matmul");
   });
-  return rc;
+  return launched("grouped_matmul");
 }
 
 }  // namespace
@@ -805,10 +776,25 @@ using namespace bitsmoe::experts;
 
 extern "C" {
 
+int bitsmoe_grouped_matmul_workspace_size(int op, const void* a, int64_t lda, int64_t a_rows,
+                                          const void* b, int64_t ldb, int64_t b_rows, int R, int E,
+                                          int N, int K, int act, size_t* bytes) {
+  if (!bytes) return fail(BITSMOE_EINVAL, "bytes is null");
+  if (op < BITSMOE_GROUPED_FORWARD || op > BITSMOE_GROUPED_DW) return fail(BITSMOE_EINVAL, "op=%d", op);
+  if (R < 0 || E < 1 || N < 1 || K < 1 || a_rows < 0 || b_rows < 0 || b_rows > 0x7FFFFFFFll)
+    return fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d", R, E, N, K);
+  MmArgs s{};
+  s.a = a, s.lda = lda, s.b = b, s.ldb = op == BITSMOE_GROUPED_DW ? ldb : K;
+  s.x_rows = (int)b_rows, s.R = R, s.E = E, s.N = N, s.K = K, s.act = act;
+  const Pad p = pad_of(s, op, a_rows);
+  *bytes = p.a_bytes + p.b_bytes;
+  return BITSMOE_OK;
+}
+
 int bitsmoe_grouped_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const int32_t* rows,
                            int div, const void* w, const int32_t* bounds, int R, int E, int N,
-                           int K, int act, void* y, int y_dtype, int64_t ldy,
-                           bitsmoe_stream_t stream) {
+                           int K, int act, void* y, int y_dtype, int64_t ldy, void* ws,
+                           size_t ws_bytes, bitsmoe_stream_t stream) {
   int st = mm_check(dtype, y_dtype, R, E, N, K, bounds);
   if (st || (st = rows_check(rows, div, x_rows, R))) return st;
   if (act != BITSMOE_ACT_NONE && act != BITSMOE_ACT_SILU_MUL)
@@ -816,32 +802,33 @@ int bitsmoe_grouped_matmul(int dtype, const void* x, int64_t ldx, int x_rows, co
   if (ldx < K || ldy < N) return fail(BITSMOE_ESHAPE, "a row stride is too small");
   if (R == 0) return BITSMOE_OK;
   if (!w || !y || (x_rows && !x)) return fail(BITSMOE_EINVAL, "null pointer argument");
-  MmArgs s{x, ldx, w, 0, rows, div, x_rows, bounds, R, E, N, K, y, ldy, act};
-  return launch_mm<kFwd>(s, dtype, y_dtype, (hipStream_t)stream);
+  const MmArgs s{x, ldx, w, K, rows, div, x_rows, bounds, R, E, N, K, y, ldy, act, 0};
+  return launch_mm<kFwd>(s, dtype, y_dtype, x_rows, ws, ws_bytes, (hipStream_t)stream);
 }
 
 int bitsmoe_grouped_matmul_dx(int dtype, const void* dy, int64_t lddy, const void* w,
                               const int32_t* bounds, int R, int E, int N, int K, void* dx,
-                              int dx_dtype, int64_t lddx, bitsmoe_stream_t stream) {
+                              int dx_dtype, int64_t lddx, void* ws, size_t ws_bytes,
+                              bitsmoe_stream_t stream) {
   const int st = mm_check(dtype, dx_dtype, R, E, N, K, bounds);
   if (st) return st;
   if (lddy < N || lddx < K) return fail(BITSMOE_ESHAPE, "a row stride is too small");
   if (R == 0) return BITSMOE_OK;
   if (!dy || !w || !dx) return fail(BITSMOE_EINVAL, "null pointer argument");
-  MmArgs s{dy, lddy, w, 0, nullptr, 1, R, bounds, R, E, N, K, dx, lddx, 0};
-  return launch_mm<kDx>(s, dtype, dx_dtype, (hipStream_t)stream);
+  const MmArgs s{dy, lddy, w, K, nullptr, 1, R, bounds, R, E, N, K, dx, lddx, 0, 0};
+  return launch_mm<kDx>(s, dtype, dx_dtype, R, ws, ws_bytes, (hipStream_t)stream);
 }
 
 int bitsmoe_grouped_matmul_dw(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                               int x_rows, const int32_t* rows, int div, const int32_t* bounds,
-                              int R, int E, int N, int K, void* dw, int dw_dtype,
-                              bitsmoe_stream_t stream) {
+                              int R, int E, int N, int K, void* dw, int dw_dtype, void* ws,
+                              size_t ws_bytes, bitsmoe_stream_t stream) {
   int st = mm_check(dtype, dw_dtype, R, E, N, K, bounds);
   if (st || (st = rows_check(rows, div, x_rows, R))) return st;
   if (lddy < N || ldx < K) return fail(BITSMOE_ESHAPE, "a row stride is too small");
   if (!dw || (R && (!dy || (x_rows && !x)))) return fail(BITSMOE_EINVAL, "null pointer argument");
-  MmArgs s{dy, lddy, x, ldx, rows, div, x_rows, bounds, R, E, N, K, dw, 0, 0};
-  return launch_mm<kDw>(s, dtype, dw_dtype, (hipStream_t)stream);
+  const MmArgs s{dy, lddy, x, ldx, rows, div, x_rows, bounds, R, E, N, K, dw, K, 0, 0};
+  return launch_mm<kDw>(s, dtype, dw_dtype, R, ws, ws_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

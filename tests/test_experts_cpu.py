@@ -39,21 +39,21 @@ def group(**kw):
 
 def matmul(**kw):
     a = dict(dtype=F16, x=P, ldx=64, x_rows=10, rows=None, div=1, w=P, bounds=P, R=10, E=4, N=32,
-             K=64, act=0, y=P, y_dtype=F16, ldy=32)
+             K=64, act=0, y=P, y_dtype=F16, ldy=32, ws=None, ws_bytes=0)
     a.update(kw)
     return _status("grouped_matmul", *a.values(), None)
 
 
 def matmul_dx(**kw):
     a = dict(dtype=F16, dy=P, lddy=32, w=P, bounds=P, R=10, E=4, N=32, K=64, dx=P, dx_dtype=F16,
-             lddx=64)
+             lddx=64, ws=None, ws_bytes=0)
     a.update(kw)
     return _status("grouped_matmul_dx", *a.values(), None)
 
 
 def matmul_dw(**kw):
     a = dict(dtype=F16, dy=P, lddy=32, x=P, ldx=64, x_rows=10, rows=None, div=1, bounds=P, R=10,
-             E=4, N=32, K=64, dw=P, dw_dtype=F32)
+             E=4, N=32, K=64, dw=P, dw_dtype=F32, ws=None, ws_bytes=0)
     a.update(kw)
     return _status("grouped_matmul_dw", *a.values(), None)
 
@@ -125,6 +125,12 @@ def w4(**kw):
     (matmul_dw, dict(ldx=63), bm.ESHAPE), (matmul_dw, dict(dw=None), bm.EINVAL),
     (matmul_dw, dict(x=None), bm.EINVAL), (matmul_dw, dict(x_rows=9), bm.ESHAPE),
     (matmul_dw, dict(R=0, dw=None), bm.EINVAL),
+    # operands that are not 16-byte rows, without (enough of) a workspace
+    (matmul, dict(R=4000, x_rows=4000, ldx=65), bm.ENOSPC), (matmul, dict(R=4000, x_rows=4000, x=P + 2), bm.ENOSPC),
+    (matmul_dx, dict(N=33, lddy=40), bm.ENOSPC), (matmul_dx, dict(K=63), bm.ENOSPC),
+    (matmul_dx, dict(N=33, lddy=40, ws=P, ws_bytes=100), bm.ENOSPC),
+    (matmul_dx, dict(N=33, lddy=40, ws=P + 16, ws_bytes=1 << 20), bm.EINVAL),
+    (matmul_dw, dict(K=63), bm.ENOSPC), (matmul_dw, dict(dy=P + 4), bm.ENOSPC),
     (act, dict(dtype=F32), bm.EINVAL), (act, dict(F=0), bm.ESHAPE), (act, dict(lda=63), bm.ESHAPE),
     (act, dict(ldh=31), bm.ESHAPE), (act, dict(bounds=P), bm.ESHAPE), (act, dict(h=None), bm.EINVAL),
     (act_grad, dict(ldda=63), bm.ESHAPE), (act_grad, dict(da=None), bm.EINVAL),
@@ -165,6 +171,24 @@ def test_group_workspace():
     out = ctypes.c_size_t()
     assert bm._lib.bitsmoe_moe_group_workspace_size(8, 0, ctypes.byref(out)) == bm.ESHAPE
     assert bm._lib.bitsmoe_moe_group_workspace_size(8, 4, None) == bm.EINVAL
+
+
+def test_matmul_workspace():
+    size = ctypes.c_size_t(7)
+
+    def need(op, a=P, lda=64, a_rows=10, b=P, ldb=64, b_rows=10, R=10, E=4, N=32, K=64, act=0):
+        assert _status("grouped_matmul_workspace_size", op, a, lda, a_rows, b, ldb, b_rows, R, E, N,
+                       K, act, ctypes.byref(size)) == bm.OK
+        return size.value
+    assert need(0) == need(1, lda=32) == need(2, lda=32) == 0
+    assert need(0, K=63, lda=63) == 0              # few rows: read in place
+    assert need(0, K=63, lda=63, R=4000, a_rows=4000) == 4000 * 128 + 4 * 32 * 128
+    assert need(1, lda=33, N=33) == 10 * 80 // 256 * 256 + 256      # dy alone
+    assert need(2, ldb=65) == 10 * 128 // 256 * 256                 # x alone
+    assert _status("grouped_matmul_workspace_size", 3, P, 64, 1, P, 64, 1, 1, 1, 8, 8, 0,
+                   ctypes.byref(size)) == bm.EINVAL
+    assert _status("grouped_matmul_workspace_size", 0, P, 64, 1, P, 64, 1, 1, 1, 8, 8, 0,
+                   None) == bm.EINVAL
 
 
 def test_binding_refuses_host_tensors_and_wrong_layouts():
