@@ -174,7 +174,12 @@ inline long long max_tiles(long long R, long long E, long long BM) {
   return R / BM + (R < E ? R : E);
 }
 
-inline int elem_bytes(int dtype) { return dtype == BITSMOE_F32 ? 4 : 2; }
+// Whether counts of tiles stay within 32 bits whatever the bounds hold (each
+// expert's rows are clamped to R, but wrong bounds may give every expert R).
+inline bool countable(long long R, long long E, long long BM) {
+  return E * ((R + BM - 1) / BM) < 0x40000000ll;
+}
+
 inline bool is_half(int dtype) { return dtype == BITSMOE_F16 || dtype == BITSMOE_BF16; }
 
 inline int launched(const char* what) {

@@ -535,7 +535,7 @@ __device__ __forceinline__ V few_load(const T* p, int left) {
 template <class T, class O, bool ACT, int MB>
 __device__ __forceinline__ void few_rows(const MmArgs& s, const Tile& t, float* lds) {
   typedef typename Vec8<T>::type V;
-  constexpr int U = MB == 1 ? 4 : 2;  // turns whose loads are in flight together
+  constexpr int U = MB == 1 ? 4 : MB == 2 ? 2 : 1;  // turns whose loads are in flight together
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * (ACT ? kFewCols / 2 : kFewCols);
@@ -662,12 +662,14 @@ int mm_check(int dtype, int o_dtype, int R, int E, int N, int K, const int32_t* 
   if (R < 0 || R > (1 << 26) || E < 1 || E > 65535 || N < 1 || K < 1 || N > (1 << 20) ||
       K > (1 << 20))
     return fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d", R, E, N, K);
+  if (!countable(R, E, kFewRows)) return fail(BITSMOE_ESHAPE, "R=%d with E=%d", R, E);
   if (!bounds) return fail(BITSMOE_EINVAL, "bounds is null");
   return BITSMOE_OK;
 }
 
 int rows_check(const int32_t* rows, int div, int x_rows, int R) {
-  if (rows ? (div < 1 || x_rows < 0) : x_rows < R)
+  // (with rows: a row of x that a wrong index may be clamped to)
+  if (rows ? (div < 1 || x_rows < (R > 0)) : x_rows < R)
     return fail(BITSMOE_ESHAPE, "div=%d, %d rows of x for R=%d", div, x_rows, R);
   return BITSMOE_OK;
 }

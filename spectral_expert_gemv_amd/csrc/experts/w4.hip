@@ -574,7 +574,7 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   if (!bounds && E != 1) return fail(BITSMOE_EINVAL, "E=%d without bounds", E);
   if (act != BITSMOE_ACT_NONE && act != BITSMOE_ACT_SILU_MUL)
     return fail(BITSMOE_EINVAL, "act=%d", act);
-  if (rows ? (div < 1 || x_rows < 0) : x_rows < R)
+  if (rows ? (div < 1 || x_rows < (R > 0)) : x_rows < R)
     return fail(BITSMOE_ESHAPE, "div=%d, %d rows of x for R=%d", div, x_rows, R);
   if (ldx < K || ldy < N) return fail(BITSMOE_ESHAPE, "a row stride is too small");
   if (R == 0) return BITSMOE_OK;
@@ -587,6 +587,7 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   const bool wide = ((uintptr_t)x & 15u) == 0 && ldx % 8 == 0;
   const bool few = R <= (long long)kFewRows * E;
   const int rows_tile = !wide ? 1 : few ? kFewRows : kRows;
+  if (!countable(R, E, rows_tile)) return fail(BITSMOE_ESHAPE, "R=%d with E=%d", R, E);
   const long long tiles =
       bounds ? max_tiles(R, E, rows_tile) : ((long long)R + rows_tile - 1) / rows_tile;
   if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);

@@ -116,6 +116,9 @@ def w4(**kw):
     (matmul, dict(w=None), bm.EINVAL), (matmul, dict(x=None), bm.EINVAL),
     (matmul, dict(y=None), bm.EINVAL), (matmul, dict(ldx=63), bm.ESHAPE),
     (matmul, dict(ldy=31), bm.ESHAPE), (matmul, dict(act=2), bm.EINVAL),
+    (matmul, dict(rows=P, x_rows=0), bm.ESHAPE), (matmul_dw, dict(rows=P, x_rows=0), bm.ESHAPE),
+    (w4, dict(rows=P, x_rows=0), bm.ESHAPE), (matmul, dict(E=65535, R=1 << 26, x_rows=1 << 26), bm.ESHAPE),
+    (w4, dict(E=65535, R=1 << 24, x_rows=1 << 24), bm.ESHAPE),
     (matmul, dict(x_rows=9), bm.ESHAPE), (matmul, dict(rows=P, div=0), bm.ESHAPE),
     (matmul, dict(rows=P, x_rows=-1), bm.ESHAPE), (matmul, dict(K=(1 << 20) + 1, ldx=1 << 21), bm.ESHAPE),
     (matmul_dx, dict(dtype=F32), bm.EINVAL), (matmul_dx, dict(dx_dtype=BF16), bm.EINVAL),

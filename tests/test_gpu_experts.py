@@ -575,6 +575,54 @@ def test_a_layer_and_its_gradients(bm, T, E, k, D, F, dtype):
         assert err < tol, (name, err, tol)
 
 
+@pytest.mark.parametrize("T, E, k, D, F", [(1, 8, 2, 64, 96), (50, 16, 4, 256, 128), (300, 4, 2, 128, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_expert_layer(bm, T, E, k, D, F, dtype, on_stream):
+    """The layer's own forward passes (dense and 4-bit) and gradients."""
+    from spectral_expert_gemv_amd import ExpertLayer
+    _say("ExpertLayer", T, E, k, D, F, dtype, on_stream)
+    logits, x, w1, w2, dout = layer_inputs(T, E, k, D, F, dtype, 17)
+    dout = dout.to(dtype)
+    stream = torch.cuda.Stream() if on_stream else None
+    torch.cuda.synchronize()
+    layer = ExpertLayer(w1, w2)
+    out = layer.forward(x, logits, k, stream=stream)
+    got = layer.gradients(x, logits, k, dout, stream=stream)
+    packed = ExpertLayer.w4(w1.float().cpu().numpy(), w2.float().cpu().numpy(), group=32)
+    q = packed.forward(x, logits, k, torch.empty(T, D, dtype=F32, device="cuda"), stream=stream)
+    torch.cuda.synchronize()
+
+    def plain(v1, v2):
+        p = torch.softmax(logits.double(), 1)
+        top = torch.topk(logits, k, 1).indices
+        g = p.gather(1, top)
+        gate = torch.zeros_like(p).scatter(1, top, g / g.sum(1, keepdim=True))
+        o = 0
+        for e in range(E):
+            a = x.double() @ v1[e].double().t()
+            h = torch.nn.functional.silu(a[:, :F]) * a[:, F:]
+            o = o + gate[:, e:e + 1] * (h @ v2[e].double().t())
+        return o
+
+    def deq(w):
+        codes, s, m = w
+        c = torch.stack([codes & 15, codes >> 4], -1).reshape(codes.shape[0], codes.shape[1], -1).double()
+        return c * s.double().repeat_interleave(32, 2) + m.double().repeat_interleave(32, 2)
+
+    # the longest way has h, y and out rounded: 3 half steps, doubled as before
+    tol = 6 * torch.finfo(dtype).eps / 2
+    for o, want in ((out, plain(w1, w2)), (got[0], plain(w1, w2)), (q, plain(deq(packed.w1), deq(packed.w2)))):
+        assert float((o.double() - want).norm() / want.norm()) < tol
+    ref = layer_step(bm, logits, x, w1, w2, dout, k)
+    for a, b in ((got[2], ref[4]), (got[3], ref[2]), (got[4], ref[3])):
+        assert torch.equal(a, b)
+    # dx is rounded to the rows' type here, to float32 there
+    assert float((got[1].double() - ref[1].double()).norm() / ref[1].double().norm()) < tol
+    with pytest.raises(ValueError, match="gradients"):
+        packed.gradients(x, logits, k, dout)
+
+
 def test_streams_graphs_and_repeats(bm):
     """The same bits eagerly, again, on another stream and from a replayed
     graph with eager work between the replays."""
