@@ -6,6 +6,7 @@ streams); host buffers are numpy arrays.  There is no fallback: if the
 library is missing, importing this module raises.
 """
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -428,9 +429,9 @@ def _matrix(name, t, shape=None):
     return t.data_ptr(), max(step, have[1]) if have[0] <= 1 else step
 
 
-def _array(name, t, dtype, shape):
-    """Pointer of a contiguous tensor of that dtype and shape."""
-    if t.dtype != dtype or t.shape != shape:
+def _array(name, t, dtype, shape=None):
+    """Pointer of a contiguous tensor of that dtype (and shape)."""
+    if t.dtype is not dtype or (shape is not None and t.shape != shape):
         raise ValueError("%s must be %s of shape %s, got %s of %s" % (name, dtype, shape, t.dtype,
                                                                       tuple(t.shape)))
     if not t.is_contiguous():
@@ -480,6 +481,7 @@ def _scratch(nbytes, dev, stream):
     return _new(nbytes, torch.uint8, dev, stream) if nbytes else None
 
 
+@functools.lru_cache(maxsize=256)
 def moe_group_workspace_size(P, E):
     out = ctypes.c_size_t(0)
     _check(_lib.bitsmoe_moe_group_workspace_size(P, E, ctypes.byref(out)))
@@ -596,7 +598,7 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, ws=None, st
     if y is None:
         y = _new((R, N), x.dtype, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
-    pw, code = _array("w", w, x.dtype, (E, n2, K)), ACT[act]
+    pw, code = _array("w", w, x.dtype), ACT[act]
     ws = _matmul_scratch(0, px, ldx, x.shape[0], pw, K, 0, R, E, N, K, code, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div, pw,
              _bounds(bounds, E), R, E, N, K, code, py, _dtype(y), ldy, _ptr(ws),
@@ -614,7 +616,7 @@ def grouped_matmul_dx(dy, w, bounds, dx=None, ws=None, stream=None):
     if dx is None:
         dx = _new((R, K), dy.dtype, dev, stream)
     px, ldx = _matrix("dx", dx, (R, K))
-    pw = _array("w", w, dy.dtype, (E, N, K))
+    pw = _array("w", w, dy.dtype)
     ws = _matmul_scratch(1, pd, ldd, R, pw, K, 0, R, E, N, K, 0, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul_dx, dev, stream, _dtype(dy), pd, ldd, pw,
              _bounds(bounds, E), R, E, N, K, px, _dtype(dx), ldx, _ptr(ws),
@@ -762,7 +764,7 @@ def w4_matmul(x, codes, scales, mins=None, y=None, bounds=None, rows=None, div=1
         y = _new((R, N), x.dtype, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
     _enqueue(_lib.bitsmoe_w4_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div,
-             _array("codes", codes, torch.uint8, (E, n2, half)),
+             _array("codes", codes, torch.uint8),
              _array("scales", scales, torch.float16, (E, n2, groups)),
              None if mins is None else _array("mins", mins, torch.float16, (E, n2, groups)),
              K // groups, None if bounds is None else _bounds(bounds, E), R, E, N, K, ACT[act], py,
