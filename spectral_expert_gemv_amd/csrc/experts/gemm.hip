@@ -68,7 +68,9 @@ __global__ __launch_bounds__(256) void k_mm_pad(const uint16_t* __restrict__ src
 // Work-group tile of TM output rows x TN output columns, WM x WN waves, the
 // contraction in steps of 64 (whole 128-byte lines of a row).  Every step's two operand tiles are copied
 // straight into LDS by 16-byte loads (no registers in between) into one of
-// two buffers, a step ahead of the products.
+// kBufs buffers, kBufs - 1 steps ahead of the products: 2 of the 256 x 256
+// tile's 64 KB, 4 of the 128 x 128 tile's 32 KB, whose steps are too short to
+// hide one copy's latency.
 //
 // An operand whose rows run along the contraction lies in LDS as
 // [row][64 elements]: 16-byte piece p of row r at place p ^ (r / 2 % 8), so
@@ -192,7 +194,7 @@ constexpr uint32_t kLds = 2 * 2 * kTile * kStep * 2;  // two buffers of two oper
 
 // Output rows m0 .. m0 + mn and columns n0 .. n0 + nn of expert e, with the
 // contraction c0 .. c0 + cn.
-template <class T, class O, int MODE, int TM, int TN, int WM, int WN, bool ACT>
+template <class T, class O, int MODE, int TM, int TN, int WM, int WN, int kBufs, bool ACT>
 __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, int m0, int mn,
                                         int n0, int nn, int c0, int cn) {
   constexpr int NT = 64 * WM * WN;
@@ -201,6 +203,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   typedef Operand<TM, kTrA, NT> OpA;
   typedef Operand<TN, kTrB, NT> OpB;
   constexpr uint32_t kBuf = OpA::kBytes + OpB::kBytes;
+  static_assert(kBufs * kBuf <= kLds, "buffers");
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // addresses of the pieces of step 0
@@ -267,8 +270,9 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
     if (i < OpA::kCopies) {
       const uint8_t* p = a.ptr[i];
       if (!whole && c + (kTrA ? OpA::line(i) : 8 * OpA::piece(i)) >= cn) p = (const uint8_t*)g_pad;
-      // (rows past the tile's are not copied: nobody uses what lies there)
-      if (kTrA || whole || i * (NT / 8) < mn) copy16(p, OpA::dest(buf, wv, i));
+      // (rows past the tile's need not be copied: nobody uses what lies there;
+      // with more than two buffers the copies in flight are counted, though)
+      if (kTrA || whole || kBufs > 2 || i * (NT / 8) < mn) copy16(p, OpA::dest(buf, wv, i));
       if (kTrA)
         a.ptr[i] += (int64_t)kStep * lda;
       else
@@ -310,18 +314,19 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
       if (j * 2 / NI == part) fb[half][j] = OpB::template frag<T>(at, j, half);
   };
   uint32_t cur = base, at_a = base + off_a, at_b = base + off_b;
+  auto after = [&](uint32_t b) { return b == base + (kBufs - 1) * kBuf ? base : b + kBuf; };
   // kind 0: the step copied meanwhile is whole; 1: it may not be; 2: there is
   // no next step
   auto step = [&](int c, auto kind_) {
     constexpr int kKind = decltype(kind_)::value;
     constexpr bool kLast = kKind == 2;
-    const uint32_t nxt = cur == base ? base + kBuf : base;
+    const uint32_t nxt = after(cur);
     uint32_t next_a = nxt + off_a, next_b = nxt + off_b;
     asm("" : "+v"(next_a), "+v"(next_b));  // one register and immediate offsets each
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       if (!kLast && g == kSwitch) {
-        wait_copies<0>();
+        wait_copies<(kBufs - 2) * kPieces>();
         lds_barrier();
       }
       if (!kLast || g + kAhead < kGroups) {
@@ -335,7 +340,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
           if (i * kAhead / kPieces == g - kSwitch)
-            stage_piece(i, c + 2 * kStep, kKind == 0, cur);
+            stage_piece(i, c + kBufs * kStep, kKind == 0, cur);
       }
 #pragma unroll
       for (int j = 0; j < NI; ++j)
@@ -347,11 +352,11 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   if (cn > 0) {
     const bool full = kTrA || mn > TM - NT / 8;  // every copy has rows
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kBufs; ++i)
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) stage_piece(j, i * kStep, false, base + i * kBuf);
-    if (full)
-      wait_copies<kPieces>();  // the first step's
+    if (full || kBufs > 2)
+      wait_copies<(kBufs - 1) * kPieces>();  // the first step's
     else
       wait_copies<0>();
     lds_barrier();
@@ -364,18 +369,18 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
       read_a(1, at_a);
       read_a(2, at_a);
       if (full)
-        for (; c + 3 * kStep <= cn; c += kStep) step(c, integral_constant<int, 0>{});
+        for (; c + (kBufs + 1) * kStep <= cn; c += kStep) step(c, integral_constant<int, 0>{});
 #pragma unroll 1
       for (; c + kStep < cn; c += kStep) step(c, integral_constant<int, 1>{});
       step(c, integral_constant<int, 2>{});
     } else {  // a wave past the tile's rows only copies
 #pragma unroll 1
       for (; c + kStep < cn; c += kStep) {
-        wait_copies<0>();
+        wait_copies<(kBufs - 2) * kPieces>();
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) stage_piece(i, c + 2 * kStep, false, cur);
-        cur = cur == base ? base + kBuf : base;
+        for (int i = 0; i < kPieces; ++i) stage_piece(i, c + kBufs * kStep, false, cur);
+        cur = after(cur);
       }
     }
     wait_copies<0>();  // nothing is written into this work-group's LDS after its end
@@ -493,12 +498,12 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   }
   int n0 = ni * kCols, nn = min(kCols, cols - n0);
   if (part < 0) {
-    mm_tile<T, O, MODE, kTile, kTile, 2, 4, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
+    mm_tile<T, O, MODE, kTile, kTile, 2, 4, 2, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
   } else {
     const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
     mn = min(kTile / 2, mn - pm), nn = min(kCols / 2, nn - pn);
     if (mn <= 0 || nn <= 0) return;
-    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
+    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, 4, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
                                                                 nn, c0, cn);
   }
 }
