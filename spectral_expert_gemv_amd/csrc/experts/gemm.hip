@@ -681,12 +681,13 @@ int rows_check(const int32_t* rows, int div, int x_rows, int R) {
 
 bool rows16(const void* p, int64_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0; }
 
-// Up to this many rows per expert on average the forward product is bound by
-// the weights' bytes (64 experts of 1536 x 2048, us by the few-rows and the
-// tiled kernel: 32 rows 111 and 128, 64 rows 148 and 131); so it is with up to
-// 128 rows while there are few 256 x 256 tiles (one expert of 4096 x 4096, 128
-// rows: 31 and 42).
-constexpr int kFewMean = 48, kFewMeanSmall = 128, kFewTiles = 64;
+// Up to kFewMean rows per expert on average the few-rows kernel is the faster
+// one (us by it and by the tiled one: 64 experts of 1536 x 2048, 16 rows 97 and
+// 109, 32 rows 112 and 111, 64 rows 149 and 116; 8 experts of 4096 x 4096, 16
+// rows 70 and 57), and up to kFewMeanSmall while there are few 256 x 256 tiles
+// to spread over the chip (one expert of 4096 x 4096: 32 rows 21 and 27, 64
+// rows 32 and 27).
+constexpr int kFewMean = 12, kFewMeanSmall = 32, kFewTiles = 32;
 
 bool few(const MmArgs& s) {
   const long long tiles = (long long)((s.N + kTile - 1) / kTile) * s.E * ((s.R / s.E + kTile - 1) / kTile);
