@@ -392,13 +392,14 @@ constexpr int kEnoughGroups = 4096;
 constexpr int kVecInputs = 16384;  // rows x inputs of x that the LDS holds
 constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kMostTurns * kVecRows * 4;
 
-template <class T, class O, bool ACT, int M>
+template <class T, class O, bool ACT, int M, bool kWide>
 __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* lds) {
   typedef Magic<T> Mg;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int log_lanes = s.K <= 256 ? 3 : s.K <= 512 ? 4 : s.K <= 1024 ? 5 : 6;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int log_lanes = kWide ? 6 : s.K <= 256 ? 3 : s.K <= 512 ? 4 : 5;
   const int lanes = 1 << log_lanes, sub = 64 >> log_lanes;  // lanes per row, rows per load
-  const int at = lane & (lanes - 1), which = lane >> log_lanes;
+  // (kWide: a load's row is the wave's, and its address a scalar)
+  const int at = kWide ? lane : lane & (lanes - 1), which = kWide ? 0 : lane >> log_lanes;
   const int chunks = (s.K + 32 * lanes - 1) >> (5 + log_lanes);
   constexpr int kN = ACT ? kOuts / 2 : kOuts;
   const int outs = kOuts * s.turns;
@@ -542,10 +543,15 @@ __global__ __launch_bounds__(64 * kWaves, 3) void k_w4_few(W4Args s) {
   if (t.n <= 0) return;
   // (x of the tile in LDS, in whole turns of 64 lanes x 32 inputs)
   const bool vec = t.n <= kVecRows && t.n * ((s.K + 2047) & ~2047) <= kVecInputs;
-  if (vec && t.n == 1)
-    w4_vec<T, O, ACT, 1>(s, t, lds);
+  const bool wide = s.K > 1024;
+  if (vec && t.n == 1 && wide)
+    w4_vec<T, O, ACT, 1, true>(s, t, lds);
+  else if (vec && t.n == 1)
+    w4_vec<T, O, ACT, 1, false>(s, t, lds);
+  else if (vec && wide)
+    w4_vec<T, O, ACT, 2, true>(s, t, lds);
   else if (vec)
-    w4_vec<T, O, ACT, 2>(s, t, lds);
+    w4_vec<T, O, ACT, 2, false>(s, t, lds);
   else
     w4_rows<T, O, G, ACT, 1, 1>(s, t, (float*)lds);
 }
