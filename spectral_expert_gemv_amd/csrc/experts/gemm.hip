@@ -493,6 +493,7 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
     cn = hi - c0;
   } else {
     const Tile t = find_tile(s.bounds, s.E, s.R, mi, kTile);
+    if (t.n <= 0) return;
     e = t.e, m0 = t.row0, mn = t.n;
     c0 = 0, cn = MODE == kFwd ? s.K : s.N;
   }

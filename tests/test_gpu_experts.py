@@ -664,3 +664,114 @@ def test_an_explicit_stream(bm):
         y2 = bm.grouped_matmul(x, w1, b2, rows=o2, div=8, act="silu_mul", stream=stream)
         side.synchronize()
         assert torch.equal(i2, ids) and torch.equal(o2, o) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("T", [0, 1, 9])
+def test_batches_of_padding(bm, T):
+    """No token at all, and tokens without any expert."""
+    from spectral_expert_gemv_amd import ExpertLayer
+    _, x, w1, w2, dout = layer_inputs(max(T, 1), 8, 2, 64, 96, BF16, 3)
+    x, dout = x[:T], dout[:T].to(BF16)
+    logits = torch.full((T, 8), -float("inf"), device="cuda")
+    layer = ExpertLayer(w1, w2)
+    assert layer.forward(x, logits, 2).tolist() == [[0.0] * 64] * T
+    out, dx, dl, dw1, dw2 = layer.gradients(x, logits, 2, dout)
+    for t, shape in ((out, (T, 64)), (dx, (T, 64)), (dl, (T, 8)), (dw1, w1.shape), (dw2, w2.shape)):
+        assert t.shape == shape and not bool(t.any())
+    q = ExpertLayer.w4(w1.float().cpu().numpy(), w2.float().cpu().numpy(), group=32)
+    assert not bool(q.forward(x, logits, 2).any())
+
+
+def test_two_streams_at_once(bm):
+    """Calls of different sizes and data, interleaved on two streams."""
+    jobs = []
+    for i, (T, E, k) in enumerate([(300, 16, 4), (700, 16, 4)]):
+        args = layer_inputs(T, E, k, 256, 128, BF16, 40 + i)
+        jobs.append((torch.cuda.Stream(), args, k, layer_step(bm, *args, k)))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for stream, args, k, _ref in jobs:
+            with torch.cuda.stream(stream):
+                got.append(layer_step(bm, *args, k))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for a, b in zip(g, jobs[i % 2][3]):
+            assert torch.equal(a, b), i
+
+
+def test_two_graphs_replayed_in_turn(bm):
+    a_args = layer_inputs(64, 16, 4, 256, 128, F16, 50)
+    b_args = layer_inputs(2000, 16, 4, 256, 128, F16, 51)
+    refs = [layer_step(bm, *args, 4) for args in (a_args, b_args)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for args in (a_args, b_args):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer_step(bm, *args, 4))
+        graphs.append(g)
+    for turn in range(3):
+        for g in graphs:
+            g.replay()
+        layer_step(bm, *a_args, 4)
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, refs):
+            for x, y in zip(got, ref):
+                assert torch.equal(x, y), turn
+
+
+def test_offsets_past_32_bits(bm):
+    """Weights, rows and gradients of more than 2^31 elements, looked at where
+    they end."""
+    E, N, K = 5, 16384, 32768
+    g = rng(60)
+    w = torch.empty(E, N, K, dtype=BF16, device="cuda").uniform_(-0.01, 0.01, generator=g)
+    counts = [2, 0, 40, 0, 70]  # the few-rows and the tiled kernel's range
+    bounds, R = ragged(g, E, counts)
+    x = normal(g, 70000, K, dtype=BF16)
+    rows = torch.randint(69000, 70000, (R,), generator=g, device="cuda", dtype=torch.int32)
+    dy = normal(g, R, N, dtype=BF16)
+    at = slice(R - 70, R)
+    xe = x[rows[at].long()].double()
+    we = w[4, N - 300:].double()
+    y = bm.grouped_matmul(x, w, bounds, rows=rows)
+    want = xe @ we.t()
+    check(y[at, N - 300:], want, half_step(want, BF16) + xe.abs() @ we.abs().t() * (K * STEP), "y")
+    two = torch.tensor([0, 0, 0, 0, 0, 3], dtype=torch.int32, device="cuda")
+    few = bm.grouped_matmul(x, w, two, rows=rows[at][:3].contiguous())
+    check(few[:, N - 300:], want[:3], half_step(want[:3], BF16) + (xe.abs() @ we.abs().t())[:3] * (K * STEP), "few")
+    dx = bm.grouped_matmul_dx(dy, w, bounds)
+    d, wc = dy[at].double(), w[4, :, K - 200:].double()
+    want = d @ wc
+    check(dx[at, K - 200:], want, half_step(want, BF16) + d.abs() @ wc.abs() * (N * STEP), "dx")
+    dw = bm.grouped_matmul_dw(dy, x, bounds, torch.empty_like(w), rows)
+    want = d[:, N - 300:].t() @ xe
+    check(dw[4, N - 300:], want, half_step(want, BF16) + d[:, N - 300:].abs().t() @ xe.abs() * (70 * STEP), "dw")
+    assert not bool(dw[3, -1].any())
+    slot = torch.randperm(70000, generator=g, device="cuda")[:64].reshape(32, 2).int()
+    slot[31, 1] = 69999
+    gates = torch.rand(32, 2, generator=g, device="cuda")
+    out = bm.moe_combine(x, slot, gates)
+    r, wt = plain_combine(x, slot, gates)
+    want = (r * wt[:, :, None]).sum(1)
+    check(out, want, half_step(want, BF16) + (r * wt[:, :, None]).abs().sum(1) * 3 * STEP, "combine")
+
+
+def test_w4_offsets_past_32_bits(bm):
+    E, N, K = 9, 32768, 16384
+    g = rng(61)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(E, N, K // 128, generator=g, device="cuda") * 0.01).half()
+    m = (s.float() * -7.5).half()
+    for counts in ([0] * 8 + [1], [0] * 8 + [20]):
+        bounds, R = ragged(g, E, counts)
+        x = normal(g, R, K, dtype=F16)
+        y = bm.w4_matmul(x, codes, s, m, torch.empty(R, N, dtype=F32, device="cuda"), bounds)
+        last = slice(N - 200, N)
+        q = torch.stack([codes[8, last] & 15, codes[8, last] >> 4], -1).reshape(200, K).double()
+        sd = s[8, last].double().repeat_interleave(128, 1)
+        md = m[8, last].double().repeat_interleave(128, 1)
+        want = x.double() @ (sd * q + md).t()
+        size = x.double().abs() @ (sd * q + md.abs() + 32 * sd).t()
+        check(y[:, last], want, half_step(want, F32) + size * (K * STEP), "w4")
