@@ -69,8 +69,8 @@ __global__ __launch_bounds__(256) void k_mm_pad(const uint16_t* __restrict__ src
 // contraction in steps of 64 (whole 128-byte lines of a row).  Every step's two operand tiles are copied
 // straight into LDS by 16-byte loads (no registers in between) into one of
 // kBufs buffers, kBufs - 1 steps ahead of the products: 2 of the 256 x 256
-// tile's 64 KB, 4 of the 128 x 128 tile's 32 KB, whose steps are too short to
-// hide one copy's latency.
+// tile's 64 KB, 3 of the 256 x 128 tile's 48 KB, 4 of the 128 x 128 tile's
+// 32 KB, whose steps are too short to hide one copy's latency.
 //
 // An operand whose rows run along the contraction lies in LDS as
 // [row][64 elements]: 16-byte piece p of row r at place p ^ (r / 2 % 8), so
@@ -190,7 +190,8 @@ __device__ __forceinline__ void tile_place(uint32_t id, int mt, int nt, int& m, 
 }
 
 constexpr int kTile = 256;                          // rows and columns of a tile
-constexpr uint32_t kLds = 2 * 2 * kTile * kStep * 2;  // two buffers of two operands
+constexpr uint32_t kOutLds = 2 * 2 * kTile * kStep * 2;  // of the output on its way
+constexpr uint32_t kLds = 3 * (kTile + kTile / 2) * kStep * 2;  // three buffers of a 256 x 128 tile
 
 // Output rows m0 .. m0 + mn and columns n0 .. n0 + nn of expert e, with the
 // contraction c0 .. c0 + cn.
@@ -393,7 +394,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   // whole rows, 16 bytes a lane.  16-byte piece p of LDS row r lies at
   // p ^ (r % 16), which spreads 16 rows' writes over the banks.
   constexpr int kOut = ACT ? TN / 2 : TN;                         // columns
-  constexpr int kPassRows = kLds / (kOut * (int)sizeof(O)) < TM ? kLds / (kOut * (int)sizeof(O)) : TM;
+  constexpr int kPassRows = kOutLds / (kOut * (int)sizeof(O)) < TM ? kOutLds / (kOut * (int)sizeof(O)) : TM;
   constexpr int kPasses = TM / kPassRows, kI = MI / kPasses;       // 16-row blocks of a wave per pass
   constexpr int kRowPieces = kOut * (int)sizeof(O) / 16;
   constexpr int kKey = kRowPieces < 16 ? kRowPieces - 1 : 15;
@@ -451,10 +452,11 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 }
 
 // One work-group per tile: first the whole rounds of the chip's compute units
-// with 256 x 256 tiles, then what is left, cut into 128 x 128 tiles if it
-// would fill at most half a round (see kSplitMost).
+// with 256 x 256 tiles, then what is left: cut in four 128 x 128 tiles where
+// those make one round at most, in two of 256 x 128 where those do (a quarter
+// takes about 0.45 of a tile's time, a half 0.65: its copies, not its
+// products, take the time), else as it is.
 constexpr int kUnits = 256;       // compute units of an MI355X, one work-group each (its LDS)
-constexpr int kSplitMost = 128;   // left-over tiles that are cut in four
 
 template <class T, class O, int MODE, bool ACT>
 __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
@@ -465,7 +467,8 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   const int ntn = (cols + kCols - 1) / kCols, ntm = (s.N + kTile - 1) / kTile;
   const int mt = MODE == kDw ? s.E * ntm : count_tiles(s.bounds, s.E, s.R, kTile);
   const uint32_t total = (uint32_t)mt * ntn, left = total % kUnits;
-  const uint32_t whole = left <= kSplitMost ? total - left : total;
+  const uint32_t parts = left <= kUnits / 4 ? 4 : left <= kUnits / 2 ? 2 : 1;
+  const uint32_t whole = parts > 1 ? total - left : total;
   // Work-group b runs on XCD b % 8, and every XCD takes 32 consecutive tiles of
   // a round, which share operand rows in its L2.  (One long run per XCD would
   // leave those with the small experts' part tiles idle at the end.)
@@ -477,11 +480,11 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
     if (id >= whole) return;
   } else {
     b -= rounds * kUnits;
-    const uint32_t run4 = ((total - whole) * 4 + 7) / 8;
-    const uint32_t id4 = (b & 7) * run4 + (b >> 3);
-    if ((b >> 3) >= run4 || id4 >= (total - whole) * 4) return;
-    id = whole + id4 / 4;
-    part = id4 & 3;
+    const uint32_t cut = (total - whole) * parts, run = (cut + 7) / 8;
+    const uint32_t at = (b & 7) * run + (b >> 3);
+    if ((b >> 3) >= run || at >= cut) return;
+    id = whole + at / parts;
+    part = at % parts;
   }
   int e, m0, mn, c0, cn, mi, ni;
   tile_place(id, mt, ntn, mi, ni);
@@ -500,12 +503,17 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   int n0 = ni * kCols, nn = min(kCols, cols - n0);
   if (part < 0) {
     mm_tile<T, O, MODE, kTile, kTile, 2, 4, 2, ACT>(s, base, e, m0, mn, n0, nn, c0, cn);
-  } else {
+  } else if (parts == 4) {
     const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
     mn = min(kTile / 2, mn - pm), nn = min(kCols / 2, nn - pn);
     if (mn <= 0 || nn <= 0) return;
-    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, 4, ACT>(s, base, e, m0 + pm, mn, n0 + pn,
-                                                                nn, c0, cn);
+    mm_tile<T, O, MODE, kTile / 2, kTile / 2, 2, 4, 4, ACT>(s, base, e, m0 + pm, mn, n0 + pn, nn,
+                                                            c0, cn);
+  } else {
+    const int pn = part * (kCols / 2);
+    nn = min(kCols / 2, nn - pn);
+    if (nn <= 0) return;
+    mm_tile<T, O, MODE, kTile, kTile / 2, 2, 4, 3, ACT>(s, base, e, m0, mn, n0 + pn, nn, c0, cn);
   }
 }
 
@@ -766,8 +774,7 @@ int launch_mm(MmArgs s, int dtype, int o_dtype, int64_t a_rows, void* ws, size_t
       }
     }
     // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
-    const long long cut = mt * ntn < kSplitMost ? mt * ntn : kSplitMost;
-    const dim3 grid((unsigned)((mt * ntn + kUnits - 1) / kUnits * kUnits + cut * 4 + 8));
+    const dim3 grid((unsigned)((mt * ntn + kUnits - 1) / kUnits * kUnits + kUnits + 8));
     if (MODE == kFwd && s.act)
       hipLaunchKernelGGL((k_mm_tile<T, O, MODE, MODE == kFwd>), grid, dim3(512), 0, st, s);
     else

@@ -375,6 +375,21 @@ def test_grouped_matmul_gradients(bm, E, counts, N, K, dtype, out):
     assert bool((dx[n:] == 7).all())
 
 
+# E, rows of expert i, N, K: tiles of 256 x 256 that make a round and more, and
+# left-overs that are cut in four (60, 30), in two (104, 120, 90, 88) or not (130,
+# 234, 182), forward, with the activation, dx and dw
+ROUNDS = [(24, 53, 300, 1032, 1032), (24, 53, 300, 776, 776), (16, 97, 290, 1000, 1288),
+          (20, 71, 520, 1100, 1290), (24, 53, 300, 2568, 520)]
+
+
+@pytest.mark.parametrize("E, step, most, N, K", ROUNDS)
+@pytest.mark.parametrize("dtype, out", [(BF16, BF16), (F16, F32)])
+def test_grouped_matmul_rounds_of_tiles(bm, E, step, most, N, K, dtype, out):
+    counts = [i * step % most for i in range(E)]
+    test_grouped_matmul(bm, E, counts, N, K, dtype, out)
+    test_grouped_matmul_gradients(bm, E, counts, N, K, dtype, out)
+
+
 @pytest.mark.parametrize("N, K", [(96, 256), (40, 31)])
 def test_grouped_matmul_strides_and_bad_rows(bm, N, K):
     g = rng(4)
