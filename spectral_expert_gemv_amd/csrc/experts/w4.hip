@@ -25,7 +25,6 @@ struct W4Args {
   void* y;
   int64_t ldy;
   int act;
-  int turns;  // blocks of kCols weight rows of a work-group: 1 or kWaves
 };
 
 __device__ inline int w4_row(const W4Args& s, int i) {
@@ -79,9 +78,8 @@ __global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
 // A work-group takes up to 32 rows of one expert and a block of 32 rows of its
 // weights (with the activation 16 of the gate and the same 16 of the up
 // half), whose inputs its four waves split in turns of 128, adding up through
-// LDS; or, when there is enough work, a block for each of its waves.  Every
-// code is read once per tile of rows, 16 bytes (32 inputs of one row) a lane,
-// a stage of turns ahead of its use.
+// LDS.  Every code is read once per tile of rows, 16 bytes (32 inputs of one
+// row) a lane, a stage of turns ahead of its use.
 //
 // In a turn lane (r, q) loads the codes of row r, inputs 32 q .. 32 q + 31.
 // One matrix-core step takes 32 inputs, 8 a lane, that have to lie in one
@@ -170,11 +168,8 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int groups = s.K / G;
-  // One block of columns for the work-group, whose waves split the inputs, or
-  // one for each of its waves.
-  const int parts = s.turns == 1 ? kWaves : 1, part = s.turns == 1 ? wv : 0;
-  const int n0 = (s.turns == 1 ? blockIdx.x : blockIdx.x * kWaves + wv) * kPer;
-  const int stages = (s.K + kTurn * parts * U - 1) / (kTurn * parts * U);
+  const int n0 = blockIdx.x * kPer;
+  const int stages = (s.K + kTurn * kWaves * U - 1) / (kTurn * kWaves * U);
   const T* x[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
@@ -197,12 +192,12 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
     scales[b] = s.scales + row * groups;
     mins[b] = s.mins + row * groups;
   }
-  // Turn u of stage st starts at input ((st U + u) parts + part) kTurn.  Past
+  // Turn u of stage st starts at input ((st U + u) kWaves + wave) kTurn.  Past
   // the end x is 0, and codes and groups are the row's last ones.
   auto load = [&](int st, Stage& v) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = ((st * U + u) * parts + part) * kTurn;
+      const int k = ((st * U + u) * kWaves + wv) * kTurn;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         v.c[u][b] = *reinterpret_cast<const uint4*>(codes[b] + min(k + 32 * q, s.K - 32) / 2);
@@ -292,13 +287,6 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
       ((O*)s.y)[(int64_t)(t.row0 + row) * s.ldy + n] = from_f32<O>(o);
     }
   };
-  if (parts == 1) {
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-      for (int b = 0; b < (ACT ? 1 : 2); ++b) put(m, b, acc[m][b], acc[m][1]);
-    return;
-  }
   // the four waves' sums, [wave][tile of 16 x 16][lane]
   f32x4* sums = (f32x4*)lds;
 #pragma unroll
@@ -385,12 +373,10 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 }
 
 constexpr int kVecRows = 2;  // rows of x the vector path takes
-constexpr int kOuts = 8;     // rows of the weights per wave and block
-constexpr int kMostTurns = 4;
+constexpr int kOuts = 8;     // rows of the weights per wave
 constexpr int kBatch = 4;    // loads whose rows are summed together
-constexpr int kEnoughGroups = 4096;
 constexpr int kVecInputs = 16384;  // rows x inputs of x that the LDS holds
-constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kMostTurns * kVecRows * 4;
+constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * kVecRows * 4;
 
 template <class T, class O, bool ACT, int M, bool kWide>
 __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* lds) {
@@ -402,12 +388,11 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
   const int at = kWide ? lane : lane & (lanes - 1), which = kWide ? 0 : lane >> log_lanes;
   const int chunks = (s.K + 32 * lanes - 1) >> (5 + log_lanes);
   constexpr int kN = ACT ? kOuts / 2 : kOuts;
-  const int outs = kOuts * s.turns;
-  const int n0 = (blockIdx.x * kWaves + wv) * kN * s.turns;
+  const int n0 = (blockIdx.x * kWaves + wv) * kN;
   const int groups = s.K / s.G;
   uint4* xs = (uint4*)lds;                                   // [m][chunk][piece][lane]
   float* sums = (float*)(lds + kVecInputs * 2);              // [m][chunk][lane]
-  float* mine = (float*)(lds + kVecInputs * 2 + kVecInputs / 32 * 4) + wv * outs * M;
+  float* mine = (float*)(lds + kVecInputs * 2 + kVecInputs / 32 * 4) + wv * kOuts * M;
 
   // the wave's rows, clamped to the last one
   const int64_t first = (int64_t)t.e * (ACT ? 2 : 1) * s.N + min(n0, s.N - 1);
@@ -430,9 +415,9 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
       const int j = (batch * kBatch + i) * sub + which;
       l.c[i] = uint4{0, 0, 0, 0};
       l.s[i] = l.m[i] = (f16)0.f;
-      if (j < outs && k < s.K) {
-        // (the rows of a wave lie within 2^25 bytes and 2^21 groups)
-        const int wr = min(ACT ? (j >> 3) * 4 + (j & 3) : j, most);
+      if (j < kOuts && k < s.K) {
+        // (the rows of a wave lie within 2^22 bytes and 2^18 groups)
+        const int wr = min(ACT ? j & 3 : j, most);
         const bool up = ACT && (j & 4);
         const int g = wr * groups + (k >> log_g);
         l.c[i] = *reinterpret_cast<const uint4*>((up ? codes_up : codes) + wr * (s.K / 2) + k / 2);
@@ -465,7 +450,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
   }
   __syncthreads();
 
-  const int batches = (outs + sub * kBatch - 1) / (sub * kBatch);
+  const int batches = (kOuts + sub * kBatch - 1) / (sub * kBatch);
   float acc[kBatch][M];
   for (int batch = 0, chunk = 0; batch < batches;) {
     const bool last = chunk + 1 == chunks;
@@ -513,7 +498,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
 #pragma unroll
         for (int m = 0; m < M; ++m) {
           const float v = lanes_sum(acc[i][m], lanes);
-          if (at == 0 && j < outs) mine[j * M + m] = v;
+          if (at == 0 && j < kOuts) mine[j * M + m] = v;
         }
       }
     }
@@ -521,12 +506,12 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
     batch = nb, chunk = nc;
   }
   __syncthreads();
-  static_assert(kOuts * kMostTurns * kVecRows <= 64, "an output per lane");
-  if (lane < kN * s.turns * M) {
+  static_assert(kOuts * kVecRows <= 64, "an output per lane");
+  if (lane < kN * M) {
     const int j = lane / M, m = lane % M;
     if (m < t.n && n0 + j < s.N) {
-      float o = mine[(ACT ? (j >> 2) * 8 + (j & 3) : j) * M + m];
-      if (ACT) o = gated(o, mine[((j >> 2) * 8 + 4 + (j & 3)) * M + m]);
+      float o = mine[j * M + m];
+      if (ACT) o = gated(o, mine[(j + kN) * M + m]);
       if (s.rows && w4_row(s, t.row0 + m) < 0) o = __builtin_nanf("");
       ((O*)s.y)[(int64_t)(t.row0 + m) * s.ldy + n0 + j] = from_f32<O>(o);
     }
@@ -588,7 +573,7 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   if (((uintptr_t)codes & 15u) || ((uintptr_t)scales & 3u) || ((uintptr_t)mins & 3u))
     return fail(BITSMOE_EINVAL, "codes must be 16-byte aligned, scales and mins 4-byte aligned");
   W4Args s{x, ldx, rows, div, x_rows, (const uint8_t*)codes, (const f16*)scales, (const f16*)mins,
-           bounds, R, E, N, K, G, y, ldy, act, 1};
+           bounds, R, E, N, K, G, y, ldy, act};
   const hipStream_t st = (hipStream_t)stream;
   const bool wide = ((uintptr_t)x & 15u) == 0 && ldx % 8 == 0;
   const bool few = R <= (long long)kFewRows * E;
@@ -597,12 +582,7 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   const long long tiles =
       bounds ? max_tiles(R, E, rows_tile) : ((long long)R + rows_tile - 1) / rows_tile;
   if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);
-  int per = !wide ? 4 : act ? kCols / 2 : kCols;
-  // a block per wave once there are enough work-groups to fill the chip
-  // several times over: finding the rows and bringing in x is done once for
-  // four blocks, and the waves have no sums to exchange
-  if (wide && tiles * ((N + per * kWaves - 1) / (per * kWaves)) >= kEnoughGroups) s.turns = kWaves;
-  per *= s.turns;
+  const int per = !wide ? 4 : act ? kCols / 2 : kCols;
   const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)tiles);
   auto go = [&](auto t, auto o) {
     using T = decltype(t);
