@@ -1,7 +1,9 @@
 // The gated activation h = SiLU(gate) * up of rows [gate | up], its gradient,
 // and the routing-weighted combine of the experts' rows with its gradient.
 // Every kernel here is bound by memory: each input element is read once and
-// each output written once, 16 bytes a lane where the rows allow it.
+// each output written once, 16 bytes a lane where the rows allow it.  24576 x
+// 1408: 33 us and 53 us with the gradient's; combine of 8192 x 6 rows of 2048:
+// 53 us, its gradient 73.
 #include "experts.h"
 
 namespace bitsmoe {

@@ -451,6 +451,10 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
   }
 }
 
+// Bound by the matrix cores and the copies that feed them: 8 experts of
+// 4096 x 14336 with 1024 rows each, forward 745 us (1290 TFLOP/s), dx 830, dw
+// (1.9 GB of float32 written) 1095.
+//
 // One work-group per tile: first the whole rounds of the chip's compute units
 // with 256 x 256 tiles, then what is left: cut in four 128 x 128 tiles where
 // those make one round at most, in two of 256 x 128 where those do (a quarter
@@ -524,7 +528,9 @@ __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
 // split the inputs in turns of 64, a whole 128-byte line of each weight row,
 // and add up their sums through LDS.  The weights are the products' first
 // operand, so that 16 rows of x fill the other side of one matrix-core
-// instruction; rows of x past the tile's repeat the last one.
+// instruction; rows of x past the tile's repeat the last one.  Bound by the
+// weights' bytes: gate/up of 8 experts (50 MB) 12.3 us, of the 70 experts that
+// 32 tokens reach (429 MB) 85 us, 5.0 TB/s.
 constexpr int kFewRows = 64, kFewCols = 32, kFewWaves = 4;
 
 // 8 elements from an address of any element's alignment (the hardware takes
