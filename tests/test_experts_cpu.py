@@ -252,3 +252,53 @@ def test_w4_pack_refuses():
         bm.w4_pack(np.zeros((2, 48), np.float32), 32)
     with pytest.raises(bm.BitsMoEError):
         bm.w4_pack(np.zeros((2, 48), np.float32), 16)
+
+
+SANITIZED = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+#include "bitsmoe.h"
+int main() {
+  const int groups[] = {32, 64, 128};
+  for (int g : groups) {
+    const int K = 256, rows = 7;
+    float* w = (float*)malloc(sizeof(float) * rows * K);
+    for (int i = 0; i < rows * K; ++i) w[i] = (float)((i * 2654435761u) % 2001) * 60.f - 60000.f;
+    for (int i = 0; i < K; ++i) w[i] = 0.f, w[K + i] = i % 2 ? -0.f : 0.f, w[2 * K + i] = 1e-8f * i;
+    unsigned char* c = (unsigned char*)malloc(rows * K / 2);
+    unsigned short *s = (unsigned short*)malloc(2 * rows * K / g), *m = (unsigned short*)malloc(2 * rows * K / g);
+    if (bitsmoe_w4_pack(w, rows, K, g, c, s, m)) return 1;
+    if (bitsmoe_w4_pack(w, rows, K, 16, c, s, m) != BITSMOE_ESHAPE) return 2;
+    if (bitsmoe_w4_pack(w, rows, K + 8, g, c, s, m) != BITSMOE_ESHAPE) return 3;
+    if (bitsmoe_w4_pack(w, -1, K, g, c, s, m) != BITSMOE_ESHAPE) return 4;
+    if (bitsmoe_w4_pack(w, 0, K, g, 0, 0, 0)) return 5;
+    if (bitsmoe_w4_pack(w, rows, K, g, 0, s, m) != BITSMOE_EINVAL) return 6;
+    w[rows * K - 1] = 60001.f;
+    if (bitsmoe_w4_pack(w, rows, K, g, c, s, m) != BITSMOE_EBITS) return 7;
+    free(w), free(c), free(s), free(m);
+  }
+  puts("ok");
+  return 0;
+}
+"""
+
+
+def test_w4_pack_under_sanitizers(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "spectral_expert_gemv_amd", "csrc")
+    src = tmp_path / "w4.cpp"
+    src.write_text(SANITIZED)
+    exe = str(tmp_path / "w4")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined",
+                    "-fno-sanitize-recover=all", "-I", os.path.join(root, "include"), "-I", csrc,
+                    os.path.join(csrc, "common.cpp"), os.path.join(csrc, "experts", "w4_pack.cpp"),
+                    str(src), "-o", exe], check=True)
+    r = subprocess.run([exe], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
