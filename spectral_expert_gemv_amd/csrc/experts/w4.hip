@@ -339,7 +339,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_w4_mm(W4Args s) {
 // (which lie in one group), and two products are added per v_dot2.  The
 // decode of 8 codes is 8 instructions however few rows there are, and here
 // nothing but one sum per row is exchanged between lanes.  One row of each of
-// 128 experts (1536 x 2048): 48 us, 4.7 TB/s; one row of 4096 x 2048: 5.7 us, a
+// 128 experts (1536 x 2048): 46 us, 4.9 TB/s over weights that the call before
+// read as well; one row of 4096 x 2048: 5.7 us, a
 // chain of latencies.  (On the matrix cores the latter took 7.1.)
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c, f16) {
   typedef __attribute__((ext_vector_type(2))) _Float16 h2;
