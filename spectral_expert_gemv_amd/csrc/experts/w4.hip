@@ -3,7 +3,7 @@
 // and minima m per group of G inputs; dense or grouped by expert, optionally
 // SiLU(gate) * up of the two halves of the rows.  Per group
 //   sum_c W x = s (sum_c q x) + m (sum_c x),
-// so the codes enter the products as small whole numbers, exactly.
+// so the codes enter the products as the whole numbers 0..15, exactly.
 #include <type_traits>
 
 #include "experts.h"
@@ -85,40 +85,42 @@ __global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
 // One matrix-core step takes 32 inputs, 8 a lane, that have to lie in one
 // group: a 4 x 4 transpose of the words between the four lanes of a row (two
 // row swaps each way) gives lane (r, q) the inputs 32 s + 8 q .. of step s.
-// A word's eight codes become eight fp16 (bf16) values 16 + q, exactly, by a
-// shift and an and-or per pair (q goes into the mantissa of 16.0), in the
-// order 0 4 1 5 2 6 3 7; x is put into that order.  Per group
-//   y += s (sum (16 + q) x) + (m - 16 s) (sum x),
-// where sum x comes from one more matrix-core step with ones.  x is the first
+// A word's eight codes become eight fp16 (bf16) values q, exactly: a byte q of
+// 0..15 is the e4m3 number q 2^-9 (a subnormal up to 7, then 2^-6 (1 + (q - 8) / 8)),
+// which the hardware converts two at a time, times 512.  Seven instructions,
+// in the order 0 2 4 6 1 3 5 7; x is put into that order.  Per group
+//   y += s (sum q x) + m (sum x),
+// where sum x comes from one more matrix-core step with ones.  (The values 16 + q, q
+// in the mantissa of 16.0, cost eight instructions and the difference of two
+// sums as large as 16 s sum |x| where s q and m may be small.)  x is the first
 // operand, so a lane's sums all belong to its own row of weights, whose s and
-// m it holds.  All sums are float32.  Bound by vector instructions (about 175 a
-// turn and wave, 40 % of them decode): 8 rows of each of 128 experts 96 us.
+// m it holds.  All sums are float32.  Bound by vector instructions (about 170 a
+// turn and wave, a third of them decode): 8 rows of each of 128 experts of
+// 1536 x 2048, groups of 128, weights that no cache holds: 102 us.
 constexpr int kRows = 32, kCols = 32, kWaves = 4, kTurn = 128;
 
+// two ones
 template <class T>
-struct Magic;
+constexpr uint32_t kOnes = 0x3C003C00u;
 template <>
-struct Magic<f16> {
-  static constexpr int kShift = 6;  // q in mantissa bits 6 .. 9 of 16.0
-  static constexpr uint32_t kMask = 0x03C003C0u, kOr = 0x4C004C00u, kOne = 0x3C003C00u;
-};
-template <>
-struct Magic<bf16> {
-  static constexpr int kShift = 3;  // bits 3 .. 6
-  static constexpr uint32_t kMask = 0x00780078u, kOr = 0x41804180u, kOne = 0x3F803F80u;
-};
+constexpr uint32_t kOnes<bf16> = 0x3F803F80u;
 
-// 8 codes of a word as 16 + q, order 0 4 1 5 2 6 3 7
+// the e4m3 numbers of the lower (upper) two bytes times 512
+template <bool kHigh>
+__device__ __forceinline__ uint32_t codes2(uint32_t w, f16) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 512.0f, kHigh));
+}
+template <bool kHigh>
+__device__ __forceinline__ uint32_t codes2(uint32_t w, bf16) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, kHigh));
+}
+
+// 8 codes of a word, order 0 2 4 6 1 3 5 7
 template <class T>
 __device__ __forceinline__ typename Vec8<T>::type codes8(uint32_t w) {
-  typedef Magic<T> M;
-  uint4 o;
-  auto put = [&](int n) {
-    const int sh = M::kShift - 4 * n;
-    const uint32_t v = sh >= 0 ? w << (sh > 0 ? sh : 0) : w >> (sh < 0 ? -sh : 0);
-    return (v & M::kMask) | M::kOr;
-  };
-  o.x = put(0), o.y = put(1), o.z = put(2), o.w = put(3);
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  const uint4 o = {codes2<false>(even, T{}), codes2<true>(even, T{}), codes2<false>(odd, T{}),
+                   codes2<true>(odd, T{})};
   return __builtin_bit_cast(typename Vec8<T>::type, o);
 }
 
@@ -126,10 +128,10 @@ __device__ __forceinline__ typename Vec8<T>::type codes8(uint32_t w) {
 template <class T>
 __device__ __forceinline__ typename Vec8<T>::type order8(uint4 v) {
   uint4 o;
-  o.x = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
-  o.y = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
-  o.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
-  o.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
+  o.x = __builtin_amdgcn_perm(v.y, v.x, 0x05040100u);
+  o.y = __builtin_amdgcn_perm(v.w, v.z, 0x05040100u);
+  o.z = __builtin_amdgcn_perm(v.y, v.x, 0x07060302u);
+  o.w = __builtin_amdgcn_perm(v.w, v.z, 0x07060302u);
   return __builtin_bit_cast(typename Vec8<T>::type, o);
 }
 
@@ -175,7 +177,7 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
 #pragma unroll
   for (int m = 0; m < MB; ++m)
     x[m] = (const T*)s.x + (int64_t)max(w4_row(s, t.row0 + min(16 * m + r, t.n - 1)), 0) * s.ldx + 8 * q;
-  const uint4 ones = {Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne, Magic<T>::kOne};
+  const uint4 ones = {kOnes<T>, kOnes<T>, kOnes<T>, kOnes<T>};
   const typename Vec8<T>::type one8 = __builtin_bit_cast(typename Vec8<T>::type, ones);
 
   struct Stage {
@@ -255,7 +257,7 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float sc = (float)v.s[u][b][g];
-          const float mn = s.mins ? fmaf(-16.f, sc, (float)v.m[u][b][g]) : -24.f * sc;
+          const float mn = s.mins ? (float)v.m[u][b][g] : -8.f * sc;
 #pragma unroll
           for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -337,11 +339,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_w4_mm(W4Args s) {
 // while the next four are in flight.  x lies in LDS, in the codes' order and
 // so that a read is contiguous over the lanes, with its sums per 32 inputs
 // (which lie in one group), and two products are added per v_dot2.  The
-// decode of 8 codes is 8 instructions however few rows there are, and here
+// decode of 8 codes is 7 instructions however few rows there are, and here
 // nothing but one sum per row is exchanged between lanes.  One row of each of
-// 128 experts (1536 x 2048): 46 us, 4.9 TB/s over weights that the call before
-// read as well; one row of 4096 x 2048: 5.7 us, a
-// chain of latencies.  (On the matrix cores the latter took 7.1.)
+// 128 experts (1536 x 2048, groups of 128): 58 us, 3.7 TB/s over weights that
+// no cache holds, 52 us over the same ones at each call; one row of 4096 x
+// 2048: 5.4 us, a chain of latencies.  (On the matrix cores the latter took
+// 1.4 us more.)
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c, f16) {
   typedef __attribute__((ext_vector_type(2))) _Float16 h2;
   return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, a), __builtin_bit_cast(h2, b), c, false);
@@ -384,7 +387,6 @@ constexpr int kVecLds = kVecInputs * 2 + kVecInputs / 32 * 4 + kWaves * kOuts * 
 
 template <class T, class O, bool ACT, int M, bool kWide>
 __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* lds) {
-  typedef Magic<T> Mg;
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int log_lanes = kWide ? 6 : s.K <= 256 ? 3 : s.K <= 512 ? 4 : 5;
   const int lanes = 1 << log_lanes, sub = 64 >> log_lanes;  // lanes per row, rows per load
@@ -444,10 +446,10 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
       const uint4 o = __builtin_bit_cast(uint4, order8<T>(v));
       const int a = (p >> 2) & (lanes - 1), c = p >> (log_lanes + 2);
       xs[(((m * chunks + c) * 4 + (p & 3)) << log_lanes) + a] = o;
-      float f = dot2(o.x, Mg::kOne, 0.f, T{});
-      f = dot2(o.y, Mg::kOne, f, T{});
-      f = dot2(o.z, Mg::kOne, f, T{});
-      f = dot2(o.w, Mg::kOne, f, T{});
+      float f = dot2(o.x, kOnes<T>, 0.f, T{});
+      f = dot2(o.y, kOnes<T>, f, T{});
+      f = dot2(o.z, kOnes<T>, f, T{});
+      f = dot2(o.w, kOnes<T>, f, T{});
       f = dpp_add<0x4E>(dpp_add<0xB1>(f));  // the four neighbours' sum
       if ((p & 3) == 0) sums[((m * chunks + c) << log_lanes) + a] = f;
     }
@@ -491,7 +493,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const float sc = (float)now.s[i];
-        const float mn = s.mins ? fmaf(-16.f, sc, (float)now.m[i]) : -24.f * sc;
+        const float mn = s.mins ? (float)now.m[i] : -8.f * sc;
         acc[i][m] = fmaf(sc, d[i][m], fmaf(mn, sx, acc[i][m]));
       }
     }
