@@ -426,8 +426,11 @@ int bitsmoe_moe_combine_grad(const void* dout, int out_dtype, int64_t ldo, int y
  * NULL: symmetric, -8 * scales.  Arrays are E x rows x (K/2 bytes, K/G, K/G),
  * rows = N, or 2N (gate first) with BITSMOE_ACT_SILU_MUL; codes 16-byte
  * aligned, scales and mins 4-byte aligned.  K must be a multiple of G.
- * y, x, rows, div, bounds as for bitsmoe_grouped_matmul; bounds NULL (E = 1):
- * one dense projection of all R rows.
+ * y, x, rows, div, bounds as for bitsmoe_grouped_matmul, but without a
+ * workspace: x's rows are read in place at any alignment; bounds NULL (E = 1):
+ * one dense projection of all R rows.  R <= 2^24, E <= 65535 (and E times the
+ * tiles of R rows below 2^30), N and K <= 2^20.  A code is decoded again for
+ * every 16 (R <= 16 E) or 32 rows of an expert.
  * bitsmoe_w4_pack (host arrays): quantizes `rows` rows of K float32 weights
  * with the packer's rule at 4 bits: s = fp16_rne((max - min) / 15), 1 if that
  * is 0; m = fp16_rne(min); q = clamp(nearbyint((w - m) / s), 0, 15).

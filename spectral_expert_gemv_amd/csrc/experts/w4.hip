@@ -34,44 +34,14 @@ __device__ inline int w4_row(const W4Args& s, int i) {
   return r < s.x_rows ? r : -1;
 }
 
-// A wave per (row, output): lanes along the inputs, 8 codes at a time.  For
-// rows of x that are not 16-byte aligned.
-template <class T, class O>
-__global__ __launch_bounds__(256) void k_w4_any(W4Args s) {
-  const int lane = threadIdx.x & 63;
-  const int n = blockIdx.x * 4 + (threadIdx.x >> 6);
-  int e = 0, i = blockIdx.y;
-  if (s.bounds) {
-    const Tile t = find_tile(s.bounds, s.E, s.R, blockIdx.y, 1);
-    if (t.n == 0) return;
-    e = t.e, i = t.row0;
-  }
-  if (n >= s.N) return;
-  const int xr = w4_row(s, i);
-  const int groups = s.K / s.G;
-  float y[2] = {0.f, 0.f};
-  for (int h = 0; h < (s.act ? 2 : 1); ++h) {
-    const size_t row = (size_t)e * (s.act ? 2 : 1) * s.N + (size_t)h * s.N + n;
-    const T* x = (const T*)s.x + (int64_t)max(xr, 0) * s.ldx;
-    float acc = 0.f;
-    for (int c = lane * 8; c < s.K; c += 64 * 8) {
-      const uint8_t* q = s.codes + row * (s.K / 2) + c / 2;
-      const float st = (float)s.scales[row * groups + c / s.G];
-      const float mn = s.mins ? (float)s.mins[row * groups + c / s.G] : -8.f * st;
-      for (int j = 0; j < 8; ++j) {
-        const int code = (q[j >> 1] >> (4 * (j & 1))) & 15;
-        acc = fmaf(fmaf(st, (float)code, mn), to_f32(x[c + j]), acc);
-      }
-    }
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) acc += __shfl_xor(acc, m, 64);
-    y[h] = acc;
-  }
-  if (lane == 0) {
-    float o = s.act ? gated(y[0], y[1]) : y[0];
-    if (xr < 0) o = __builtin_nanf("");
-    ((O*)s.y)[(int64_t)i * s.ldy + n] = from_f32<O>(o);
-  }
+// 8 elements of x from an address of any element's alignment: the hardware
+// takes 16 bytes at once all the same, so rows of any stride and offset run
+// the same kernel, with the same bits.
+template <class T>
+__device__ __forceinline__ uint4 load_x8(const T* p) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  typedef u4 loose __attribute__((aligned(2)));
+  return __builtin_bit_cast(uint4, (u4)*reinterpret_cast<const loose*>(p));
 }
 
 // ------------------------------------------------------- three rows and more
@@ -222,7 +192,7 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
           v.x[u][m][i] = uint4{0, 0, 0, 0};
-          if (in) v.x[u][m][i] = *reinterpret_cast<const uint4*>(x[m] + k + 32 * i);
+          if (in) v.x[u][m][i] = load_x8(x[m] + k + 32 * i);
         }
       }
     }
@@ -314,9 +284,12 @@ __device__ __forceinline__ void w4_rows(const W4Args& s, const Tile& t, float* l
   }
 }
 
+// The row tiles are the grid's y, in layers of kTilesY (what a grid takes).
+constexpr int kTilesY = 65535;
 __device__ __forceinline__ Tile w4_tile(const W4Args& s, int rows) {
-  if (s.bounds) return find_tile(s.bounds, s.E, s.R, blockIdx.y, rows);
-  const int row0 = blockIdx.y * rows;
+  const int tile = blockIdx.z * kTilesY + blockIdx.y;
+  if (s.bounds) return find_tile(s.bounds, s.E, s.R, tile, rows);
+  const int row0 = tile * rows;
   return Tile{0, row0, min(rows, s.R - row0)};
 }
 
@@ -442,7 +415,7 @@ __device__ __forceinline__ void w4_vec(const W4Args& s, const Tile& t, uint8_t* 
     const T* x = (const T*)s.x + (int64_t)max(w4_row(s, t.row0 + min(m, t.n - 1)), 0) * s.ldx;
     for (int p = tid; p < pieces; p += 64 * kWaves) {
       uint4 v = uint4{0, 0, 0, 0};
-      if (8 * p < s.K) v = *reinterpret_cast<const uint4*>(x + 8 * p);
+      if (8 * p < s.K) v = load_x8(x + 8 * p);
       const uint4 o = __builtin_bit_cast(uint4, order8<T>(v));
       const int a = (p >> 2) & (lanes - 1), c = p >> (log_lanes + 2);
       xs[(((m * chunks + c) * 4 + (p & 3)) << log_lanes) + a] = o;
@@ -581,22 +554,17 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
   W4Args s{x, ldx, rows, div, x_rows, (const uint8_t*)codes, (const f16*)scales, (const f16*)mins,
            bounds, R, E, N, K, G, y, ldy, act};
   const hipStream_t st = (hipStream_t)stream;
-  const bool wide = ((uintptr_t)x & 15u) == 0 && ldx % 8 == 0;
   const bool few = R <= (long long)kFewRows * E;
-  const int rows_tile = !wide ? 1 : few ? kFewRows : kRows;
+  const int rows_tile = few ? kFewRows : kRows;
   if (!countable(R, E, rows_tile)) return fail(BITSMOE_ESHAPE, "R=%d with E=%d", R, E);
   const long long tiles =
       bounds ? max_tiles(R, E, rows_tile) : ((long long)R + rows_tile - 1) / rows_tile;
-  if (tiles > 65535) return fail(BITSMOE_ESHAPE, "R=%d E=%d make too many row tiles", R, E);
-  const int per = !wide ? 4 : act ? kCols / 2 : kCols;
-  const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)tiles);
+  const int per = act ? kCols / 2 : kCols;
+  const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)(tiles < kTilesY ? tiles : kTilesY),
+                  (unsigned)((tiles + kTilesY - 1) / kTilesY));
   auto go = [&](auto t, auto o) {
     using T = decltype(t);
     using O = decltype(o);
-    if (!wide) {
-      hipLaunchKernelGGL((k_w4_any<T, O>), grid, dim3(256), 0, st, s);
-      return;
-    }
     const dim3 block(64 * kWaves);
     auto rows_of = [&](auto g) {
       constexpr int kG = decltype(g)::value;

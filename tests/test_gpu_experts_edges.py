@@ -62,3 +62,40 @@ def test_w4_of_one_sided_groups(bm, E, counts, K, G, dtype, size, off):
     mag = torch.matmul((sq + md.abs())[e], r.abs()[:, :, None])[:, :, 0]
     # K products and a few sums of groups and waves; the size of s q and m alone, not of an offset
     check(y, want, mag * ((K + 16) * STEP) + half_step(want, F32), "y")
+
+
+@pytest.mark.parametrize("E, counts, K, G", W4_ROWS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_w4_bits_do_not_depend_on_alignment(bm, E, counts, K, G, dtype):
+    _say("alignment", E, counts, K, G, dtype)
+    g = rng(K + 1)
+    bounds, R = ragged(g, E, counts)
+    codes = torch.randint(0, 256, (E, 66, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(E, 66, K // G, generator=g, device="cuda") * 0.1).half()
+    m = (s.float() * normal(g, E, 66, K // G)).half()
+    x = normal(g, R, K, dtype=dtype)
+    for act in (None, "silu_mul"):
+        want = bm.w4_matmul(x, codes, s, m, bounds=bounds, act=act)
+        for off in (1, 2, 4, 7):
+            assert torch.equal(bm.w4_matmul(at_offset(x, off), codes, s, m, bounds=bounds, act=act), want), off
+
+
+@pytest.mark.parametrize("R, off", [(70000, 1), (65535 * 32 + 77, 0), (65535 * 32 + 77, 3)])
+@pytest.mark.parametrize("E", [1, 2])
+def test_w4_of_many_rows(bm, R, off, E):
+    """More row tiles than one dimension of a grid takes."""
+    _say("many rows", R, off, E)
+    g = rng(R)
+    K, N = 32, 5
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(E, N, 1, generator=g, device="cuda") + 0.5).half()
+    m = (s.float() * -7.5).half()
+    x = at_offset(normal(g, R, K, dtype=F16), off)
+    first = R // 3 if E == 2 else R
+    bounds = None if E == 1 else torch.tensor([0, first, R], dtype=torch.int32, device="cuda")
+    y = bm.w4_matmul(x, codes, s, m, torch.empty(R, N, device="cuda"), bounds)
+    sq, md = dequantized(codes, s, m, K)
+    for e, rows in ((0, slice(0, first)), (E - 1, slice(R - (R - first or R), R))):
+        r = x[rows].double()
+        want = r @ (sq + md)[e].t()
+        check(y[rows], want, r.abs() @ (sq + md.abs())[e].t() * ((K + 16) * STEP) + half_step(want, F32), "y")
