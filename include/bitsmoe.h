@@ -431,6 +431,8 @@ int bitsmoe_moe_combine_grad(const void* dout, int out_dtype, int64_t ldo, int y
  * one dense projection of all R rows.  R <= 2^24, E <= 65535 (and E times the
  * tiles of R rows below 2^30), N and K <= 2^20.  A code is decoded again for
  * every 16 (R <= 16 E) or 32 rows of an expert.
+ * An infinity, or a value near float32's largest, in x gives what the products'
+ * sum gives (such outputs are computed one by one, which is slow).
  * bitsmoe_w4_pack (host arrays): quantizes `rows` rows of K float32 weights
  * with the packer's rule at 4 bits: s = fp16_rne((max - min) / 15), 1 if that
  * is 0; m = fp16_rne(min); q = clamp(nearbyint((w - m) / s), 0, 15).

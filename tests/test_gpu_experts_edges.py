@@ -99,3 +99,54 @@ def test_w4_of_many_rows(bm, R, off, E):
         r = x[rows].double()
         want = r @ (sq + md)[e].t()
         check(y[rows], want, r.abs() @ (sq + md.abs())[e].t() * ((K + 16) * STEP) + half_step(want, F32), "y")
+
+
+def same_kind(got, want, tol, what):
+    """NaN where want is, the same infinities, finite values within tol."""
+    got = got.double().cpu()
+    assert torch.equal(got.isnan(), want.isnan()), what + ": NaN"
+    inf = want.isinf()
+    assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf]), what + ": infinities"
+    fine = want.isfinite()
+    check(got[fine], want[fine], tol[fine], what)
+
+
+@pytest.mark.parametrize("E, counts, K, G", W4_ROWS)
+@pytest.mark.parametrize("dtype, off", [(F16, 0), (BF16, 0), (BF16, 5)])
+@pytest.mark.parametrize("symmetric", [False, True])
+def test_w4_of_infinities_and_nan(bm, E, counts, K, G, dtype, off, symmetric):
+    """An output is what sum_c W x is: +-inf, NaN for 0 inf or inf - inf, and
+    finite where only the sums of q x would pass float32's range."""
+    _say("w4 infinities", E, counts, K, G, dtype, off, symmetric)
+    g = rng(K + 9)
+    N = 20
+    bounds, R = ragged(g, E, counts)
+    codes = torch.randint(0, 256, (E, 2 * N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = ((torch.rand(E, 2 * N, K // G, generator=g, device="cuda") + 0.5) * 2.0 ** -6).half()
+    m = None if symmetric else (s.float() * (normal(g, *s.shape) - 7.5)).half()
+    clean = normal(g, R, K, dtype=dtype)
+    row, e = R - 1, E - 1
+    sq, md = dequantized(codes[e], s[e], None if m is None else m[e], G)
+    w = (sq + md).cpu()
+    half = lambda t: None if t is None else t[:, :N].contiguous()  # noqa: E731
+    y0 = bm.w4_matmul(clean, half(codes), half(s), half(m), bounds=bounds)
+    h0 = bm.w4_matmul(clean, codes, s, m, bounds=bounds, act="silu_mul")
+    kinds = {"inf": {5: INF}, "-inf": {K - 1: -INF}, "both": {1: INF, K - 2: -INF}, "nan": {3: NAN}}
+    if dtype == BF16:
+        kinds["large"] = {7: 3e37, K - 7: 3e37}  # 15 times this is past float32
+    for kind, put in kinds.items():
+        x = clean.clone()
+        for c, v in put.items():
+            x[row, c] = v
+        terms = w * x[row].double().cpu()
+        # (each product of w and the input, then their sum: as a product by a matrix would be)
+        v, tol = terms.sum(1), terms.abs().sum(1) * ((K + 16) * STEP)
+        x = at_offset(x, off)
+        y = bm.w4_matmul(x, half(codes), half(s), half(m), bounds=bounds)
+        same_kind(y[row], v[:N], tol[:N] + half_step(v[:N], dtype), kind)
+        assert torch.equal(y[:row], y0[:row]), kind
+        h = bm.w4_matmul(x, codes, s, m, bounds=bounds, act="silu_mul")
+        assert torch.equal(h[:row], h0[:row]), kind
+        if kind != "large":
+            want = torch.nn.functional.silu(v[:N]) * v[N:]
+            same_kind(h[row], want, torch.zeros_like(want), kind + " activated")
