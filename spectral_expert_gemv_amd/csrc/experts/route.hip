@@ -319,6 +319,12 @@ __global__ __launch_bounds__(64 * kOneWaves) void k_group_one(const int32_t* __r
   group_one(ids, P, E, bits, bounds, order, slot);
 }
 
+// No pairs: bounds of 0, however many experts.
+__global__ __launch_bounds__(256) void k_group_none(int E, int32_t* __restrict__ bounds) {
+  const int e = blockIdx.x * 256 + threadIdx.x;
+  if (e <= E) bounds[e] = 0;
+}
+
 // Up to 4 tokens and 64 pairs: one wave, nothing but registers.  Lane p holds
 // pair p's id; a place is the number of pairs with a lower id, or the same
 // and a lower index.
@@ -466,11 +472,15 @@ int group_check(int P, int E) {
 }
 
 size_t group_ws(int P, int E) {
-  return group_in_one(P, E) ? 0 : (size_t)group_blocks(P, E) * (grid_waves(E) + 1) * (E + 1) * 4;
+  return P == 0 || group_in_one(P, E) ? 0 : (size_t)group_blocks(P, E) * (grid_waves(E) + 1) * (E + 1) * 4;
 }
 
 int run_group(const int32_t* ids, int P, int E, int32_t* bounds, int32_t* order, int32_t* slot,
               void* ws, hipStream_t st) {
+  if (P == 0) {  // (the grids below would have no work-group)
+    hipLaunchKernelGGL(k_group_none, dim3((unsigned)(E / 256 + 1)), dim3(256), 0, st, E, bounds);
+    return launched("moe_group");
+  }
   const int bits = id_bits(E);
   if (group_in_one(P, E)) {
     const size_t lds = ((size_t)kOneWaves * (E + 1) + kOneWaves + 1) * 4;

@@ -150,3 +150,31 @@ def test_w4_of_infinities_and_nan(bm, E, counts, K, G, dtype, off, symmetric):
         if kind != "large":
             want = torch.nn.functional.silu(v[:N]) * v[N:]
             same_kind(h[row], want, torch.zeros_like(want), kind + " activated")
+
+
+# ---------------------------------------------------- empty batches
+
+@pytest.mark.parametrize("E", [1, 255, 256, 512, 513, 600, 1024, 2048])
+def test_no_tokens_at_all(bm, E):
+    _say("no tokens", E)
+    ids = torch.empty((0, 1), dtype=torch.int32, device="cuda")
+    full = lambda *n: torch.full(n, 7, dtype=torch.int32, device="cuda")  # noqa: E731
+    b = full(E + 9)
+    bounds, order, slot = bm.moe_group(ids, E, b[:E + 1])
+    assert not bool(bounds.any()) and bool((b[E + 1:] == 7).all()) and order.numel() == slot.numel() == 0
+    bounds = full(E + 1)
+    bm.moe_route(torch.empty(0, E, device="cuda"), 1, bounds=bounds, order=full(0), slot=full(0, 1))
+    assert not bool(bounds.any())
+
+
+@pytest.mark.parametrize("E", [4, 600])
+def test_a_layer_of_no_tokens(bm, E):
+    from spectral_expert_gemv_amd import ExpertLayer
+    g = rng(E)
+    w1, w2 = normal(g, E, 16, 32, dtype=BF16), normal(g, E, 32, 8, dtype=BF16)
+    layer = ExpertLayer(w1, w2)
+    x, logits = torch.empty(0, 32, dtype=BF16, device="cuda"), torch.empty(0, E, device="cuda")
+    assert layer.forward(x, logits, 2).shape == (0, 32)
+    out, dx, dl, dw1, dw2 = layer.gradients(x, logits, 2, x)
+    assert out.shape == dx.shape == (0, 32) and dl.shape == (0, E)
+    assert dw1.shape == w1.shape and not bool(dw1.any()) and not bool(dw2.any())
