@@ -88,12 +88,16 @@ __device__ inline void store8(float* p, const float (&v)[8]) {
 // reciprocal: each within a step of float32, a third of the instructions of
 // an exact exp and division (products with the activation, 24576 rows of 64
 // experts: 361 -> 351 us).
-// (The maximum turns the NaN of inf - inf into a factor that leaves 0 or inf.)
+// Below g = -87.3, where it would be subnormal, it is 0: a SiLU of up to
+// 1.1e-36 there is lost.
+// (The low part is under 1e-5 wherever the exp is neither 0 nor inf.  Where the
+// product overflows it is infinite or NaN: the median of it, -1 and 1 is a
+// factor that leaves them 0 and inf.)
 __device__ inline float sigmoid(float g) {
 #pragma clang fp contract(off)
   constexpr float kHi = -1.44269502162933349609375f, kLo = -1.92596299112661746887e-8f;
   const float t = g * kHi;
-  const float lo = fmaxf(fmaf(g, kLo, fmaf(g, kHi, -t)), -1.0f);
+  const float lo = __builtin_amdgcn_fmed3f(fmaf(g, kLo, fmaf(g, kHi, -t)), -1.0f, 1.0f);
   const float e = __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182464599609375f, 1.0f);
   return __builtin_amdgcn_rcpf(1.0f + e);
 }

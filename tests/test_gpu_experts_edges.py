@@ -178,3 +178,32 @@ def test_a_layer_of_no_tokens(bm, E):
     out, dx, dl, dw1, dw2 = layer.gradients(x, logits, 2, x)
     assert out.shape == dx.shape == (0, 32) and dl.shape == (0, E)
     assert dw1.shape == w1.shape and not bool(dw1.any()) and not bool(dw2.any())
+
+
+# ------------------------------------------------- activation, router, combine
+
+@pytest.mark.parametrize("dtype, huge", [(F16, 65504.0), (BF16, 3.3e38)])
+@pytest.mark.parametrize("F", [48, 45])
+def test_silu_mul_of_infinities_nan_and_the_largest(bm, dtype, huge, F):
+    """As the formulas in 64 bits give it, for gates and ups up to the type's
+    largest value, infinities and NaN."""
+    _say("silu_mul", dtype, F)
+    gates = [INF, -INF, NAN, huge, -huge, huge * 0.73, huge * 0.69, -huge * 0.73, 0.0, 1.0, -20.0, 20.0]
+    ups = [1.0, -0.5, 0.0, INF, -INF, NAN, huge, 2.0 ** -10]
+    pairs = torch.tensor([(g, u) for g in gates for u in ups], dtype=dtype, device="cuda")
+    n = (len(pairs) + F - 1) // F
+    a = torch.ones(n, 2 * F, dtype=dtype, device="cuda")
+    at = torch.arange(len(pairs), device="cuda")
+    a[at // F, at % F] = pairs[:, 0]
+    a[at // F, F + at % F] = pairs[:, 1]
+    g, u = a[:, :F].double().cpu(), a[:, F:].double().cpu()
+    s = torch.sigmoid(g)
+    # (what passes the type's largest value rounds to an infinity; that rounding is the second half step)
+    v = (g * s * u).to(F32).to(dtype).double()
+    same_kind(bm.silu_mul(a), v, half_step(v, dtype) * 2 + v.abs() * 2.0 ** -20, "h")
+    dh = torch.full((n, F), 0.25, dtype=dtype, device="cuda")
+    da = bm.silu_mul_grad(a, dh)
+    for got, v, size in ((da[:, :F], 0.25 * u * (s * (1 + g * (1 - s))), 0.25 * u.abs() * s * (1 + (g * (1 - s)).abs())),
+                         (da[:, F:], 0.25 * (g * s), 0.25 * (g * s).abs())):
+        v = v.to(F32).to(dtype).double()
+        same_kind(got, v, half_step(v, dtype) * 2 + size * 2.0 ** -20 + 1e-30, "da")
