@@ -408,7 +408,8 @@ int bitsmoe_silu_mul_grad(int dtype, const void* a, int64_t lda, const void* dh,
                           bitsmoe_stream_t stream);
 
 /* Combine: out[t] = sum over j, in slot order, of g[t*k + j] y[slot[t*k + j]]
- * (y: R rows of D; g NULL: weights of 1).  A slot outside [0, R) has no row.
+ * (y: R rows of D; g NULL: weights of 1).  A slot outside [0, R) has a row of
+ * zeros, so the NaN weights of a token without a softmax make out[t] NaN.
  * Gradient: dy[slot] = g dout[t] (rows that no slot names are left as they
  * were; slots must differ), dg[t*k + j] = <dout[t], y[slot]>, 0 without a
  * row (dg NULL: not computed, y not read). */

@@ -686,7 +686,7 @@ def silu_mul_grad(a, dh, da=None, bounds=None, stream=None):
 
 def moe_combine(y, slot, g=None, out=None, stream=None):
     """out (T x D) = sum over j of g[t, j] * y[slot[t, j]], in slot order; a
-    slot of -1 has no row.  out has y's dtype, or float32 where given so."""
+    slot of -1 has a row of zeros.  out has y's dtype, or float32 where given so."""
     T, k = slot.shape
     R, D = y.shape
     dev = _same_device(y, slot, g, out)

@@ -77,7 +77,8 @@ __global__ __launch_bounds__(kThreads) void k_silu_mul_grad(
 constexpr int kSlots = 8;  // slots of a token whose rows are in flight together
 
 // out[t] = sum_j g[t, j] y[slot[t, j]] in slot order, float32 sums.  A slot
-// outside [0, R) has no row.  One work-group takes kThreads * V columns of a
+// outside [0, R) has a row of zeros: the NaN weights of a token that has no
+// softmax make its output NaN.  One work-group takes kThreads * V columns of a
 // token; the rows of kSlots slots are loaded before the first is used.
 template <class T, class O, int V>
 __global__ __launch_bounds__(kThreads) void k_combine_rows(const T* __restrict__ y, int64_t ldy,
@@ -95,11 +96,10 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const T* __restrict__
     for (int u = 0; u < kSlots; ++u) {
       const int s = j0 + u < k ? slot[t * k + j0 + u] : -1;
       const bool there = s >= 0 && s < R;
-      w[u] = 0.f;
+      w[u] = j0 + u < k && g ? g[t * k + j0 + u] : 1.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) row[u][i] = 0.f;
       if (there) {
-        w[u] = g ? g[t * k + j0 + u] : 1.f;
         if constexpr (V == 8)
           load8(y + s * ldy + c, row[u]);
         else

@@ -63,7 +63,10 @@ class ExpertLayer:
     (gate rows first), w2: E x D x F device tensors, float16 or bfloat16 (for
     4-bit experts what ExpertLayer.w4 makes of dense host weights).  Every step
     is one of the library's operators; tokens are grouped by expert once and
-    read in place by the first product.
+    read in place by the first product.  A token whose logits are all -inf gets
+    zeros; one whose logits hold a NaN or +inf gets NaN (out and dlogits; its
+    dx is 0, no
+    expert's weights and no other token's rows see it).
     """
 
     def __init__(self, w1, w2, renorm=True, scale=1.0, group=None):

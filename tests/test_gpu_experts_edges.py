@@ -207,3 +207,41 @@ def test_silu_mul_of_infinities_nan_and_the_largest(bm, dtype, huge, F):
                          (da[:, F:], 0.25 * (g * s), 0.25 * (g * s).abs())):
         v = v.to(F32).to(dtype).double()
         same_kind(got, v, half_step(v, dtype) * 2 + size * 2.0 ** -20 + 1e-30, "da")
+
+
+@pytest.mark.parametrize("D", [64, 37])
+def test_combine_of_missing_rows(bm, D):
+    """A slot without a row adds its weight times 0."""
+    y = normal(rng(1), 6, D, dtype=F16)
+    slot = torch.tensor([[0, -1], [-1, 5], [9, -1], [2, 3]], dtype=torch.int32, device="cuda")
+    g = torch.tensor([[0.5, 0.0], [NAN, 2.0], [0.0, 7.0], [1.0, 1.0]], device="cuda")
+    out = bm.moe_combine(y, slot, g, torch.empty(4, D, device="cuda"))
+    assert torch.equal(out[0], 0.5 * y[0].float()) and not bool(out[2].any()) and bool(out[1].isnan().all())
+    assert torch.equal(out[3], y[2].float() + y[3].float())
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_a_token_without_a_softmax_is_nan(bm, bad):
+    """Its output and its dlogits are; padding is 0 and the other tokens' results
+    are those of the batch without it."""
+    from spectral_expert_gemv_amd import ExpertLayer
+    g = rng(3)
+    T, E, k, D, F = 12, 8, 2, 64, 32
+    x, dout = normal(g, T, D, dtype=BF16), normal(g, T, D, dtype=BF16)
+    w1, w2 = normal(g, E, 2 * F, D, dtype=BF16, scale=0.1), normal(g, E, D, F, dtype=BF16, scale=0.1)
+    logits = normal(g, T, E)
+    logits[7] = -INF
+    other = logits.clone()
+    other[4] = -INF
+    logits[4, 5] = bad
+    keep = torch.arange(T, device="cuda") != 4
+    q = ExpertLayer.w4(w1.float().cpu().numpy(), w2.float().cpu().numpy(), group=32)
+    for layer in (ExpertLayer(w1, w2), q):
+        out, ref = layer.forward(x, logits, k), layer.forward(x, other, k)
+        assert bool(out[4].isnan().all()) and torch.equal(out[keep], ref[keep]) and not bool(out[7].any())
+    layer = ExpertLayer(w1, w2)
+    got, ref = layer.gradients(x, logits, k, dout), layer.gradients(x, other, k, dout)
+    assert bool(got[0][4].isnan().all()) and bool(got[2][4].isnan().all())
+    for a, b in zip(got[:3], ref[:3]):
+        assert torch.equal(a[keep], b[keep])
+    assert torch.equal(got[3], ref[3]) and torch.equal(got[4], ref[4])
