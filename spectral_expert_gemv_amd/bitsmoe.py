@@ -592,7 +592,7 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, ws=None, st
     if act not in ACT or (act and n2 % 2):
         raise ValueError("act=%r with %d rows of w" % (act, n2))
     R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x.shape[0]
-    dev = _same_device(x, w, bounds, y, rows)
+    dev = _same_device(x, w, bounds, y, rows, ws)
     px, ldx = _matrix("x", x, (x.shape[0], K))
     pr, div = _gather(x, rows, div, R)
     if y is None:
@@ -611,7 +611,7 @@ def grouped_matmul_dx(dy, w, bounds, dx=None, ws=None, stream=None):
     sorted rows (of a gathered x, moe_combine adds up a token's rows)."""
     E, N, K = w.shape
     R = dy.shape[0]
-    dev = _same_device(dy, w, bounds, dx)
+    dev = _same_device(dy, w, bounds, dx, ws)
     pd, ldd = _matrix("dy", dy, (R, N))
     if dx is None:
         dx = _new((R, K), dy.dtype, dev, stream)
@@ -630,7 +630,7 @@ def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, ws=None, stream=
     R, N = dy.shape
     K = x.shape[1]
     E = bounds.shape[0] - 1
-    dev = _same_device(dy, x, bounds, dw, rows)
+    dev = _same_device(dy, x, bounds, dw, rows, ws)
     pd, ldd = _matrix("dy", dy)
     px, ldx = _matrix("x", x)
     if x.dtype != dy.dtype:

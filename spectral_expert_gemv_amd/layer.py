@@ -65,8 +65,7 @@ class ExpertLayer:
     is one of the library's operators; tokens are grouped by expert once and
     read in place by the first product.  A token whose logits are all -inf gets
     zeros; one whose logits hold a NaN or +inf gets NaN (out and dlogits; its
-    dx is 0, no
-    expert's weights and no other token's rows see it).
+    dx is 0, and no expert's weights and no other token's rows see it).
     """
 
     def __init__(self, w1, w2, renorm=True, scale=1.0, group=None):

@@ -1,0 +1,32 @@
+"""CPU checks of what the binding of the expert layer's operators refuses by
+itself, with host tensors that say they are on a GPU."""
+import pytest
+
+from spectral_expert_gemv_amd import bitsmoe as bm
+
+torch = pytest.importorskip("torch")
+
+
+class OnGpu(torch.Tensor):
+    def get_device(self):
+        return 0
+
+
+def gpu(*shape, dtype=torch.float16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def products(ws):
+    """The three products with operands that need a workspace (odd sizes)."""
+    b, i32 = gpu(3, dtype=torch.int32), torch.int32
+    x, dy, w = gpu(40, 31), gpu(40, 7), gpu(2, 7, 31)
+    rows = gpu(40, dtype=i32)
+    return [lambda: bm.grouped_matmul(x, w, b, gpu(40, 7), rows=rows, ws=ws),
+            lambda: bm.grouped_matmul_dx(dy, w, b, gpu(40, 31), ws=ws),
+            lambda: bm.grouped_matmul_dw(dy, x, b, gpu(2, 7, 31), ws=ws)]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_a_workspace_on_another_device_is_refused(which):
+    with pytest.raises(ValueError, match="tensors on"):
+        products(torch.zeros(1 << 16, dtype=torch.uint8))[which]()
