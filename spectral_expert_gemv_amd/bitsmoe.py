@@ -477,6 +477,14 @@ def _new(shape, dtype, index, stream, zero=False):
         return make(shape, dtype=dtype, device=dev)
 
 
+def _ws_bytes(ws):
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return _nbytes(ws)
+
+
 def _scratch(nbytes, dev, stream):
     return _new(nbytes, torch.uint8, dev, stream) if nbytes else None
 
@@ -509,7 +517,7 @@ def moe_group(ids, E, bounds=None, order=None, slot=None, ws=None, stream=None):
     if ws is None:
         ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
     _enqueue(_lib.bitsmoe_moe_group, dev, stream, pi, T * k, E, bounds.data_ptr(),
-             order.data_ptr(), slot.data_ptr(), _ptr(ws), 0 if ws is None else _nbytes(ws))
+             order.data_ptr(), slot.data_ptr(), _ptr(ws), _ws_bytes(ws))
     return bounds, order, slot
 
 
@@ -537,7 +545,7 @@ def moe_route(logits, k, ids=None, g=None, renorm=False, scale=1.0, bounds=None,
         if ws is None and T * k:
             ws = _scratch(moe_group_workspace_size(T * k, E), dev, stream)
     _enqueue(_lib.bitsmoe_moe_route, dev, stream, _dtype(logits), pl, ld, T, E, k, int(renorm),
-             scale, pi, pg, pb, po, ps, _ptr(ws), 0 if ws is None else _nbytes(ws))
+             scale, pi, pg, pb, po, ps, _ptr(ws), _ws_bytes(ws))
     return ids, g
 
 
@@ -602,7 +610,7 @@ def grouped_matmul(x, w, bounds, y=None, rows=None, div=1, act=None, ws=None, st
     ws = _matmul_scratch(0, px, ldx, x.shape[0], pw, K, 0, R, E, N, K, code, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul, dev, stream, _dtype(x), px, ldx, x.shape[0], pr, div, pw,
              _bounds(bounds, E), R, E, N, K, code, py, _dtype(y), ldy, _ptr(ws),
-             0 if ws is None else _nbytes(ws))
+             _ws_bytes(ws))
     return y
 
 
@@ -620,7 +628,7 @@ def grouped_matmul_dx(dy, w, bounds, dx=None, ws=None, stream=None):
     ws = _matmul_scratch(1, pd, ldd, R, pw, K, 0, R, E, N, K, 0, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul_dx, dev, stream, _dtype(dy), pd, ldd, pw,
              _bounds(bounds, E), R, E, N, K, px, _dtype(dx), ldx, _ptr(ws),
-             0 if ws is None else _nbytes(ws))
+             _ws_bytes(ws))
     return dx
 
 
@@ -641,8 +649,7 @@ def grouped_matmul_dw(dy, x, bounds, dw=None, rows=None, div=1, ws=None, stream=
     ws = _matmul_scratch(2, pd, ldd, R, px, ldx, x.shape[0], R, E, N, K, 0, ws, dev, stream)
     _enqueue(_lib.bitsmoe_grouped_matmul_dw, dev, stream, _dtype(dy), pd, ldd, px, ldx, x.shape[0],
              pr, div, _bounds(bounds, E), R, E, N, K, _array("dw", dw, dw.dtype, (E, N, K)),
-             _dtype(dw), _ptr(ws),
-             0 if ws is None else _nbytes(ws))
+             _dtype(dw), _ptr(ws), _ws_bytes(ws))
     return dw
 
 

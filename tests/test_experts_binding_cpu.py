@@ -30,3 +30,20 @@ def products(ws):
 def test_a_workspace_on_another_device_is_refused(which):
     with pytest.raises(ValueError, match="tensors on"):
         products(torch.zeros(1 << 16, dtype=torch.uint8))[which]()
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_a_workspace_with_holes_is_refused(which):
+    """Its bytes are not those from its first one on."""
+    ws = gpu(1 << 17, dtype=torch.uint8)[::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        products(ws)[which]()
+
+
+def test_a_grouping_workspace_with_holes_is_refused():
+    ws, i32 = gpu(1 << 17, dtype=torch.int32)[::2], torch.int32
+    out = dict(bounds=gpu(65, dtype=i32), order=gpu(10000, dtype=i32), slot=gpu(5000, 2, dtype=i32), ws=ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        bm.moe_group(gpu(5000, 2, dtype=i32), 64, **out)
+    with pytest.raises(ValueError, match="contiguous"):
+        bm.moe_route(gpu(5000, 64), 2, ids=gpu(5000, 2, dtype=i32), g=gpu(5000, 2, dtype=torch.float32), **out)
