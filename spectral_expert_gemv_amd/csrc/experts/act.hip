@@ -44,10 +44,12 @@ __global__ __launch_bounds__(kThreads) void k_silu_mul(const T* __restrict__ a, 
   }
 }
 
+// (da may be a: a lane reads its elements of a before it writes them to da,
+// and neither pointer promises that they differ)
 template <class T, int V>
 __global__ __launch_bounds__(kThreads) void k_silu_mul_grad(
-    const T* __restrict__ a, int64_t lda, const T* __restrict__ dh, int64_t lddh,
-    const int32_t* __restrict__ bounds, int E, int R, int F, T* __restrict__ da, int64_t ldda) {
+    const T* a, int64_t lda, const T* __restrict__ dh, int64_t lddh,
+    const int32_t* __restrict__ bounds, int E, int R, int F, T* da, int64_t ldda) {
   const int n = live_rows(bounds, E, R);
   const int per = F / V;
   const int64_t total = (int64_t)n * per;
