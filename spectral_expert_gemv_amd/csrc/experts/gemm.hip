@@ -88,12 +88,10 @@ __device__ __align__(16) const uint32_t g_pad[8] = {0,           0,           0,
 // Copies 16 bytes per lane from `src` to LDS at lds + 16 lane.  (The
 // compiler would wait for all such copies before any LDS read, so the copy is
 // an opaque statement without register outputs; the loop below waits for its
-// copies by count.)
+// copies by count.  The LDS address is an operand in m0, so the compiler knows
+// what it holds; the copy may not be the instruction after the one that sets it.)
 __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :
-               : "v"(src), "s"(lds)
-               : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(lds) : "memory");
 }
 // all but the last kLeft copies of the wave have landed
 template <int kLeft>
