@@ -10,6 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+from .oracle_ref import max_rel_err, pairs_ref  # noqa: E402
 from .test_gpu_experts import BF16, F16, F32, STEP, _say, bm, check, half_step, normal, ragged, rng  # noqa: E402,F401
 
 INF, NAN = float("inf"), float("nan")
@@ -245,3 +246,81 @@ def test_a_token_without_a_softmax_is_nan(bm, bad):
     for a, b in zip(got[:3], ref[:3]):
         assert torch.equal(a[keep], b[keep])
     assert torch.equal(got[3], ref[3]) and torch.equal(got[4], ref[4])
+
+
+# ------------------------------------------------------------- together
+
+def test_w4_repeats_streams_and_graphs(bm):
+    """The same bits again, on another stream and from replayed graphs, for
+    experts of one, two, a few and many rows of more than 1024 inputs."""
+    g = rng(21)
+    E, N, K, G = 6, 200, 2048, 64
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(E, N, K // G, generator=g, device="cuda") * 0.02).half()
+    m = (s.float() * (normal(g, *s.shape) - 7.5)).half()
+    for counts in ([1, 2, 2, 0, 5, 13], [1, 2, 40, 0, 70, 16]):
+        bounds, R = ragged(g, E, counts)
+        x = normal(g, R, K, dtype=BF16)
+        ref = bm.w4_matmul(x, codes, s, m, bounds=bounds)
+        sq, md = dequantized(codes, s, m, G)
+        b = bounds.tolist()
+        for e in range(E):
+            r = x[b[e]:b[e + 1]].double()
+            want = r @ (sq + md)[e].t()
+            tol = r.abs() @ (sq + md.abs())[e].t() * ((K + 16) * STEP) + half_step(want, BF16)
+            check(ref[b[e]:b[e + 1]], want, tol, "%d rows" % counts[e])
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        y = bm.w4_matmul(x, codes, s, m, bounds=bounds, stream=side)
+        side.synchronize()
+        assert torch.equal(y, ref)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = bm.w4_matmul(x, codes, s, m, bounds=bounds)
+        for turn in range(3):
+            y.fill_(NAN)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, ref), turn
+            assert torch.equal(bm.w4_matmul(x, codes, s, m, bounds=bounds), ref)
+
+
+@pytest.mark.parametrize("T", [1, 4, 8, 64])
+def test_the_router_in_front_of_the_spectral_path(bm, T):
+    """ids and weights of moe_route go into gate/up and down: a slot without an
+    expert has NaN rows of h and adds nothing, a token without one gives zeros."""
+    import numpy as np
+
+    import synth
+    from oracle import path
+    from oracle.quantize import quantize_expert
+    from spectral_expert_gemv_amd import DeviceLayer
+    _say("router, gate/up, down", T)
+    L = synth.make_layer(synth.LAYERS["tiny"])
+    D, spec = synth.make_down(L), L.spec
+    x, _ = synth.make_batch(synth.workload("tiny_t64"), L, step=2, T=T)
+    logits = normal(rng(T), T, spec.E, dtype=F16)
+    logits[T // 2] = -INF
+    logits[T // 2, 1] = 0.5       # one expert: the second slot is empty
+    if T > 1:
+        logits[T - 1] = -INF      # none
+    ids, g = bm.moe_route(logits, spec.k, renorm=True)
+    assert ids[T // 2].tolist() == [1, -1] and g[T // 2].tolist() == [1.0, 0.0]
+    dev = DeviceLayer.from_synth(L)
+    h = dev.gateup(torch.from_numpy(np.ascontiguousarray(x)).cuda(), ids)
+    assert bool(h[ids < 0].isnan().all()) and bool(h[ids >= 0].isfinite().all())
+    phi16 = np.asarray(D.phi, np.float16)
+    blob = torch.from_numpy(np.ascontiguousarray(bm.pack(D.p, D.a, D.bits))).cuda()
+    phit = torch.from_numpy(np.ascontiguousarray(phi16.T)).cuda()
+    out = bm.moe_down(blob, phit, h, ids, g, spec.E, spec.din, D.phi.shape[1]).cpu().numpy()
+    i, hd = ids.cpu().numpy(), h.cpu().numpy()
+    live = i >= 0
+    pairs = [(int(t), int(j)) for t, j in zip(*np.nonzero(live))]
+    # the bars of the gate/up and the down projection's own tests, by a row's largest value
+    for (t, j), want in pairs_ref(L, x, i, pairs).items():
+        assert max_rel_err(hd[t, j], want) <= 2e-3, (t, j)
+    phat = np.stack([quantize_expert(D.p[e], D.bits[e])["phat"] for e in range(spec.E)])
+    ref = path.moe_down(phi16, D.a, phat, D.bits, np.where(live[:, :, None], hd, 0.0), i, g.cpu().numpy())
+    for t in range(T):
+        assert max_rel_err(out[t], ref[t]) <= 5e-4, t
+    assert T == 1 or not out[T - 1].any()
