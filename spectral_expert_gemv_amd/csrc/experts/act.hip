@@ -203,7 +203,8 @@ int combine_check(int T, int k, int R, int D, int y_dtype, int o_dtype, const vo
                   int64_t ldy, const int32_t* slot, const void* out, int64_t ldo) {
   if (T < 0 || k < 1 || R < 0 || D < 1)
     return fail(BITSMOE_ESHAPE, "T=%d k=%d R=%d D=%d", T, k, R, D);
-  if (T > (1 << 30) / (k < 64 ? 64 : k)) return fail(BITSMOE_ESHAPE, "T=%d k=%d too large", T, k);
+  // (a work-group per token, 2^32 - 1 work-items a grid)
+  if (T > ((1 << 30) - 1) / (k < 64 ? 64 : k)) return fail(BITSMOE_ESHAPE, "T=%d k=%d too large", T, k);
   if (D > (1 << 24)) return fail(BITSMOE_ESHAPE, "D=%d too large", D);
   if (!is_half(y_dtype) || (o_dtype != y_dtype && o_dtype != BITSMOE_F32))
     return fail(BITSMOE_EINVAL, "y dtype %d, out dtype %d", y_dtype, o_dtype);

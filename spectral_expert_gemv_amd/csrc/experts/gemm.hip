@@ -753,7 +753,9 @@ int launch_mm(MmArgs s, int dtype, int o_dtype, int64_t a_rows, void* ws, size_t
   const long long ntn = (cols + per - 1) / per;
   const long long mt =
       MODE == kDw ? (long long)s.E * ((s.N + kTile - 1) / kTile) : max_tiles(s.R, s.E, kTile);
-  if (mt * ntn > 0x1FFFFFFFll)
+  // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
+  const long long groups = (mt * ntn + kUnits - 1) / kUnits * kUnits + kUnits + 8;
+  if (groups * 512 > 0xFFFFFFFFll)  // (a grid's work-items)
     return fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", s.R, s.E, s.N, s.K);
   int rc = BITSMOE_OK;
   if (p.a &&
@@ -777,8 +779,7 @@ int launch_mm(MmArgs s, int dtype, int o_dtype, int64_t a_rows, void* ws, size_t
         return;
       }
     }
-    // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
-    const dim3 grid((unsigned)((mt * ntn + kUnits - 1) / kUnits * kUnits + kUnits + 8));
+    const dim3 grid((unsigned)groups);
     if (MODE == kFwd && s.act)
       hipLaunchKernelGGL((k_mm_tile<T, O, MODE, MODE == kFwd>), grid, dim3(512), 0, st, s);
     else

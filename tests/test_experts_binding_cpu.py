@@ -4,6 +4,8 @@ import pytest
 
 from spectral_expert_gemv_amd import bitsmoe as bm
 
+from .test_experts_cpu import combine, combine_grad, matmul, matmul_dx
+
 torch = pytest.importorskip("torch")
 
 
@@ -47,3 +49,13 @@ def test_a_grouping_workspace_with_holes_is_refused():
         bm.moe_group(gpu(5000, 2, dtype=i32), 64, **out)
     with pytest.raises(ValueError, match="contiguous"):
         bm.moe_route(gpu(5000, 64), 2, ids=gpu(5000, 2, dtype=i32), g=gpu(5000, 2, dtype=torch.float32), **out)
+
+
+@pytest.mark.parametrize("call, sizes", [
+    # 65790 row tiles x 128 column tiles of 512 lanes; as many tokens as 256-lane work-groups pass 2^32 lanes
+    (matmul, dict(E=65535, R=65535, x_rows=65535, N=32768, ldy=32768)),
+    (matmul_dx, dict(E=65535, R=65535, K=32768, lddx=32768)),
+    (combine, dict(T=1 << 24)), (combine_grad, dict(T=1 << 24)),
+])
+def test_what_no_grid_takes_is_refused(call, sizes):
+    assert call(**sizes) == bm.ESHAPE
