@@ -327,9 +327,11 @@ int bitsmoe_ssd(const float* W, int E, int dout, int din, int r, float* phi, flo
  * operands' type or BITSMOE_F32.  Row strides (ld*) are in elements; the
  * elements of a row are contiguous.  Pointers need the alignment of their
  * element type; rows that are 16-byte aligned (pointer, stride and sizes) are
- * the fast case.  All calls are asynchronous on `stream` and may be captured
- * into a graph.  Sums, softmax and norms are float32; each output is rounded
- * once. */
+ * the fast case.  T < 2^24 tokens (T k < 2^30), R <= 2^26 rows, E <= 65535
+ * experts (2048 to route or group), N and K <= 2^20, D <= 2^24; sizes whose
+ * work-groups no grid takes are refused.  All calls are asynchronous on
+ * `stream` and may be captured into a graph.  Sums, softmax and norms are
+ * float32; each output is rounded once. */
 #define BITSMOE_F32  0
 #define BITSMOE_F16  1
 #define BITSMOE_BF16 2

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_grad(
 }
 
 unsigned elem_grid(int64_t work) {
-  // 256 compute units, 8 work-groups each, then a loop over the rest
+  // 256 compute units, 16 work-groups each, then a loop over the rest
   const int64_t b = (work + kThreads - 1) / kThreads;
   return (unsigned)(b < 1 ? 1 : b > 4096 ? 4096 : b);
 }

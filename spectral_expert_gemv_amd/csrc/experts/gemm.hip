@@ -450,8 +450,8 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 }
 
 // Bound by the matrix cores and the copies that feed them: 8 experts of
-// 4096 x 14336 with 1024 rows each, forward 745 us (1290 TFLOP/s), dx 830, dw
-// (1.9 GB of float32 written) 1095.
+// 4096 x 14336 with 1024 rows each, forward 745 us (1290 TFLOP/s), dx 745, dw
+// (1.9 GB of float32 written) 1045.
 //
 // One work-group per tile: first the whole rounds of the chip's compute units
 // with 256 x 256 tiles, then what is left: cut in four 128 x 128 tiles where

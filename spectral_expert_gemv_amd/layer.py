@@ -126,6 +126,8 @@ class ExpertLayer:
         dw2 = bm.grouped_matmul_dw(dy, h, bounds, stream=s)
         da = bm.silu_mul_grad(a, dh, bounds=bounds, stream=s)
         dw1 = bm.grouped_matmul_dw(da, x, bounds, rows=order, div=k, stream=s)
+        # (a sorted row's dx is rounded to x's type before a token's rows are added up in
+        # float32: half the bytes of float32 rows, at half a step of each term)
         dx = bm.moe_combine(bm.grouped_matmul_dx(da, self.w1, bounds, stream=s), slot, stream=s)
         dlogits = bm.moe_route_grad(logits, ids, dg, renorm=self.renorm, scale=self.scale, stream=s)
         return out, dx, dlogits, dw1, dw2
