@@ -324,3 +324,40 @@ def test_the_router_in_front_of_the_spectral_path(bm, T):
     for t in range(T):
         assert max_rel_err(out[t], ref[t]) <= 5e-4, t
     assert T == 1 or not out[T - 1].any()
+
+
+@pytest.mark.parametrize("counts, N, K", [([3, 0, 5], 40, 136), ([3, 0, 5], 33, 101), ([150, 0, 300], 40, 136), ([150, 0, 300], 33, 101),
+                                          ([700, 1, 260], 264, 328)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_products_of_infinities_and_nan(bm, counts, N, K, dtype):
+    """They reach the outputs that their rows reach, and no others: not by the
+    rows and columns that fill up a tile."""
+    _say("products of infinities", counts, N, K, dtype)
+    g = rng(K)
+    bounds, R = ragged(g, 3, counts, tail=2)
+    n = R - 2
+    x, dy, w = normal(g, R, K, dtype=dtype), normal(g, R, N, dtype=dtype), normal(g, 3, N, K, dtype=dtype)
+    x[n:] = dy[n:] = NAN
+    rows = {0: (K - 1, INF), counts[0] - 1: (K // 2, -INF), n - 1: (0, NAN)}
+    good = bm.grouped_matmul(x, w, bounds), bm.grouped_matmul_dx(dy, w, bounds), bm.grouped_matmul_dw(dy, x, bounds)
+    xb, dyb = x.clone(), dy.clone()
+    for r, (c, v) in rows.items():
+        xb[r, c] = dyb[r, c % N] = v
+    y, dx = bm.grouped_matmul(xb, w, bounds), bm.grouped_matmul_dx(dyb, w, bounds)
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    keep[n:] = False
+    for r in rows:
+        keep[r] = False
+        e = 0 if r < counts[0] else 2
+        for got, a, m in ((y, xb, w[e]), (dx, dyb, w[e].t())):
+            want = (m.double().cpu() * a[r].double().cpu()).sum(1)  # no product is 0 but by chance
+            same_kind(got[r], want, torch.zeros_like(want), "row %d" % r)
+    assert torch.equal(y[keep], good[0][keep]) and torch.equal(dx[keep], good[1][keep])
+    # dw: the columns of x, or the rows of dy, that hold them, of their experts alone
+    for a, b, axis in ((dy, xb, 1), (dyb, x, 0)):
+        dw = bm.grouped_matmul_dw(a, b, bounds)
+        hit = torch.zeros_like(dw, dtype=torch.bool)
+        for r, (c, v) in rows.items():
+            e = 0 if r < counts[0] else 2
+            hit[e].select(axis, c if axis else c % N).fill_(True)
+        assert not bool(dw[hit].isfinite().any()) and torch.equal(dw[~hit], good[2][~hit])
