@@ -339,7 +339,7 @@ def _e4m3(v):
     """The nearest e4m3 number (64 bits, ties to even) of values up to 448; NaN where v is not finite."""
     a = v.abs()
     exp = (torch.frexp(torch.where(torch.isfinite(a), a, 1.0))[1] - 1).clamp(min=-6)
-    step = torch.ldexp(torch.ones_like(a), exp - 3)
+    step = ((exp.long() + (1023 - 3)) << 52).view(torch.float64)  # 2^(exp - 3) by its bits (torch.ldexp is a step off)
     return torch.where(torch.isfinite(a), torch.copysign(torch.round(a / step) * step, v), math.nan)
 
 
