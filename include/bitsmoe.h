@@ -335,6 +335,7 @@ int bitsmoe_ssd(const float* W, int E, int dout, int din, int r, float* phi, flo
 #define BITSMOE_F32  0
 #define BITSMOE_F16  1
 #define BITSMOE_BF16 2
+#define BITSMOE_E4M3 3  /* OCP 8-bit floating point: rows of bitsmoe_fp8_matmul alone */
 
 #define BITSMOE_ACT_NONE     0
 #define BITSMOE_ACT_SILU_MUL 1
@@ -446,6 +447,84 @@ int bitsmoe_w4_matmul(int dtype, const void* x, int64_t ldx, int x_rows, const i
                       int y_dtype, int64_t ldy, bitsmoe_stream_t stream);
 int bitsmoe_w4_pack(const float* w, int64_t rows, int K, int G, uint8_t* codes, uint16_t* scales,
                     uint16_t* mins);
+
+/* 8-bit floating point (OCP e4m3) with a float32 scale per group: 128
+ * consecutive elements of a row, or a block of 128 x 128 weights (the last of
+ * an axis may be short).  With a the largest finite magnitude of the group, in
+ * IEEE float32 steps:
+ *   scale = a / 448, code = e4m3(v * (448 / a)), to nearest even
+ * (both factors 1 where a < 2^-80: codes of 0); a value that is not finite
+ * gets the code of NaN.  Rows of codes are filled up with codes of 0 to whole
+ * groups: K' = 128 ceil(K / 128) bytes; rows of codes are 16-byte aligned
+ * (pointer and stride).
+ * bitsmoe_fp8_rows: R rows of K (F32, F16 or BF16; with BITSMOE_ACT_SILU_MUL
+ * rows [gate | up] of 2 K, of which SiLU(gate) * up is quantized as it is in
+ * float32) to rows of codes (stride ldc >= K') and scales (stride
+ * lds >= K' / 128).  bounds (may be NULL, with E): only rows below bounds[E]
+ * are read and written.
+ * bitsmoe_fp8_weights: E x N x K weights (contiguous; F32, F16 or BF16) to
+ * codes E x N x K' and scales E x ceil(N / 128) x K' / 128; with codes_t and
+ * scales_t (both or none) also the same values transposed, E x K x N' and
+ * E x ceil(K / 128) x N' / 128, the weights of a product's dx.  N, K <= 2^21;
+ * at most 2^24 - 1 blocks. */
+int bitsmoe_fp8_rows(int dtype, const void* x, int64_t ldx, int act, const int32_t* bounds, int R,
+                     int E, int K, void* codes, int64_t ldc, float* scales, int64_t lds,
+                     bitsmoe_stream_t stream);
+int bitsmoe_fp8_weights(int dtype, const void* w, int E, int N, int K, void* codes, float* scales,
+                        void* codes_t, float* scales_t, bitsmoe_stream_t stream);
+
+/* Products by expert with 8-bit weights (codes, scales as above):
+ *   y[i, n] = sum over groups g of sx[i, g] sw[n / 128, g] <codes of both in g>
+ * or SiLU(gate) * up of it: with BITSMOE_ACT_SILU_MUL codes are E x 2N x K',
+ * gate rows first, and scales E x 2 ceil(N / 128) x K' / 128: the halves are
+ * quantized each by itself (as 2E matrices of N rows).
+ * x: rows of K, F16 or BF16, quantized on the way as by bitsmoe_fp8_rows (y
+ * has their type or is F32), or BITSMOE_E4M3 rows of K' codes with x_scales
+ * (stride ldxs; y of any type).  y, rows, div, bounds as for
+ * bitsmoe_grouped_matmul; bounds NULL (E = 1): one dense projection of all R
+ * rows.  dx of a product: the call with dy's rows and the transposed weights.
+ * Each group's sum is taken by the matrix cores, the sum over groups in
+ * float32; a group's two scales are multiplied in float32 first.
+ * ws: at least bitsmoe_fp8_matmul_workspace_size() bytes, 256-byte aligned, 0
+ * for rows of codes and for few rows (ws may then be NULL). */
+int bitsmoe_fp8_matmul_workspace_size(int x_dtype, int x_rows, int R, int E, int N, int K, int act,
+                                      size_t* bytes);
+int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_scales, int64_t ldxs,
+                       int x_rows, const int32_t* rows, int div, const void* codes,
+                       const float* scales, const int32_t* bounds, int R, int E, int N, int K,
+                       int act, void* y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                       bitsmoe_stream_t stream);
+
+/* The router's balance.  logits: T rows of E (F32, F16 or BF16), ids: T x k
+ * (of bitsmoe_moe_route).  Sequence s is the tokens [seqs[s], seqs[s + 1])
+ * (S + 1 int32 on the device; NULL with S = 1: all tokens).  A token takes part
+ * if one of its ids lies in [0, E) and one of its logits is above -inf; what
+ * the logits of the others hold does not matter.  Over a sequence's n tokens
+ * that do, with p = softmax(logits):
+ *   counts[s, e] = #{(t, j): id = e},  f_e = E / (k n) counts[s, e]
+ *   loss[s] = sum_e f_e 1/n sum_t p_te,  z[s] = 1/n sum_t (log sum_e exp l_te)^2
+ *   tokens[s] = n (loss and z are 0 where that is 0)
+ * A NaN or +inf among the logits of a token that takes part makes its
+ * sequence's losses NaN.
+ * bitsmoe_moe_balance_grad: the gradient of sum_s dloss[s] loss[s] + dz[s] z[s]
+ * (either may be NULL: 0) with respect to the logits, f held fixed, from the
+ * forward call's counts and tokens:
+ *   dl_te = p_te (dloss / n (f_e - sum_m p_tm f_m) + 2 dz / n lse_t),
+ * 0 for tokens that take no part; `add`: added to what dlogits holds.  Rows of
+ * tokens in no sequence are neither read nor written.  E <= 2048, k <= 64,
+ * T <= 2^24, S <= 65535.  ws: bitsmoe_moe_balance_workspace_size() bytes, 4-byte
+ * aligned; its contents carry nothing between calls.  The sums do not depend on
+ * an order of atomics. */
+int bitsmoe_moe_balance_workspace_size(int T, int E, int S, size_t* bytes);
+int bitsmoe_moe_balance(int dtype, const void* logits, int64_t ld, const int32_t* ids,
+                        const int32_t* seqs, int S, int T, int E, int k, float* loss, float* z,
+                        int32_t* counts, int32_t* tokens, void* ws, size_t ws_bytes,
+                        bitsmoe_stream_t stream);
+int bitsmoe_moe_balance_grad(int dtype, const void* logits, int64_t ld, const int32_t* ids,
+                             const int32_t* seqs, int S, int T, int E, int k,
+                             const int32_t* counts, const int32_t* tokens, const float* dloss,
+                             const float* dz, int add, void* dlogits, int64_t ldd,
+                             bitsmoe_stream_t stream);
 
 /* Zero-fills a workspace with a kernel (no memset node), on `stream`. */
 int bitsmoe_workspace_init(void* ws, size_t ws_bytes, bitsmoe_stream_t stream);

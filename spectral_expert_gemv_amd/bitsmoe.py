@@ -95,6 +95,16 @@ _SIGS = {
     "bitsmoe_w4_matmul": ([_i, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i,
                            _vp, _i, _i64, _vp], _i),
     "bitsmoe_w4_pack": ([_vp, _i64, _i, _i, _vp, _vp, _vp], _i),
+    "bitsmoe_fp8_rows": ([_i, _vp, _i64, _i, _vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp], _i),
+    "bitsmoe_fp8_weights": ([_i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp], _i),
+    "bitsmoe_fp8_matmul_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _psz], _i),
+    "bitsmoe_fp8_matmul": ([_i, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i,
+                            _i, _vp, _i, _i64, _vp, _sz, _vp], _i),
+    "bitsmoe_moe_balance_workspace_size": ([_i, _i, _i, _psz], _i),
+    "bitsmoe_moe_balance": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz,
+                             _vp], _i),
+    "bitsmoe_moe_balance_grad": ([_i, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i,
+                                  _vp, _i64, _vp], _i),
     "bitsmoe_ssd": ([_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _pi, _i, _vp, _sz, _vp], _i),
 }
 FQCM_WS_BYTES = 1024 + 65536 * 24
@@ -777,3 +787,187 @@ def w4_matmul(x, codes, scales, mins=None, y=None, bounds=None, rows=None, div=1
              K // groups, None if bounds is None else _bounds(bounds, E), R, E, N, K, ACT[act], py,
              _dtype(y), ldy)
     return y
+
+
+_F8 = torch.float8_e4m3fn
+GROUP = 128  # elements with one scale
+
+
+def _groups(n):
+    return -(-n // GROUP)
+
+
+def fp8_rows(x, codes=None, scales=None, act=None, bounds=None, stream=None):
+    """(codes R x K', scales R x K'/128) of rows x (R x K): e4m3 values with a
+    float32 scale for each 128 elements, K' = K rounded up to whole groups.
+    With act="silu_mul" of SiLU(gate) * up of rows x = [gate | up] (R x 2K).
+    With bounds only the experts' rows."""
+    R, K = x.shape
+    if act not in ACT or (act and K % 2):
+        raise ValueError("act=%r with %d columns of x" % (act, K))
+    K = K // 2 if act else K
+    G = _groups(K)
+    dev = _same_device(x, codes, scales, bounds)
+    px, ldx = _matrix("x", x)
+    if codes is None:
+        codes = _new((R, G * GROUP), _F8, dev, stream)
+    if scales is None:
+        scales = _new((R, G), _F32, dev, stream)
+    if codes.dtype is not _F8 or scales.dtype is not _F32:
+        raise ValueError("codes must be %s and scales float32" % _F8)
+    pc, ldc = _matrix("codes", codes, (R, G * GROUP))
+    ps, lds = _matrix("scales", scales, (R, G))
+    E = 0 if bounds is None else bounds.shape[0] - 1
+    _enqueue(_lib.bitsmoe_fp8_rows, dev, stream, _dtype(x), px, ldx, ACT[act],
+             None if bounds is None else _bounds(bounds, E), R, E, K, pc, ldc, ps, lds)
+    return codes, scales
+
+
+def fp8_weights(w, codes=None, scales=None, codes_t=None, scales_t=None, transposed=False,
+                stream=None):
+    """(codes E x N x K', scales E x N'/128 x K'/128) of weights w (E x N x K):
+    e4m3 values with a float32 scale for each block of 128 x 128.  With
+    transposed=True (or codes_t, scales_t given) also (codes_t E x K x N',
+    scales_t E x K'/128 x N'/128), the weights of a product's dx."""
+    E, N, K = w.shape
+    kg, ng = _groups(K), _groups(N)
+    if (codes_t is None) != (scales_t is None):
+        raise ValueError("codes_t and scales_t go together")
+    transposed = transposed or codes_t is not None
+    dev = _same_device(w, codes, scales, codes_t, scales_t)
+    if codes is None:
+        codes = _new((E, N, kg * GROUP), _F8, dev, stream)
+    if scales is None:
+        scales = _new((E, ng, kg), _F32, dev, stream)
+    if transposed and codes_t is None:
+        codes_t = _new((E, K, ng * GROUP), _F8, dev, stream)
+        scales_t = _new((E, kg, ng), _F32, dev, stream)
+    _enqueue(_lib.bitsmoe_fp8_weights, dev, stream, _dtype(w), _array("w", w, w.dtype), E, N, K,
+             _array("codes", codes, _F8, (E, N, kg * GROUP)),
+             _array("scales", scales, _F32, (E, ng, kg)),
+             _array("codes_t", codes_t, _F8, (E, K, ng * GROUP)) if transposed else None,
+             _array("scales_t", scales_t, _F32, (E, kg, ng)) if transposed else None)
+    return (codes, scales, codes_t, scales_t) if transposed else (codes, scales)
+
+
+@functools.lru_cache(maxsize=256)
+def fp8_matmul_workspace_size(x_dtype, x_rows, R, E, N, K, act=None):
+    """Bytes that fp8_matmul needs for these sizes (x_dtype: x's)."""
+    out = ctypes.c_size_t(0)
+    _check(_lib.bitsmoe_fp8_matmul_workspace_size(3 if x_dtype is _F8 else _DTYPES[x_dtype], x_rows, R,
+                                                  E, N, K, ACT[act], ctypes.byref(out)))
+    return out.value
+
+
+def fp8_matmul(x, codes, scales, y=None, x_scales=None, bounds=None, rows=None, div=1, act=None,
+               ws=None, stream=None):
+    """y (R x N) = W x with the 8-bit weights that fp8_weights makes: codes E x
+    N x K' (or N x K' for one dense projection), scales a float32 for each
+    block of 128 x 128.  x: float16 or bfloat16 rows of K, quantized on the way,
+    or rows of codes (R x K') with x_scales, as by fp8_rows.  With
+    act="silu_mul" codes are E x 2N x K' (gate rows first) and scales E x 2
+    N'/128 x K'/128, the halves quantized as 2E matrices of N rows.  bounds, rows
+    and div as for grouped_matmul (bounds may be None when E is 1).  y has x's
+    dtype (bfloat16 for codes), or another where it is given so: float32, for
+    codes any.  The gradient of the rows: fp8_matmul(dy, codes_t, scales_t,
+    bounds=bounds)."""
+    if codes.dim() == 2:
+        codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+    E, n2, kp = codes.shape
+    N = n2 // 2 if act else n2
+    if act not in ACT or (act and n2 % 2):
+        raise ValueError("act=%r with %d rows of codes" % (act, n2))
+    x_rows, K = x.shape
+    given = x.dtype is _F8
+    if given != (x_scales is not None):
+        raise ValueError("rows of codes and x_scales go together")
+    if kp % GROUP or _groups(K) * GROUP != kp:
+        raise ValueError("x has %d inputs, the weights %d" % (K, kp))
+    R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x_rows
+    dev = _same_device(x, codes, scales, y, x_scales, bounds, rows, ws)
+    px, ldx = _matrix("x", x, (x_rows, kp) if given else None)
+    ps, lds = None, 0
+    if given:
+        if x_scales.dtype is not _F32:
+            raise ValueError("x_scales must be float32")
+        ps, lds = _matrix("x_scales", x_scales, (x_rows, kp // GROUP))
+    pr, div = _gather(x, rows, div, R)
+    if y is None:
+        y = _new((R, N), torch.bfloat16 if given else x.dtype, dev, stream)
+    py, ldy = _matrix("y", y, (R, N))
+    if ws is None:
+        ws = _scratch(fp8_matmul_workspace_size(x.dtype, x_rows, R, E, N, K, act), dev, stream)
+    _enqueue(_lib.bitsmoe_fp8_matmul, dev, stream, 3 if given else _dtype(x), px, ldx, ps, lds, x_rows,
+             pr, div, _array("codes", codes, _F8),
+             _array("scales", scales, _F32, (E, _groups(N) * (2 if act else 1), kp // GROUP)),
+             None if bounds is None else _bounds(bounds, E), R, E, N, K, ACT[act], py, _dtype(y),
+             ldy, _ptr(ws), _ws_bytes(ws))
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def moe_balance_workspace_size(T, E, S=1):
+    out = ctypes.c_size_t(0)
+    _check(_lib.bitsmoe_moe_balance_workspace_size(T, E, S, ctypes.byref(out)))
+    return out.value
+
+
+def _sequences(seqs):
+    if seqs is None:
+        return None, 1
+    S = seqs.shape[0] - 1
+    return _array("seqs", seqs, _I32, (S + 1,)), S
+
+
+def moe_balance(logits, ids, seqs=None, loss=None, z=None, counts=None, tokens=None, ws=None,
+                stream=None):
+    """(loss S, z S, counts S x E int32, tokens S int32) of logits (T x E) and
+    the ids (T x k int32) that moe_route gave for them, for each sequence of
+    tokens [seqs[s], seqs[s + 1]) (seqs: S + 1 int32; None: one of all tokens).
+    Over the n tokens with an id of the experts' and a logit above -inf: counts
+    of each expert's pairs, loss = sum_e f_e mean_t p_te with f_e = E counts_e /
+    (k n) and p = softmax(logits) (1 for a perfect balance), z = the mean of the
+    squared logarithm of sum_e exp(logits)."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    dev = _same_device(logits, ids, seqs, loss, z, counts, tokens, ws)
+    pl, ld = _matrix("logits", logits)
+    pq, S = _sequences(seqs)
+    loss = _new(S, _F32, dev, stream) if loss is None else loss
+    z = _new(S, _F32, dev, stream) if z is None else z
+    counts = _new((S, E), _I32, dev, stream) if counts is None else counts
+    tokens = _new(S, _I32, dev, stream) if tokens is None else tokens
+    if ws is None:
+        ws = _scratch(moe_balance_workspace_size(T, E, S), dev, stream)
+    _enqueue(_lib.bitsmoe_moe_balance, dev, stream, _dtype(logits), pl, ld,
+             _array("ids", ids, _I32, (T, k)), pq, S, T, E, k, _array("loss", loss, _F32, (S,)),
+             _array("z", z, _F32, (S,)), _array("counts", counts, _I32, (S, E)),
+             _array("tokens", tokens, _I32, (S,)), _ptr(ws), _ws_bytes(ws))
+    return loss, z, counts, tokens
+
+
+def moe_balance_grad(logits, ids, counts, tokens, dloss=None, dz=None, seqs=None, dlogits=None,
+                     add=False, stream=None):
+    """dlogits (T x E, the logits' dtype): the gradient of sum_s dloss[s] *
+    loss[s] + dz[s] * z[s] (float32 on the device; None: 0) from moe_balance's
+    counts and tokens, the counts held fixed.  Tokens that take no part get 0;
+    rows in no sequence are left as they were (0 in a new dlogits).  add: added
+    to what dlogits holds, as moe_route_grad's result."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    dev = _same_device(logits, ids, counts, tokens, dloss, dz, seqs, dlogits)
+    pl, ld = _matrix("logits", logits)
+    pq, S = _sequences(seqs)
+    if dlogits is None:
+        if add:
+            raise ValueError("add without dlogits")
+        dlogits = _new((T, E), logits.dtype, dev, stream, zero=seqs is not None)
+    if dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must have the logits' dtype")
+    pd, ldd = _matrix("dlogits", dlogits, (T, E))
+    _enqueue(_lib.bitsmoe_moe_balance_grad, dev, stream, _dtype(logits), pl, ld,
+             _array("ids", ids, _I32, (T, k)), pq, S, T, E, k,
+             _array("counts", counts, _I32, (S, E)), _array("tokens", tokens, _I32, (S,)),
+             None if dloss is None else _array("dloss", dloss, _F32, (S,)),
+             None if dz is None else _array("dz", dz, _F32, (S,)), int(add), pd, ldd)
+    return dlogits

@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 HOST_SOURCES = ["common.cpp", "pack.cpp", "experts/w4_pack.cpp"]
 HIP_SOURCES = ["bitsmoe.hip", "fused.hip", "one.hip", "grouped.hip", "pack_gpu.hip", "fqcm.hip", "down.hip", "ssd.hip",
-               "experts/route.hip", "experts/act.hip", "experts/gemm.hip", "experts/w4.hip"]
+               "experts/route.hip", "experts/act.hip", "experts/gemm.hip", "experts/w4.hip",
+               "experts/fp8.hip", "experts/fp8_mm.hip", "experts/balance.hip"]
 
 HIP_FLAGS = [
     "-x", "hip", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",

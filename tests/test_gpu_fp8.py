@@ -1,0 +1,438 @@
+"""GPU tests of the 8-bit floating point operators against plain 64-bit
+implementations.
+
+The quantizers' definition is exact in IEEE float32 steps, so their codes and
+scales are equal to the oracle's (in 64 bits, where a product of two float32
+numbers is exact and a quotient rounds to the same float32 number).  Products:
+half a step of the output's type, plus (K + 16) 2^-23 of the sum of the
+magnitudes for a float32 sum of K products (every addition off by at most one
+step, whatever the order; the 16 for a group's product of scales and its two
+multiplications), plus 2^-20 for SiLU.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32, F64, F8 = torch.float16, torch.bfloat16, torch.float32, torch.float64, torch.float8_e4m3fn
+STEP = 2.0 ** -23
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def bm():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from spectral_expert_gemv_amd import bitsmoe
+    return bitsmoe
+
+
+def _say(*a):
+    print(*a, flush=True)
+
+
+def rng(seed):
+    g = torch.Generator("cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def half_step(v, dtype):
+    t = v.abs() * (torch.finfo(dtype).eps / 2)
+    return t + 2.0 ** -25 if dtype == F16 else t
+
+
+def check(got, want, tol, what=""):
+    got = got.double()
+    bad = ~((got - want).abs() <= tol)
+    assert not bool(bad.any()), "%s: %d of %d off, worst %.3g of tol" % (
+        what, int(bad.sum()), bad.numel(), float(((got - want).abs() / tol.clamp(min=1e-300)).nan_to_num(1e9).max()))
+
+
+def up(n):
+    return -(-n // 128) * 128
+
+
+def e4m3(v):
+    """Nearest e4m3 numbers, ties to even; NaN where v is not finite."""
+    a = v.abs()
+    exp = (torch.frexp(torch.where(a.isfinite(), a, torch.ones_like(a)))[1] - 1).clamp(min=-6)
+    step = ((exp.long() + (1023 - 3)) << 52).view(F64)  # 2^(exp - 3) by its bits: torch.ldexp's is a step off
+    return torch.where(a.isfinite(), torch.copysign(torch.round(a / step) * step, v), torch.full_like(a, NAN))
+
+
+def quantized(v, high):
+    """(codes' values, scales) of groups of high x 128 of a 64-bit matrix whose rows are whole groups or are filled up."""
+    r, c = v.shape
+    full = torch.zeros(-(-r // high) * high, up(c), dtype=F64, device=v.device)
+    full[:r, :c] = v
+    g = full.reshape(-1, high, up(c) // 128, 128)
+    a = torch.where(g.isfinite(), g, torch.zeros_like(g)).abs().amax((1, 3), keepdim=True)
+    s, f = torch.ones_like(a), torch.ones_like(a)
+    big = a >= 2.0 ** -80
+    top = torch.full_like(a[big], 448.0)
+    s[big], f[big] = (a[big] / top).float().double(), (top / a[big]).float().double()
+    q = e4m3((g * f).float().double())
+    return q.reshape(full.shape)[:r], s[:, 0, :, 0]
+
+
+def same(got, want, what=""):
+    """Equal numbers, NaN where the other has it."""
+    got = got.double()
+    ok = (got == want) | (got.isnan() & want.isnan())
+    assert bool(ok.all()), "%s: %d of %d differ" % (what, int((~ok).sum()), ok.numel())
+
+
+def values(codes, scales, high):
+    return codes.double() * scales.double().repeat_interleave(high, 0)[: codes.shape[0]].repeat_interleave(128, 1)
+
+
+# ------------------------------------------------------------------ rows
+
+LAYOUTS = {"plain": (0, 0), "strided": (8, 0), "shifted": (9, 3)}
+
+
+@pytest.mark.parametrize("R, K", [(1, 1), (1, 128), (3, 129), (32, 2048), (67, 768), (5, 1000), (1000, 1408), (4097, 64), (2, 4133)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_rows(bm, R, K, dtype, layout):
+    _say("fp8 rows", R, K, dtype, layout)
+    g = rng(R + K)
+    pad, at = LAYOUTS[layout]
+    x = normal(g, R, K + pad, dtype=F32, scale=3.0)
+    x *= torch.exp2(torch.randint(-14, 12, (R, 1), generator=g, device="cuda").float())  # subnormal fp16 rows among them
+    x[R // 2, : min(200, K)] = 0.0
+    x = x.to(dtype)[:, at:at + K]
+    codes, scales = bm.fp8_rows(x)
+    assert codes.dtype == F8 and codes.shape == (R, up(K)) and scales.shape == (R, up(K) // 128)
+    q, s = quantized(x.double(), 1)
+    same(codes, q, "codes")
+    same(scales, s, "scales")
+    # into rows of another stride, what lies beside them left as it was
+    big = torch.full((R, up(K) + 32), 7.0, device="cuda").to(F8)
+    bs = torch.full((R, up(K) // 128 + 3), 7.0, device="cuda")
+    c2, s2 = bm.fp8_rows(x, big[:, 16:16 + up(K)], bs[:, 1:1 + up(K) // 128])
+    assert torch.equal(c2.float(), codes.float()) and torch.equal(s2, scales)
+    assert bool((big[:, :16].float() == 7.0).all()) and bool((big[:, 16 + up(K):].float() == 7.0).all())
+    assert bool((bs[:, 0] == 7.0).all()) and bool((bs[:, 1 + up(K) // 128:] == 7.0).all())
+
+
+def test_rows_every_float16_value(bm):
+    """Every finite fp16 number in a group with 448, whose factors are 1: the conversion alone, its ties and subnormals."""
+    v = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32, device="cuda").to(torch.int16).view(F16)
+    v = v[v.isfinite() & (v.abs() <= 448)]
+    n = v.numel() // 127 * 127
+    x = torch.cat([torch.full((n // 127, 1), 448.0, dtype=F16, device="cuda"), v[:n].reshape(-1, 127)], 1)
+    codes, scales = bm.fp8_rows(x)
+    assert bool((scales == 1).all())
+    same(codes, e4m3(x.double()), "codes")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_rows_of_infinities_nan_and_extremes(bm, dtype):
+    g = rng(3)
+    x = normal(g, 12, 300, dtype=dtype)
+    top = torch.finfo(dtype).max
+    x[0, 5], x[1, 130], x[2, 299] = INF, -INF, NAN
+    x[3, :] = NAN
+    x[4, :128] = INF
+    x[5, 0], x[5, 1] = top, -top
+    x[6, :] = torch.finfo(dtype).tiny
+    x[7, :] = torch.finfo(dtype).smallest_normal * 0.25
+    x[8, :] = 0.0
+    x[9, :] = -0.0
+    x[10, :] = 2.0 ** -80 if dtype != F16 else 0.0
+    x[11, :] = 2.0 ** -80 * 0.99 if dtype != F16 else 0.0
+    codes, scales = bm.fp8_rows(x)
+    q, s = quantized(x.double(), 1)
+    same(codes, q, "codes")
+    same(scales, s, "scales")
+    assert bool(scales.isfinite().all())
+
+
+@pytest.mark.parametrize("R, F", [(1, 1), (5, 7), (67, 768), (300, 1408), (33, 333)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_rows_of_the_activation(bm, R, F, dtype, layout):
+    _say("fp8 rows of silu", R, F, dtype, layout)
+    g = rng(R + F)
+    pad, at = LAYOUTS[layout]
+    a = normal(g, R, 2 * F + pad, dtype=dtype, scale=3.0)[:, at:at + 2 * F]
+    codes, scales = bm.fp8_rows(a, act="silu_mul")
+    x, u = a.double()[:, :F], a.double()[:, F:]
+    h = torch.zeros(R, up(F), dtype=F64, device="cuda")
+    h[:, :F] = x * torch.sigmoid(x) * u
+    _, s = quantized(h, 1)
+    check(scales, s, s * 2.0 ** -20, "scales")
+    # half a step of e4m3 (2^-4 of the value, 2^-10 of the scale below 2^-6), and the activation's float32 error
+    sc = s.repeat_interleave(128, 1)
+    check(values(codes, scales, 1), h, h.abs() * (2.0 ** -4 + 2.0 ** -18) + sc * (2.0 ** -10 + 2.0 ** -18), "h")
+    assert not bool(codes[:, F:].float().any())
+    n = R // 2
+    c2, s2 = torch.full_like(codes.float(), 3.0).to(F8), torch.full_like(scales, 3.0)
+    bm.fp8_rows(a, c2, s2, act="silu_mul", bounds=torch.tensor([0, n // 3, n], dtype=torch.int32, device="cuda"))
+    assert torch.equal(c2[:n].float(), codes[:n].float()) and torch.equal(s2[:n], scales[:n])
+    assert bool((c2[n:].float() == 3.0).all()) and bool((s2[n:] == 3.0).all())
+
+
+# --------------------------------------------------------------- weights
+
+@pytest.mark.parametrize("E, N, K", [(1, 1, 1), (1, 128, 128), (3, 129, 127), (2, 48, 300), (5, 768, 256), (1, 1000, 1000), (2, 33, 2048), (4, 300, 40)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_weights(bm, E, N, K, dtype):
+    _say("fp8 weights", E, N, K, dtype)
+    g = rng(N + K)
+    w = normal(g, E, N, K, scale=0.05)
+    w[:, : N // 2, : K // 3] *= 100.0
+    w[0, 0, 0] = 0.0
+    if N > 200:
+        w[0, :128, :128] = 0.0
+    w = w.to(dtype)
+    c0, s0 = bm.fp8_weights(w)
+    codes, scales, ct, st = bm.fp8_weights(w, transposed=True)
+    assert torch.equal(c0.float(), codes.float()) and torch.equal(s0, scales)
+    for e in range(E):
+        q, s = quantized(w[e].double(), 128)
+        same(codes[e], q, "codes")
+        same(scales[e], s, "scales")
+        want = torch.zeros(K, up(N), dtype=F64, device="cuda")
+        want[:, :N] = q[:, :K].t()
+        same(ct[e], want, "transposed codes")
+        same(st[e], s.t(), "transposed scales")
+
+
+def test_weights_of_infinities_and_nan(bm):
+    w = normal(rng(8), 2, 200, 260)
+    w[0, 3, 5], w[0, 150, 200], w[1, 199, 259] = INF, NAN, -INF
+    w[1, :128, :128] = NAN
+    codes, scales, ct, st = bm.fp8_weights(w, transposed=True)
+    for e in range(2):
+        q, s = quantized(w[e].double(), 128)
+        same(codes[e], q)
+        same(scales[e], s)
+        same(ct[e][:, :200], q[:, :260].t())
+    assert bool(scales.isfinite().all())
+
+
+# -------------------------------------------------------------- products
+
+def ragged(counts, tail=3):
+    n = sum(counts)
+    b = [0]
+    for c in counts:
+        b.append(b[-1] + c)
+    return torch.tensor(b, dtype=torch.int32, device="cuda"), n + tail
+
+
+def reference(xv, wv, bounds, R, act):
+    """(product in 64 bits, its sums of magnitudes) of value rows and E x n x K' values."""
+    E, n2 = wv.shape[:2]
+    N = n2 // 2 if act else n2
+    y, size = torch.zeros(R, N, dtype=F64, device="cuda"), torch.zeros(R, N, dtype=F64, device="cuda")
+    b = bounds.tolist()
+    for e in range(E):
+        a = xv[b[e]:b[e + 1]]
+        v, m = torch.mm(a, wv[e].t()), torch.mm(a.abs(), wv[e].abs().t())
+        if act:
+            g, u = v[:, :N], v[:, N:]
+            sg = torch.sigmoid(g)
+            y[b[e]:b[e + 1]] = g * sg * u
+            # |d silu(g) u| <= 1.1 |u| dg + |silu(g)| du
+            size[b[e]:b[e + 1]] = 1.1 * u.abs() * m[:, :N] + (g * sg).abs() * m[:, N:]
+        else:
+            y[b[e]:b[e + 1]], size[b[e]:b[e + 1]] = v, m
+    return y, size
+
+
+def weight_values(codes, scales, parts):
+    E, n2, kp = codes.shape
+    c, s = codes.reshape(E * parts, n2 // parts, kp), scales.reshape(E * parts, -1, kp // 128)
+    return torch.stack([values(c[i], s[i], 128) for i in range(E * parts)]).reshape(E, n2, kp)
+
+
+def make_weights(bm, g, E, N, K, parts=1, transposed=False):
+    w = normal(g, E * parts, N, K, scale=K ** -0.5, dtype=BF16)
+    q = bm.fp8_weights(w, transposed=transposed)
+    nb = up(N) // 128
+    return (q[0].reshape(E, parts * N, -1), q[1].reshape(E, parts * nb, -1)) + tuple(q[2:])
+
+
+SHAPES = [
+    (1, [1], 32, 128), (1, [5], 1, 1), (3, [2, 0, 7], 40, 136), (2, [17, 1], 129, 300), (8, [1, 0, 2, 0, 0, 3, 1, 1], 768, 2048),
+    (4, [16, 33, 0, 64], 100, 640), (2, [65, 130], 257, 257), (1, [300], 512, 1024), (3, [257, 1, 90], 96, 384), (64, [3] * 64, 48, 256),
+    (2, [500, 300], 300, 1000),
+]
+
+
+@pytest.mark.parametrize("E, counts, N, K", SHAPES)
+@pytest.mark.parametrize("x_type, out", [(F16, F16), (BF16, BF16), (BF16, F32), (F8, BF16), (F8, F16), (F8, F32)])
+@pytest.mark.parametrize("act", [None, "silu_mul"])
+def test_products(bm, E, counts, N, K, x_type, out, act):
+    _say("fp8 products", E, counts[:8], N, K, x_type, out, act)
+    g = rng(N * 3 + K)
+    bounds, R = ragged(counts)
+    n = R - 3
+    codes, scales = make_weights(bm, g, E, N, K, 2 if act else 1)
+    x = normal(g, R, K, dtype=F16 if x_type == F16 else BF16)
+    x[:, :: max(1, K // 5)] *= 9.0
+    q, s = bm.fp8_rows(x)
+    y = torch.full((R, N), 7.0, dtype=out, device="cuda")
+    if x_type == F8:
+        bm.fp8_matmul(q, codes, scales, y, x_scales=s, bounds=bounds, act=act)
+    else:
+        bm.fp8_matmul(x, codes, scales, y, bounds=bounds, act=act)
+    want, size = reference(values(q, s, 1), weight_values(codes, scales, 2 if act else 1), bounds, R, act)
+    tol = half_step(want, out) + size * ((K + 16) * STEP) + (want.abs() * 2.0 ** -20 if act else 0) + 1e-30
+    check(y[:n], want[:n], tol[:n], "y")
+    assert bool((y[n:] == 7.0).all())  # rows behind the last expert's
+    if x_type != F8:  # rows quantized on the way: the same bits
+        assert torch.equal(bm.fp8_matmul(q, codes, scales, torch.full_like(y, 7.0), x_scales=s, bounds=bounds, act=act), y)
+
+
+@pytest.mark.parametrize("E, counts, N, K", [(3, [2, 0, 7], 40, 136), (8, [40, 0, 2, 130, 0, 3, 1, 1], 768, 2048), (2, [500, 300], 300, 1000)])
+@pytest.mark.parametrize("given", [False, True])
+def test_gathered_strided_rows_and_bad_indexes(bm, E, counts, N, K, given):
+    _say("fp8 gathered", E, counts, N, K, given)
+    g = rng(K)
+    bounds, R = ragged(counts, tail=2)
+    n, div, X = R - 2, 3, 50
+    codes, scales = make_weights(bm, g, E, N, K)
+    wide = normal(g, X, K + 5, dtype=BF16)
+    x = wide[:, 3:3 + K]
+    rows = torch.randint(0, X * div, (R,), generator=g, device="cuda", dtype=torch.int32)
+    rows[n - 1], rows[n // 2], rows[n:] = X * div, -1, -1
+    q, s = bm.fp8_rows(x)
+    pick = rows.long().clamp(0, X * div - 1) // div
+    want, size = reference(values(q, s, 1)[pick], weight_values(codes, scales, 1), bounds, R, None)
+    out = torch.full((R, N + 5), 7.0, dtype=F32, device="cuda")
+    y = out[:, 1:1 + N]
+    if given:
+        big = torch.zeros(X, up(K) + 48, device="cuda").to(F8)
+        big[:, 16:16 + up(K)] = q
+        bs = torch.zeros(X, up(K) // 128 + 1, device="cuda")
+        bs[:, :-1] = s
+        bm.fp8_matmul(big[:, 16:16 + up(K)], codes, scales, y, x_scales=bs[:, :-1], bounds=bounds, rows=rows, div=div)
+    else:
+        bm.fp8_matmul(x, codes, scales, y, bounds=bounds, rows=rows, div=div)
+    bad = torch.zeros(R, dtype=torch.bool, device="cuda")
+    bad[n - 1] = bad[n // 2] = True
+    assert bool(y[bad].isnan().all())
+    good = ~bad
+    good[n:] = False
+    check(y[good], want[good], (half_step(want, F32) + size * ((K + 16) * STEP) + 1e-30)[good], "y")
+    assert bool((out[n:] == 7.0).all()) and bool((out[:, 0] == 7.0).all()) and bool((out[:, 1 + N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("R, N, K", [(1, 4096, 2048), (1, 33, 100), (7, 512, 512), (70, 300, 384), (600, 520, 700)])
+@pytest.mark.parametrize("given", [False, True])
+def test_one_dense_projection(bm, R, N, K, given):
+    _say("fp8 dense", R, N, K, given)
+    g = rng(N)
+    codes, scales = make_weights(bm, g, 1, N, K)
+    x = normal(g, R, K, dtype=F16)
+    q, s = bm.fp8_rows(x)
+    b = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    want, size = reference(values(q, s, 1), weight_values(codes, scales, 1), b, R, None)
+    if given:
+        y = bm.fp8_matmul(q, codes[0], scales[0], x_scales=s)
+        assert y.dtype == BF16
+    else:
+        y = bm.fp8_matmul(x, codes[0], scales[0])
+        assert y.dtype == F16
+    check(y, want, half_step(want, y.dtype) + size * ((K + 16) * STEP), "y")
+
+
+@pytest.mark.parametrize("E, counts, N, K", [(3, [2, 0, 7], 40, 136), (2, [17, 1], 129, 300), (4, [16, 33, 0, 64], 100, 640), (2, [500, 300], 300, 1000),
+                                             (2, [260, 700], 768, 512)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradient_of_the_rows(bm, E, counts, N, K, dtype):
+    """dx = W^T dy with the transposed weights, dy quantized on the way: against
+    the formula, and, for dy that e4m3 holds, against differences of the
+    product itself, which is linear in its rows."""
+    _say("fp8 dx", E, counts, N, K, dtype)
+    g = rng(N + 7 * K)
+    bounds, R = ragged(counts)
+    n = R - 3
+    codes, scales, ct, st = make_weights(bm, g, E, N, K, transposed=True)
+    dy = normal(g, R, N, dtype=dtype)
+    dx = torch.full((R, K), 7.0, dtype=F32, device="cuda")
+    bm.fp8_matmul(dy, ct, st, dx, bounds=bounds)
+    q, s = bm.fp8_rows(dy)
+    wv = weight_values(codes, scales, 1)[:, :, :K]
+    want, size = reference(values(q, s, 1)[:, :N], wv.transpose(1, 2).contiguous(), bounds, R, None)
+    check(dx[:n], want[:n], (half_step(want, F32) + size * ((N + 16) * STEP) + 1e-30)[:n], "dx")
+    assert bool((dx[n:] == 7.0).all())
+    # differences: x and x + d e_c, both held exactly by e4m3 with a scale of 1 (448 in every group)
+    x = torch.randint(-8, 9, (R, up(K)), generator=g, device="cuda").float()
+    x[:, 127::128] = 448.0
+    xs = torch.ones(R, up(K) // 128, device="cuda")
+    dy8 = torch.randint(-8, 9, (R, N), generator=g, device="cuda").to(dtype)
+    dy8[:, ::128] = 448.0
+    base = bm.fp8_matmul(x.to(F8), codes, scales, torch.zeros(R, N, device="cuda"), x_scales=xs, bounds=bounds)
+    dx = bm.fp8_matmul(dy8, ct, st, torch.zeros(R, K, device="cuda"), bounds=bounds)
+    for c in (0, K // 2, K - 1 if (K - 1) % 128 != 127 else K - 2):
+        moved = x.clone()
+        moved[:, c] += 1.0
+        y = bm.fp8_matmul(moved.to(F8), codes, scales, torch.zeros(R, N, device="cuda"), x_scales=xs, bounds=bounds)
+        diff = ((y - base).double() * dy8.double())[:n]
+        # both products' errors, weighed by dy, and dx's own
+        mag = reference(x.double().abs() + 1, weight_values(codes, scales, 1).abs(), bounds, R, None)[1][:n]
+        tol = 2 * ((K + 17) * STEP) * (mag * dy8.double()[:n].abs()).sum(1) + (N + 17) * STEP * diff.abs().sum(1) + 1e-20
+        check(diff.sum(1), dx[:n, c].double(), tol, "differences")
+
+
+def test_products_of_nan_infinite_and_zero_rows_and_scales(bm):
+    """They reach the outputs that their rows and columns reach, and no others."""
+    g = rng(4)
+    E, counts, N, K = 2, [5, 40], 300, 260
+    bounds, R = ragged(counts, tail=1)
+    n = R - 1
+    codes, scales = make_weights(bm, g, E, N, K)
+    x = normal(g, R, K, dtype=BF16)
+    x[n:] = NAN
+    good = bm.fp8_matmul(x, codes, scales, bounds=bounds)
+    assert bool(good[:n].isfinite().all())
+    xb = x.clone()
+    xb[0, K - 1], xb[4, 0], xb[n - 1, 130] = INF, NAN, -INF
+    xb[20, :] = 0.0
+    y = bm.fp8_matmul(xb, codes, scales, bounds=bounds)
+    hit = torch.zeros(R, dtype=torch.bool, device="cuda")
+    hit[0] = hit[4] = hit[n - 1] = True
+    assert bool(y[hit].isnan().all())
+    assert not bool(y[20].any())
+    hit[20] = True
+    hit[n:] = True
+    assert torch.equal(y[~hit], good[~hit])
+    # a NaN scale of a block of weights: its 128 outputs of its expert's rows
+    sb = scales.clone()
+    sb[1, 1, 2] = NAN
+    y = bm.fp8_matmul(x, codes, sb, bounds=bounds)
+    assert bool(y[5:n, 128:256].isnan().all())
+    assert torch.equal(y[:5], good[:5]) and torch.equal(y[5:n, :128], good[5:n, :128]) and torch.equal(y[5:n, 256:], good[5:n, 256:])
+
+
+@pytest.mark.parametrize("N, K", [(300, 260), (256, 512)])
+def test_wrong_bounds_stay_inside(bm, N, K):
+    g = rng(6)
+    codes, scales = make_weights(bm, g, 4, N, K)
+    x = normal(g, 100, K, dtype=BF16)
+    for b in ([0, 50, 20, 1000, 90], [-5, -1, 300, 300, 7], [2 ** 31 - 1] * 5, [100, 0, 100, 0, 100]):
+        y = torch.full((102, N), 7.0, dtype=BF16, device="cuda")
+        bm.fp8_matmul(x, codes, scales, y[1:101], bounds=torch.tensor(b, dtype=torch.int32, device="cuda"))
+        assert bool((y[0] == 7.0).all()) and bool((y[101] == 7.0).all())
+
+
+def test_no_rows(bm):
+    codes, scales = make_weights(bm, rng(1), 2, 64, 128)
+    b = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert bm.fp8_matmul(torch.empty(0, 128, dtype=BF16, device="cuda"), codes, scales, bounds=b).shape == (0, 64)
+    c, s = bm.fp8_rows(torch.empty(0, 130, device="cuda"))
+    assert c.shape == (0, 256) and s.shape == (0, 2)
+    y = torch.full((9, 64), 7.0, dtype=BF16, device="cuda")
+    bm.fp8_matmul(torch.ones(9, 128, dtype=BF16, device="cuda"), codes, scales, y, bounds=b)
+    assert bool((y == 7.0).all())
+    assert bm.fp8_weights(torch.empty(0, 5, 7, device="cuda"))[0].shape == (0, 5, 128)
