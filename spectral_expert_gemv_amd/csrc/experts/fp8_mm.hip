@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "fp8.h"
+#include "tiles.h"
 
 namespace bitsmoe {
 namespace experts {
@@ -43,6 +44,12 @@ __device__ __forceinline__ f32x4 group_sums(const Halves& a, const Halves& b) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) p = mfma16(a.v[j], b.v[j], p);
   return p;
+}
+
+// the same by the 8-bit instruction (scale operands of 0: none of its own)
+__device__ __forceinline__ f32x4 group_sums(const i32x8& a, const i32x8& b) {
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
 struct E4M3 {};  // rows that are codes already
@@ -277,6 +284,324 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mm8_few(Mm8Args s) {
     few8_rows<X, O, ACT, 4>(s, t, lds);
 }
 
+// --------------------------------------------------------------- tiled
+// Work-group tile of TM sorted rows x TN weight rows, WM x WN waves, the
+// contraction a group of 128 at a time: both operands' tiles are rows of 128
+// bytes, copied straight into LDS into one of kBufs buffers, kBufs - 1 groups
+// ahead of the products, with the rows' scales and the tile's (at most two)
+// weight scales behind them.  16-byte piece p of row r lies at place
+// p ^ (r / 2 % 8), so that the 16 rows a matrix-core operand touches spread
+// over all 64 banks.
+//
+// A group's 16 x 16 sums leave the matrix cores unscaled and are added to the
+// accumulators times the product of the two scales, 16 rows later in the
+// wave's order, while the matrix cores work on: four multiply-adds a lane
+// against 32 cycles of the matrix cores.
+//
+// 16-bit outputs come from the 8-bit instruction, whose sums of eight products
+// keep 14 bits of the largest (an error of 1.4e-5 to 5e-5 of a result, where
+// rounding it to fp16 adds up to 4.9e-4, to bf16 3.9e-3); float32 outputs from
+// codes turned to fp16 (EXACT), at under half the rate.
+constexpr int kTile = 256;  // rows and weight rows of a whole tile
+constexpr uint32_t kScaleLds = 2048;                              // of one buffer
+constexpr uint32_t kLds8 = 3 * ((kTile + kTile / 2) * kGroup + kScaleLds);  // three buffers of a 256 x 128 tile
+constexpr uint32_t kOutLds8 = 2 * 2 * kTile * kGroup;             // of the output on its way
+
+__device__ const float g_nan = __builtin_nanf("");
+
+// As copy16, 4 bytes per lane.
+__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(src), "{m0}"(lds) : "memory");
+}
+
+template <class V>
+__device__ __forceinline__ V lds_read(uint32_t at) {
+  typedef __attribute__((address_space(3))) const V lds_v;
+  return *(lds_v*)(uintptr_t)at;
+}
+
+// Sorted rows m0 .. m0 + mn, weight rows (of each half) n0 .. n0 + nn of expert e.
+template <class O, int TM, int TN, int WM, int WN, int kBufs, bool ACT, bool EXACT>
+__device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e, int m0, int mn,
+                                         int n0, int nn) {
+  constexpr int NT = 64 * WM * WN;
+  constexpr int MI = TM / WM / 16, NI = TN / WN / 16;  // 16 x 16 tiles of a wave
+  constexpr int kCa = TM * 8 / NT, kCb = TN * 8 / NT;  // copies of a lane
+  constexpr int kPieces = kCa + kCb + 1;
+  constexpr uint32_t kBytesA = TM * kGroup, kScales = (TM + TN) * kGroup;
+  constexpr uint32_t kBuf = kScales + kScaleLds;
+  static_assert(kBufs * kBuf <= kLds8 && kCa * NT == TM * 8 && kCb * NT == TN * 8, "buffers");
+  static_assert(NT * 4 <= (int)kScaleLds && TM <= NT - 64, "a wave for the weights' scales");
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = s.kg;
+
+  // addresses of the pieces of group 0
+  const uint8_t* pa[kCa];
+  const uint8_t* pb[kCb];
+  const int64_t kp = (int64_t)kg * kGroup;
+#pragma unroll
+  for (int i = 0; i < kCa; ++i) {
+    const int l = (i * NT + (int)threadIdx.x) >> 3, p = (threadIdx.x & 7) ^ ((l >> 1) & 7);
+    const int xr = x_row8(s, m0 + min(l, mn - 1));
+    pa[i] = (const uint8_t*)s.x + (int64_t)max(xr, 0) * s.ldx + p * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < kCb; ++i) {
+    const int l = (i * NT + (int)threadIdx.x) >> 3, p = (threadIdx.x & 7) ^ ((l >> 1) & 7);
+    // with the activation, blocks of 16 tile rows alternate gate and up
+    const int col = ACT ? (l >> 5) * 16 + (l & 15) : l;
+    const int64_t row = (int64_t)e * (ACT ? 2 : 1) * s.N + n0 + min(col, nn - 1) + (ACT && (l & 16) ? s.N : 0);
+    pb[i] = s.w + row * kp + p * 16;
+  }
+  // scales: TM / 64 waves copy the rows' (NaN for a row outside x), the others
+  // the weights', blocks 0 and 1 in turn
+  const float* ps;
+  int step_s = 1;
+  if (wv * 64 < TM) {
+    const int xr = x_row8(s, m0 + min(wv * 64 + lane, mn - 1));
+    ps = xr < 0 ? &g_nan : s.xs + (int64_t)xr * s.ldxs;
+    step_s = xr < 0 ? 0 : 1;
+  } else {
+    const int which = lane & 1, nb0 = n0 / kGroup;
+    const int64_t block = (int64_t)e * (ACT ? 2 : 1) * s.nb + (ACT ? nb0 + which * s.nb : min(nb0 + which, s.nb - 1));
+    ps = s.ws + block * kg;
+  }
+  // (copies past the last group repeat it: nobody reads them)
+  int next = 0;  // the group that the pointers stand at
+  auto stage_piece = [&](int i, uint32_t buf) {
+    if (i < kCa) {
+      copy16(pa[i], buf + (uint32_t)(i * NT + wv * 64) * 16);
+      pa[i] += next + 1 < kg ? kGroup : 0;
+    } else if (i < kCa + kCb) {
+      copy16(pb[i - kCa], buf + kBytesA + (uint32_t)((i - kCa) * NT + wv * 64) * 16);
+      pb[i - kCa] += next + 1 < kg ? kGroup : 0;
+    } else {
+      copy4(ps, buf + kScales + (uint32_t)wv * 256);
+      ps += next + 1 < kg ? step_s : 0;
+      ++next;
+    }
+  };
+
+  static_assert(MI % 2 == 0, "turns of the registers");
+  typedef typename std::conditional<EXACT, Halves, i32x8>::type Frag;
+  const int wm = (wv / WN) * (TM / WM), wn = (wv % WN) * (TN / WN);
+  const int l16 = lane & 15;
+  const uint32_t piece = ((lane >> 4) ^ ((l16 >> 1) & 7)) << 4;
+  // (buffers start at multiples of 1024 bytes, so adding one keeps the xor)
+  const uint32_t off_a = (wm + l16) * kGroup + piece, off_b = kBytesA + (wn + l16) * kGroup + piece;
+  const uint32_t off_s = kScales + (wm + l16) * 4, off_w = kScales + TM * 4 + (ACT ? 0 : wn / kGroup * 4);
+  auto raw = [&](uint32_t at, int g) {
+    const i32x4 a = lds_read<i32x4>(at + g * 16 * kGroup), b = lds_read<i32x4>((at ^ 64) + g * 16 * kGroup);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto operand = [&](const i32x8& q) -> Frag {
+    if constexpr (EXACT)
+      return halves(q);
+    else
+      return q;
+  };
+  f32x4 acc[MI][NI] = {}, part[NI] = {};
+  i32x8 fa[2], fb[NI];
+  float sa[2], sw[2], f[2] = {0.f, 0.f};
+  auto read_a = [&](int g, uint32_t buf) {
+    fa[g & 1] = raw(buf + off_a, g);
+    sa[g & 1] = lds_read<float>(buf + off_s + g * 64);
+  };
+  auto read_w = [&](uint32_t buf) {
+    sw[0] = lds_read<float>(buf + off_w);
+    if (ACT) sw[1] = lds_read<float>(buf + off_w + 4);
+  };
+  auto add = [&](int g, int j) {  // the sums of the 16 rows before, scaled
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[g][j][q] = fmaf(part[j][q], f[ACT ? j & 1 : 0], acc[g][j][q]);
+  };
+  uint32_t cur = base;
+  auto after = [&](uint32_t b) { return b == base + (kBufs - 1) * kBuf ? base : b + kBuf; };
+  // MI turns of 16 rows; the reads of a turn's rows are issued a turn ahead,
+  // the weights' of the next group as soon as the last products have theirs.
+  // Before the last turn the wave waits for its copies of the next group, meets
+  // the others, and starts to copy a later group into the buffer that nobody
+  // reads any more.
+  auto step = [&](auto last_) {
+    constexpr bool kLast = decltype(last_)::value;
+    const uint32_t nxt = after(cur);
+    Frag b[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) b[j] = operand(fb[j]);
+#pragma unroll
+    for (int g = 0; g < MI; ++g) {
+      const bool border = g == MI - 1;
+      if (!kLast && border) {
+        wait_copies<(kBufs - 2) * kPieces>();
+        lds_barrier();
+      }
+      const Frag a = operand(fa[g & 1]);
+      const float f0 = sa[g & 1] * sw[0], f1 = ACT ? sa[g & 1] * sw[1] : 0.f;
+      if (!border) read_a(g + 1, cur);
+      if (!kLast && border) {
+        read_a(0, nxt);
+        read_w(nxt);
+      }
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        add(g == 0 ? MI - 1 : g - 1, j);
+        part[j] = group_sums(b[j], a);
+        if (!kLast && border) {
+          fb[j] = raw(nxt + off_b, j);
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+            if (i * NI / kPieces == j) stage_piece(i, cur);
+        }
+      }
+      f[0] = f0, f[1] = f1;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    cur = nxt;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kBufs; ++i)
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) stage_piece(j, base + i * kBuf);
+  wait_copies<(kBufs - 1) * kPieces>();  // the first group's
+  lds_barrier();
+  if (wm < mn) {
+    read_w(cur);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[j] = raw(cur + off_b, j);
+    read_a(0, cur);
+#pragma unroll 1
+    for (int c = 1; c < kg; ++c) step(std::false_type{});
+    step(std::true_type{});
+#pragma unroll
+    for (int j = 0; j < NI; ++j) add(MI - 1, j);
+  } else {  // a wave past the tile's rows only copies
+#pragma unroll 1
+    for (int c = 1; c < kg; ++c) {
+      wait_copies<(kBufs - 2) * kPieces>();
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) stage_piece(i, cur);
+      cur = after(cur);
+    }
+  }
+  wait_copies<0>();  // nothing is written into this work-group's LDS after its end
+
+  // The products were formed transposed: lane % 16 is the output row, and a
+  // lane holds 4 consecutive columns 4 (lane / 16) .. of each 16 x 16 tile.
+  // The tile goes through LDS, as far as it fits at a time, and leaves as
+  // whole rows, 16 bytes a lane.  16-byte piece p of LDS row r lies at
+  // p ^ (r % 16), which spreads 16 rows' writes over the banks.
+  constexpr int kOut = ACT ? TN / 2 : TN;  // columns
+  constexpr int kFit = kOutLds8 / (kOut * (int)sizeof(O));
+  constexpr int kPassRows = kFit < TM ? kFit : TM;
+  constexpr int kPasses = TM / kPassRows, kI = MI / kPasses;  // 16-row blocks of a wave per pass
+  constexpr int kRowPieces = kOut * (int)sizeof(O) / 16;
+  constexpr int kKey = kRowPieces < 16 ? kRowPieces - 1 : 15;
+  static_assert(kPassRows * kPasses == TM && kI * kPasses == MI, "whole passes");
+  O* Y = (O*)s.y;
+  const int64_t ldy = s.ldy;
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    // (nobody reads the operands, or the pass before, any more)
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int row = (wv / WN) * (kPassRows / WM) + 16 * i + l16;
+#pragma unroll
+      for (int j = 0; j < NI; j += ACT ? 2 : 1) {
+        f32x4 v = acc[pass * kI + i][j];
+        if constexpr (ACT) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = gated(v[q], acc[pass * kI + i][j + 1][q]);
+        }
+        typedef __attribute__((ext_vector_type(4))) O O4;
+        O4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = (O)v[q];
+        const int at = ((ACT ? (wn + 16 * j) / 2 : wn + 16 * j) + 4 * (lane >> 4)) * (int)sizeof(O);
+        typedef __attribute__((address_space(3))) O4 lds_o4;
+        *(lds_o4*)(uintptr_t)(base + row * (kOut * (int)sizeof(O)) +
+                              ((((at >> 4) ^ (row & kKey)) << 4) | (at & 15))) = o;
+      }
+    }
+    lds_barrier();
+#pragma unroll 4
+    for (int at = threadIdx.x; at < kPassRows * kRowPieces; at += NT) {
+      const int row = at / kRowPieces, p = at % kRowPieces;
+      // the output row behind LDS row `row` of this pass
+      const int m = row / (kPassRows / WM) * (TM / WM) + pass * (kPassRows / WM) + row % (kPassRows / WM);
+      const i32x4 v = lds_read<i32x4>(base + row * (kOut * (int)sizeof(O)) + ((p ^ (row & kKey)) << 4));
+      constexpr int kPer = 16 / (int)sizeof(O);
+      const int n = p * kPer;
+      O* y = Y + (int64_t)(m0 + m) * ldy + n0 + n;
+      if (m < mn && s.y16 && n + kPer <= nn) {
+        *reinterpret_cast<i32x4*>(y) = v;
+      } else if (m < mn) {
+        typedef __attribute__((ext_vector_type(kPer))) O On;
+        const On o = __builtin_bit_cast(On, v);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (n + j < nn) y[j] = o[j];
+      }
+    }
+  }
+}
+
+// One work-group per tile: first the whole rounds of the chip's compute units
+// with 256 x 256 tiles, then what is left, cut in four 128 x 128 tiles where
+// those make one round at most, in two of 256 x 128 where those do, else as it
+// is.  float32 outputs: 256 x 128 tiles alone (fp16 operands take twice the
+// registers).
+template <class O, bool ACT>
+__global__ __launch_bounds__(512, 2) void k_mm8_tile(Mm8Args s) {
+  __shared__ __align__(1024) uint8_t lds[kLds8];
+  constexpr bool kExact = sizeof(O) == 4;
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  constexpr int kCols = (kExact ? kTile / 2 : kTile) / (ACT ? 2 : 1);  // output columns per tile
+  const int ntn = (s.N + kCols - 1) / kCols;
+  const int mt = s.bounds ? count_tiles(s.bounds, s.E, s.R, kTile) : (s.R + kTile - 1) / kTile;
+  const uint32_t total = (uint32_t)mt * ntn, left = total % kUnits;
+  const uint32_t parts = kExact ? 1 : left <= kUnits / 4 ? 4 : left <= kUnits / 2 ? 2 : 1;
+  const uint32_t whole = parts > 1 ? total - left : total;
+  // Work-group b runs on XCD b % 8, and every XCD takes 32 consecutive tiles of
+  // a round, which share operand rows in its L2.
+  uint32_t b = blockIdx.x, id;
+  int part = -1;
+  const uint32_t rounds = (whole + kUnits - 1) / kUnits;
+  if (b < rounds * kUnits) {
+    id = b / kUnits * kUnits + (b & 7) * (kUnits / 8) + b % kUnits / 8;
+    if (id >= whole) return;
+  } else {
+    b -= rounds * kUnits;
+    const uint32_t cut = (total - whole) * parts, run = (cut + 7) / 8;
+    const uint32_t at = (b & 7) * run + (b >> 3);
+    if ((b >> 3) >= run || at >= cut) return;
+    id = whole + at / parts;
+    part = at % parts;
+  }
+  int mi, ni;
+  tile_place(id, mt, ntn, mi, ni);
+  Tile t{0, mi * kTile, min(kTile, s.R - mi * kTile)};
+  if (s.bounds) t = find_tile(s.bounds, s.E, s.R, mi, kTile);
+  if (t.n <= 0) return;
+  int n0 = ni * kCols, nn = min(kCols, s.N - n0);
+  if constexpr (kExact) {
+    mm8_tile<O, kTile, kTile / 2, 2, 4, 3, ACT, true>(s, base, t.e, t.row0, t.n, n0, nn);
+  } else if (part < 0) {
+    mm8_tile<O, kTile, kTile, 2, 4, 2, ACT, false>(s, base, t.e, t.row0, t.n, n0, nn);
+  } else if (parts == 4) {
+    const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
+    t.n = min(kTile / 2, t.n - pm), nn = min(kCols / 2, nn - pn);
+    if (t.n <= 0 || nn <= 0) return;
+    mm8_tile<O, kTile / 2, kTile / 2, 2, 4, 4, ACT, false>(s, base, t.e, t.row0 + pm, t.n, n0 + pn, nn);
+  } else {
+    const int pn = part * (kCols / 2);
+    nn = min(kCols / 2, nn - pn);
+    if (nn <= 0) return;
+    mm8_tile<O, kTile, kTile / 2, 2, 4, 3, ACT, false>(s, base, t.e, t.row0, t.n, n0 + pn, nn);
+  }
+}
+
 template <class F>
 void with_out(int o_dtype, F f) {
   if (o_dtype == BITSMOE_F32)
@@ -287,9 +612,26 @@ void with_out(int o_dtype, F f) {
     f(bf16{});
 }
 
-size_t rows_ws(int x_dtype, int64_t x_rows, int K) {
-  (void)x_dtype, (void)x_rows, (void)K;
-  return 0;
+// Up to kFewMean rows per expert on average the few-rows kernel is the faster
+// one, up to kFewMeanSmall while there are few 256 x 256 tiles to spread over
+// the chip.
+constexpr int kFewMean = 12, kFewMeanSmall = 32, kFewTiles = 32;
+
+bool few8(int R, int E, int N) {
+  const long long tiles = (long long)((N + kTile - 1) / kTile) * E * ((R / E + kTile - 1) / kTile);
+  return R <= (long long)(tiles <= kFewTiles ? kFewMeanSmall : kFewMean) * E &&
+         max_tiles(R, E, kFewRows) <= 65535;
+}
+
+// The workspace of rows that are quantized before the tiled products: codes,
+// then scales.
+struct RowsWs {
+  size_t codes, scales;
+};
+RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K) {
+  if (x_dtype == kE4M3 || few8(R, E, N)) return RowsWs{0, 0};
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  return RowsWs{al((size_t)rows * groups_of(K) * kGroup), al((size_t)rows * groups_of(K) * 4)};
 }
 
 bool rows16(const void* p, int64_t ld, int size) {
@@ -322,7 +664,8 @@ int bitsmoe_fp8_matmul_workspace_size(int x_dtype, int x_rows, int R, int E, int
   if (!bytes) return fail(BITSMOE_EINVAL, "bytes is null");
   const int st = sizes8(x_dtype, x_rows, R, E, N, K, act);
   if (st) return st;
-  *bytes = rows_ws(x_dtype, x_rows, K);
+  const RowsWs w = rows_ws(x_dtype, x_rows, R, E, N, K);
+  *bytes = w.codes + w.scales;
   return BITSMOE_OK;
 }
 
@@ -348,7 +691,10 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
     return fail(BITSMOE_EINVAL, "null pointer argument");
   if (((uintptr_t)codes & 15u) || (given && !rows16(x, ldx, 1)))
     return fail(BITSMOE_EINVAL, "codes must be 16-byte aligned");
-  const size_t need = rows_ws(x_dtype, x_rows, K);
+  // (without indexes only the first R rows of x are read)
+  const int live = rows ? x_rows : R;
+  const RowsWs w = rows_ws(x_dtype, live, R, E, N, K);
+  const size_t need = w.codes + w.scales;
   if (need > ws_bytes || (need && !ws))
     return fail(BITSMOE_ENOSPC, "ws_bytes=%zu < %zu", ws_bytes, need);
   if (need && ((uintptr_t)ws & 255u))
@@ -356,12 +702,35 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
   Mm8Args s{x, ldx, x_scales, ldxs, rows, div, x_rows, (const uint8_t*)codes, scales, bounds, R, E,
             N, K, (int)kg, (int)nb, y, ldy, 0};
   s.y16 = rows16(y, ldy, y_dtype == BITSMOE_F32 ? 4 : 2);
+  const bool few = few8(R, E, N);
   const int fp = act ? kFewCols / 2 : kFewCols;
   const dim3 grid((unsigned)((N + fp - 1) / fp),
                   (unsigned)(bounds ? max_tiles(R, E, kFewRows) : (R + kFewRows - 1) / kFewRows));
-  if (grid.y > 65535) return fail(BITSMOE_ESHAPE, "R=%d with E=%d: too many row tiles", R, E);
+  const int per = (y_dtype == BITSMOE_F32 ? kTile / 2 : kTile) / (act ? 2 : 1);
+  const long long ntn = (N + per - 1) / per;
+  const long long mt = bounds ? max_tiles(R, E, kTile) : (R + kTile - 1) / kTile;
+  // enough for any split of at most mt * ntn tiles into whole rounds and cut tiles
+  const long long groups = (mt * ntn + kUnits - 1) / kUnits * kUnits + kUnits + 8;
+  if (!few && groups * 512 > 0xFFFFFFFFll)  // (a grid's work-items)
+    return fail(BITSMOE_ESHAPE, "R=%d E=%d N=%d K=%d make too many tiles", R, E, N, K);
+  if (need) {
+    s.x = ws, s.ldx = kg * kGroup;
+    s.xs = (const float*)((uint8_t*)ws + w.codes), s.ldxs = kg;
+    const int rc = run_fp8_rows(x_dtype, x, ldx, BITSMOE_ACT_NONE, rows ? nullptr : bounds, live, E, K,
+                                ws, s.ldx, (float*)s.xs, kg, (hipStream_t)stream);
+    if (rc) return rc;
+  }
   with_out(y_dtype, [&](auto o) {
     using O = decltype(o);
+    if (!few) {
+      if (act)
+        hipLaunchKernelGGL((k_mm8_tile<O, true>), dim3((unsigned)groups), dim3(512), 0,
+                           (hipStream_t)stream, s);
+      else
+        hipLaunchKernelGGL((k_mm8_tile<O, false>), dim3((unsigned)groups), dim3(512), 0,
+                           (hipStream_t)stream, s);
+      return;
+    }
     auto go = [&](auto tag) {
       using X = decltype(tag);
       if (act)

@@ -6,7 +6,7 @@
 // fp16 or bf16 operands, float32 accumulators, one rounding at the end.
 #include <type_traits>
 
-#include "experts.h"
+#include "tiles.h"
 
 namespace bitsmoe {
 namespace experts {
@@ -85,26 +85,6 @@ __global__ __launch_bounds__(256) void k_mm_pad(const uint16_t* __restrict__ src
 __device__ __align__(16) const uint32_t g_pad[8] = {0,           0,           0,           0,
                                                     0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
 
-// Copies 16 bytes per lane from `src` to LDS at lds + 16 lane.  (The
-// compiler would wait for all such copies before any LDS read, so the copy is
-// an opaque statement without register outputs; the loop below waits for its
-// copies by count.  The LDS address is an operand in m0, so the compiler knows
-// what it holds; the copy may not be the instruction after the one that sets it.)
-__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(lds) : "memory");
-}
-// all but the last kLeft copies of the wave have landed
-template <int kLeft>
-__device__ __forceinline__ void wait_copies() {
-  static_assert(kLeft < 16, "vmcnt field");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | kLeft);
-}
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 constexpr int kStep = 64;  // contraction elements per step
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
@@ -176,16 +156,6 @@ struct Operand {
     }
   }
 };
-
-// Tile `id` of mt x nt in the order that keeps the 32 work-groups of an XCD on
-// shared operand rows (in its L2): 4 row tiles by 8 column tiles, then the
-// next columns.
-__device__ __forceinline__ void tile_place(uint32_t id, int mt, int nt, int& m, int& n) {
-  const uint32_t g = id / (4u * nt), r = id - g * (4u * nt);
-  const uint32_t gm = min(4, mt - (int)g * 4);
-  m = g * 4 + r % gm;
-  n = r / gm;
-}
 
 constexpr int kTile = 256;                          // rows and columns of a tile
 constexpr uint32_t kOutLds = 2 * 2 * kTile * kStep * 2;  // of the output on its way
@@ -458,8 +428,6 @@ __device__ __forceinline__ void mm_tile(const MmArgs& s, uint32_t base, int e, i
 // those make one round at most, in two of 256 x 128 where those do (a quarter
 // takes about 0.45 of a tile's time, a half 0.65: its copies, not its
 // products, take the time), else as it is.
-constexpr int kUnits = 256;       // compute units of an MI355X, one work-group each (its LDS)
-
 template <class T, class O, int MODE, bool ACT>
 __global__ __launch_bounds__(512, 2) void k_mm_tile(MmArgs s) {
   __shared__ __align__(1024) uint8_t lds[kLds];
