@@ -80,14 +80,17 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // ------------------------------------------------- few rows per expert
 // A work-group takes up to 64 sorted rows of one expert and 32 rows of its
 // weights (with the activation 16 of the gate and the same 16 of the up half);
-// its four waves split the inputs in turns of 128, one group and a whole line
-// of each weight row, and add up their sums through LDS.  Weights go straight
-// into registers, once; they are the products' first operand, so a lane holds 4
-// outputs of one row of x, whose scale it needs once.  Which of a group's 128
-// elements lie in which lane does not matter as long as both operands agree:
-// lane (r, q) holds bytes 16 q .. and 64 + 16 q .. of row r, so that a load
-// covers 64 bytes of 16 rows.
+// its four waves split the groups, a whole line of each weight row each, and
+// add up their sums through LDS.  Weights go straight into registers, once;
+// they are the products' first operand, so a lane holds 4 outputs of one row of
+// x, whose scale it needs once.  Which of a group's 128 elements lie in which
+// lane does not matter as long as both operands agree: lane (r, q) holds bytes
+// 16 q .. and 64 + 16 q .. of row r, so that a load covers 64 bytes of 16 rows.
+//
+// Rows that are not codes yet are quantized by the work-group, a turn's groups
+// at a time, into LDS, while its weights are on their way.
 constexpr int kFewRows = 64, kFewCols = 32, kFewWaves = 4;
+constexpr int kFewTurn = 16;  // groups of 16 rows (8 of 32, 4 of 64) in a turn
 
 // 16 + 16 bytes of a row of codes at group start p (+ 16 q)
 __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
@@ -95,59 +98,22 @@ __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// One row operand of a group: codes as they are, or 16 + 16 elements on their
-// way to codes.
-template <class X>
-struct RowPiece {
-  float v[4][8];
-  __device__ __forceinline__ void load(const X* p, int left) {  // left: elements of the row from p on
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int at = (h >> 1) * 64 + (h & 1) * 8;
-      load8_any(p + at, left - at, v[h]);
-    }
-  }
-  __device__ __forceinline__ i32x8 codes(float& s) const {
-    auto over_lanes = [](uint32_t m) {  // the four lanes of the row
-#pragma unroll
-      for (int d = 16; d < 64; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
-        m = m > o ? m : o;
-      }
-      return m;
-    };
-    uint32_t a = 0;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const uint32_t m = amax_bits<false>(v[h]);
-      a = a > m ? a : m;
-    }
-    a = over_lanes(a);
-    if (__any(a >= kInfBits)) {
-      a = 0;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint32_t m = amax_bits<true>(v[h]);
-        a = a > m ? a : m;
-      }
-      a = over_lanes(a);
-    }
-    const Factors f = factors8(a);
-    s = f.s;
-    i32x8 q;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      q[2 * h] = (int)codes4(v[h][0], v[h][1], v[h][2], v[h][3], f.r);
-      q[2 * h + 1] = (int)codes4(v[h][4], v[h][5], v[h][6], v[h][7], f.r);
-    }
-    return q;
-  }
+struct FewLds {
+  // rows of a turn's codes, 16 bytes apart from a multiple of 256 so that the
+  // reads of 16 rows spread over the banks; later the waves' sums
+  union {
+    uint8_t codes[16 * (kFewTurn * kGroup) + 64 * 16];
+    f32x4 part[kFewWaves * 8 * 64];
+  };
+  float scales[16 * kFewTurn];
 };
 
 template <class X, class O, bool ACT, int MB>
-__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, float* lds) {
+__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, FewLds& lds) {
   constexpr bool kCodes = std::is_same<X, E4M3>::value;
-  constexpr int U = MB == 1 ? 4 : MB == 2 ? 2 : 1;  // turns whose loads are in flight together
+  constexpr int kTurn = kFewTurn / MB;     // groups of a turn
+  constexpr int U = kTurn / kFewWaves;     // of a wave, whose loads are in flight together
+  constexpr int kRow = kTurn * kGroup + 16;  // bytes of an LDS row
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * (ACT ? kFewCols / 2 : kFewCols);
@@ -162,49 +128,70 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, float
     // (32 and 16 divide 128: a work-group's rows share a block)
     ws[b] = s.ws + ((int64_t)t.e * (ACT ? 2 : 1) * s.nb + (ACT ? b : 0) * s.nb + n0 / kGroup) * s.kg;
   }
-  int64_t x[MB];
-  bool bad[MB];
+  const uint8_t* x[MB];
+  const float* xs[MB];
+  if constexpr (kCodes) {
 #pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    const int xr = x_row8(s, t.row0 + min(16 * m + r, t.n - 1));
-    bad[m] = xr < 0;
-    x[m] = max(xr, 0);
+    for (int m = 0; m < MB; ++m) {
+      const int xr = x_row8(s, t.row0 + min(16 * m + r, t.n - 1));
+      x[m] = (const uint8_t*)s.x + (int64_t)max(xr, 0) * s.ldx + 16 * q;
+      xs[m] = xr < 0 ? nullptr : s.xs + (int64_t)xr * s.ldxs;
+    }
   }
   f32x4 acc[MB][2] = {};
-  auto turn = [&](int g0, auto whole_) {  // group g0 and every kFewWaves on, U times
-    constexpr bool whole = decltype(whole_)::value;
-    i32x8 vw[U][2];
-    float sw[U][2];
-    // (rows of two bytes an element stay as loaded until their turn)
-    typename std::conditional<kCodes, i32x8, RowPiece<typename std::conditional<kCodes, f16, X>::type>>::type vx[U][MB];
-    float sx[U][MB];
+#pragma unroll 1
+  for (int g0 = 0; g0 < s.kg; g0 += kTurn) {
+    // (groups past the last are loaded as it and not used)
+    i32x8 vw[U][2], vx[U][MB];
+    float sw[U][2], sx[U][MB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int g = whole ? g0 + u * kFewWaves : min(g0 + u * kFewWaves, s.kg - 1);
+      const int g = min(g0 + u * kFewWaves + wv, s.kg - 1);
 #pragma unroll
       for (int b = 0; b < 2; ++b) vw[u][b] = load_codes(w[b] + (int64_t)g * kGroup), sw[u][b] = ws[b][g];
+      if constexpr (kCodes) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        if constexpr (kCodes) {
-          vx[u][m] = load_codes((const uint8_t*)s.x + x[m] * s.ldx + 16 * q + g * kGroup);
-          sx[u][m] = s.xs[x[m] * s.ldxs + g];
-        } else {
-          vx[u][m].load((const X*)s.x + x[m] * s.ldx + 16 * q + g * kGroup,
-                        s.K - (16 * q + g * kGroup));
+        for (int m = 0; m < MB; ++m) {
+          vx[u][m] = load_codes(x[m] + (int64_t)g * kGroup);
+          sx[u][m] = xs[m] ? xs[m][g] : __builtin_nanf("");
         }
       }
     }
+    if constexpr (!kCodes) {
+      if (g0) __syncthreads();  // (the turn before is read)
+      // 16 lanes a group, as in k_fp8_rows
+      const int groups = t.n * kTurn, l = threadIdx.x & 15;
+      for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
+        const int row = i / kTurn, g = i % kTurn, c = (g0 + g) * kGroup + 8 * l;
+        const int xr = i < groups ? x_row8(s, t.row0 + row) : -1;
+        float v[8] = {};
+        if (xr >= 0) load8_any((const X*)s.x + (int64_t)xr * s.ldx + c, s.K - c, v);
+        uint32_t a = row_max(amax_bits<false>(v));
+        if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
+        const Factors f = factors8(a);
+        if (i < groups) {
+          uint2 o;
+          o.x = codes4(v[0], v[1], v[2], v[3], f.r);
+          o.y = codes4(v[4], v[5], v[6], v[7], f.r);
+          *reinterpret_cast<uint2*>(lds.codes + row * kRow + g * kGroup + 8 * l) = o;
+          if (l == 0) lds.scales[row * kTurn + g] = xr < 0 ? __builtin_nanf("") : f.s;
+        }
+      }
+      __syncthreads();
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (!whole && g0 + u * kFewWaves >= s.kg) break;
+      const int gl = u * kFewWaves + wv;
+      if (g0 + gl >= s.kg) break;
       const Halves hw[2] = {halves(vw[u][0]), halves(vw[u][1])};
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        Halves hx;
-        if constexpr (kCodes)
-          hx = halves(vx[u][m]);
-        else
-          hx = halves(vx[u][m].codes(sx[u][m]));
+        if constexpr (!kCodes) {
+          const int row = min(16 * m + r, t.n - 1);
+          vx[u][m] = load_codes(lds.codes + row * kRow + gl * kGroup + 16 * q);
+          sx[u][m] = lds.scales[row * kTurn + gl];
+        }
+        const Halves hx = halves(vx[u][m]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const f32x4 p = group_sums(hw[b], hx);
@@ -214,14 +201,11 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, float
         }
       }
     }
-  };
-  constexpr int kTurn = U * kFewWaves;
-  int g = wv;
-  for (; g + kTurn - kFewWaves < s.kg; g += kTurn) turn(g, std::true_type{});
-  if (g < s.kg) turn(g, std::false_type{});
+  }
 
   // sums of the four waves: [wave][tile of 16 x 16][lane]
-  f32x4* part = (f32x4*)lds;
+  if (!kCodes) __syncthreads();
+  f32x4* part = lds.part;
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -243,17 +227,11 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, float
       }
     }
     const int n = n0 + (ACT ? 0 : 16 * (i & 1)) + 4 * q;
-    bool nan = false;
-#pragma unroll
-    for (int u = 0; u < MB; ++u) nan = u == m ? bad[u] : nan;
     if (16 * m + r >= t.n) continue;
     typedef __attribute__((ext_vector_type(4))) O O4;
     O4 o;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float f = ACT ? gated(v[0][j], v[1][j]) : v[0][j];
-      o[j] = (O)(nan ? __builtin_nanf("") : f);
-    }
+    for (int j = 0; j < 4; ++j) o[j] = (O)(ACT ? gated(v[0][j], v[1][j]) : v[0][j]);
     O* y = Y + (int64_t)(t.row0 + 16 * m + r) * s.ldy + n;
     if (s.y16 && n + 4 <= s.N) {
       *reinterpret_cast<O4*>(y) = o;
@@ -266,8 +244,8 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, float
 }
 
 template <class X, class O, bool ACT>
-__global__ __launch_bounds__(64 * kFewWaves) void k_mm8_few(Mm8Args s) {
-  __shared__ float lds[kFewWaves * 8 * 64 * 4];
+__global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
+  __shared__ FewLds lds;
   Tile t{0, 0, 0};
   if (s.bounds) {
     t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kFewRows);
