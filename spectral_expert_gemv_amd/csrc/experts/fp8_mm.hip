@@ -344,20 +344,16 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
     const int64_t block = (int64_t)e * (ACT ? 2 : 1) * s.nb + (ACT ? nb0 + which * s.nb : min(nb0 + which, s.nb - 1));
     ps = s.ws + block * kg;
   }
-  // (copies past the last group repeat it: nobody reads them)
-  int next = 0;  // the group that the pointers stand at
-  auto stage_piece = [&](int i, uint32_t buf) {
-    if (i < kCa) {
-      copy16(pa[i], buf + (uint32_t)(i * NT + wv * 64) * 16);
-      pa[i] += next + 1 < kg ? kGroup : 0;
-    } else if (i < kCa + kCb) {
-      copy16(pb[i - kCa], buf + kBytesA + (uint32_t)((i - kCa) * NT + wv * 64) * 16);
-      pb[i - kCa] += next + 1 < kg ? kGroup : 0;
-    } else {
-      copy4(ps, buf + kScales + (uint32_t)wv * 256);
-      ps += next + 1 < kg ? step_s : 0;
-      ++next;
-    }
+  // Piece i of the copies of group g: rows first, then weights, then scales.
+  // (Groups past the last repeat it: nobody reads them.)
+  auto stage_piece = [&](int i, int g, uint32_t buf) {
+    const int at = min(g, kg - 1);
+    if (i < kCa)
+      copy16(pa[i] + (int64_t)at * kGroup, buf + (uint32_t)(i * NT + wv * 64) * 16);
+    else if (i < kCa + kCb)
+      copy16(pb[i - kCa] + (int64_t)at * kGroup, buf + kBytesA + (uint32_t)((i - kCa) * NT + wv * 64) * 16);
+    else
+      copy4(ps + at * step_s, buf + kScales + (uint32_t)wv * 256);
   };
 
   static_assert(MI % 2 == 0, "turns of the registers");
@@ -397,10 +393,39 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
   auto after = [&](uint32_t b) { return b == base + (kBufs - 1) * kBuf ? base : b + kBuf; };
   // MI turns of 16 rows; the reads of a turn's rows are issued a turn ahead,
   // the weights' of the next group as soon as the last products have theirs.
-  // Before the last turn the wave waits for its copies of the next group, meets
-  // the others, and starts to copy a later group into the buffer that nobody
-  // reads any more.
-  auto step = [&](auto last_) {
+  // Before the last turn (the border) the wave waits for its copies of the next
+  // group and meets the others; then nobody reads this group's buffer any more.
+  //
+  // With two buffers the copies of a later group would have one group's time,
+  // and come all at once: so the waves meet twice more, and what is read by
+  // then (the weights, which lie in registers; the first half of the rows) is
+  // copied over early.
+  constexpr bool kEarly = kBufs == 2;
+  static_assert(!kEarly || (MI == 8 && kCa == 4 && kCb == 4), "early copies");
+  auto stage = [&](int g, int c) {  // in turn g of group c, into its own buffer
+    if constexpr (kEarly) {
+      if (g >= 1 && g <= 4) stage_piece(kCa + g - 1, c + kBufs, cur);
+      if (g == 5) stage_piece(0, c + kBufs, cur);
+      if (g == 6) stage_piece(2, c + kBufs, cur);
+      if (g == 7) {
+        stage_piece(1, c + kBufs, cur);
+        stage_piece(3, c + kBufs, cur);
+        stage_piece(kCa + kCb, c + kBufs, cur);
+      }
+    } else if (g == MI - 1) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) stage_piece(i, c + kBufs, cur);
+    }
+  };
+  auto meet = [&](int g) {
+    if (g == MI - 1) {
+      wait_copies<kEarly ? 6 : (kBufs - 2) * kPieces>();
+      lds_barrier();
+    } else if (kEarly && (g == 1 || g == 5)) {
+      lds_barrier();
+    }
+  };
+  auto step = [&](int c, auto last_) {
     constexpr bool kLast = decltype(last_)::value;
     const uint32_t nxt = after(cur);
     Frag b[NI];
@@ -409,10 +434,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
 #pragma unroll
     for (int g = 0; g < MI; ++g) {
       const bool border = g == MI - 1;
-      if (!kLast && border) {
-        wait_copies<(kBufs - 2) * kPieces>();
-        lds_barrier();
-      }
+      if (!kLast) meet(g);
       const Frag a = operand(fa[g & 1]);
       const float f0 = sa[g & 1] * sw[0], f1 = ACT ? sa[g & 1] * sw[1] : 0.f;
       if (!border) read_a(g + 1, cur);
@@ -420,18 +442,22 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
         read_a(0, nxt);
         read_w(nxt);
       }
+      if (!kLast) stage(g, c);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         add(g == 0 ? MI - 1 : g - 1, j);
         part[j] = group_sums(b[j], a);
-        if (!kLast && border) {
-          fb[j] = raw(nxt + off_b, j);
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-            if (i * NI / kPieces == j) stage_piece(i, cur);
-        }
+        if (!kLast && border) fb[j] = raw(nxt + off_b, j);
       }
       f[0] = f0, f[1] = f1;
+      if (!EXACT && !border) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     cur = nxt;
@@ -439,7 +465,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
 #pragma unroll 1
   for (int i = 0; i < kBufs; ++i)
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) stage_piece(j, base + i * kBuf);
+    for (int j = 0; j < kPieces; ++j) stage_piece(j, i, base + i * kBuf);
   wait_copies<(kBufs - 1) * kPieces>();  // the first group's
   lds_barrier();
   if (wm < mn) {
@@ -447,18 +473,20 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
 #pragma unroll
     for (int j = 0; j < NI; ++j) fb[j] = raw(cur + off_b, j);
     read_a(0, cur);
+    int c = 0;
 #pragma unroll 1
-    for (int c = 1; c < kg; ++c) step(std::false_type{});
-    step(std::true_type{});
+    for (; c + 1 < kg; ++c) step(c, std::false_type{});
+    step(c, std::true_type{});
 #pragma unroll
     for (int j = 0; j < NI; ++j) add(MI - 1, j);
   } else {  // a wave past the tile's rows only copies
 #pragma unroll 1
-    for (int c = 1; c < kg; ++c) {
-      wait_copies<(kBufs - 2) * kPieces>();
-      lds_barrier();
+    for (int c = 0; c + 1 < kg; ++c) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) stage_piece(i, cur);
+      for (int g = 0; g < MI; ++g) {
+        meet(g);
+        stage(g, c);
+      }
       cur = after(cur);
     }
   }
