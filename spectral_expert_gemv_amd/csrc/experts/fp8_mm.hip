@@ -283,7 +283,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
 constexpr int kTile = 256;  // rows and weight rows of a whole tile
 constexpr uint32_t kScaleLds = 2048;                              // of one buffer
 constexpr uint32_t kLds8 = 3 * ((kTile + kTile / 2) * kGroup + kScaleLds);  // three buffers of a 256 x 128 tile
-constexpr uint32_t kOutLds8 = 2 * 2 * kTile * kGroup;             // of the output on its way
 
 __device__ const float g_nan = __builtin_nanf("");
 
@@ -296,6 +295,15 @@ template <class V>
 __device__ __forceinline__ V lds_read(uint32_t at) {
   typedef __attribute__((address_space(3))) const V lds_v;
   return *(lds_v*)(uintptr_t)at;
+}
+
+// SiLU(g) u for a 16-bit output: the exponent -g log2(e) keeps its own
+// rounding, off by up to 5e-6 of the result (|g| < 87), where the sums' 14 bits
+// may be off by more; two thirds of gated()'s time, which is 5 us of a tile's
+// 38 with 2048 inputs.
+__device__ __forceinline__ float gated16(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(g * -1.44269502162933349609375f);
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // Sorted rows m0 .. m0 + mn, weight rows (of each half) n0 .. n0 + nn of expert e.
@@ -494,60 +502,62 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
 
   // The products were formed transposed: lane % 16 is the output row, and a
   // lane holds 4 consecutive columns 4 (lane / 16) .. of each 16 x 16 tile.
-  // The tile goes through LDS, as far as it fits at a time, and leaves as
-  // whole rows, 16 bytes a lane.  16-byte piece p of LDS row r lies at
-  // p ^ (r % 16), which spreads 16 rows' writes over the banks.
-  constexpr int kOut = ACT ? TN / 2 : TN;  // columns
-  constexpr int kFit = kOutLds8 / (kOut * (int)sizeof(O));
-  constexpr int kPassRows = kFit < TM ? kFit : TM;
-  constexpr int kPasses = TM / kPassRows, kI = MI / kPasses;  // 16-row blocks of a wave per pass
-  constexpr int kRowPieces = kOut * (int)sizeof(O) / 16;
-  constexpr int kKey = kRowPieces < 16 ? kRowPieces - 1 : 15;
-  static_assert(kPassRows * kPasses == TM && kI * kPasses == MI, "whole passes");
-  O* Y = (O*)s.y;
-  const int64_t ldy = s.ldy;
+  // 16-bit outputs: two tiles side by side trade their odd and even quarters,
+  // which leaves every lane 8 consecutive columns of one of them, so a store
+  // writes 16 bytes a lane and 64 a row (a wave with one tile across trades
+  // with the next 16 rows: 32 a row); float32 ones do as they are.
+  if (wm >= mn) return;
+  O* Y = (O*)s.y + (int64_t)m0 * s.ldy + n0;
+  constexpr int kPer = 16 / (int)sizeof(O);
+  constexpr int kOuts = ACT ? NI / 2 : NI;                             // output tiles of a wave across
+  constexpr int kTrade = sizeof(O) == 4 ? 0 : kOuts % 2 == 0 ? 1 : 2;  // with no tile, the next across, the next down
+  constexpr int kTiles = kTrade ? 2 : 1;
+  const int quarter = lane >> 4;
+  typedef __attribute__((ext_vector_type(kPer))) O On;
 #pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
-    // (nobody reads the operands, or the pass before, any more)
-    lds_barrier();
+  for (int i = 0; i < MI; i += kTrade == 2 ? 2 : 1) {
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const int row = (wv / WN) * (kPassRows / WM) + 16 * i + l16;
+    for (int j = 0; j < kOuts; j += kTrade == 1 ? 2 : 1) {
+      uint32_t w[4];
+      int row = wm + 16 * i + l16, col = (ACT ? wn / 2 : wn) + 16 * j + 4 * quarter;
+      f32x4 v[kTiles];
 #pragma unroll
-      for (int j = 0; j < NI; j += ACT ? 2 : 1) {
-        f32x4 v = acc[pass * kI + i][j];
+      for (int u = 0; u < kTiles; ++u) {
+        const int ii = i + (kTrade == 2 ? u : 0), jj = j + (kTrade == 1 ? u : 0);
+        v[u] = acc[ii][jj * (ACT ? 2 : 1)];
         if constexpr (ACT) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = gated(v[q], acc[pass * kI + i][j + 1][q]);
+          for (int q = 0; q < 4; ++q) {
+            const float g = v[u][q], up = acc[ii][jj * 2 + 1][q];
+            v[u][q] = EXACT ? gated(g, up) : gated16(g, up);
+          }
         }
-        typedef __attribute__((ext_vector_type(4))) O O4;
-        O4 o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = (O)v[q];
-        const int at = ((ACT ? (wn + 16 * j) / 2 : wn + 16 * j) + 4 * (lane >> 4)) * (int)sizeof(O);
-        typedef __attribute__((address_space(3))) O4 lds_o4;
-        *(lds_o4*)(uintptr_t)(base + row * (kOut * (int)sizeof(O)) +
-                              ((((at >> 4) ^ (row & kKey)) << 4) | (at & 15))) = o;
       }
-    }
-    lds_barrier();
-#pragma unroll 4
-    for (int at = threadIdx.x; at < kPassRows * kRowPieces; at += NT) {
-      const int row = at / kRowPieces, p = at % kRowPieces;
-      // the output row behind LDS row `row` of this pass
-      const int m = row / (kPassRows / WM) * (TM / WM) + pass * (kPassRows / WM) + row % (kPassRows / WM);
-      const i32x4 v = lds_read<i32x4>(base + row * (kOut * (int)sizeof(O)) + ((p ^ (row & kKey)) << 4));
-      constexpr int kPer = 16 / (int)sizeof(O);
-      const int n = p * kPer;
-      O* y = Y + (int64_t)(m0 + m) * ldy + n0 + n;
-      if (m < mn && s.y16 && n + kPer <= nn) {
-        *reinterpret_cast<i32x4*>(y) = v;
-      } else if (m < mn) {
-        typedef __attribute__((ext_vector_type(kPer))) O On;
-        const On o = __builtin_bit_cast(On, v);
+      if constexpr (kTiles == 2) {
+        typedef __attribute__((ext_vector_type(2))) O O2;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (n + j < nn) y[j] = o[j];
+        for (int h = 0; h < 2; ++h) {
+          const O2 a = {(O)v[0][2 * h], (O)v[0][2 * h + 1]}, b = {(O)v[1][2 * h], (O)v[1][2 * h + 1]};
+          const auto t = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                          __builtin_bit_cast(uint32_t, b), false, false);
+          w[h] = t[0], w[2 + h] = t[1];
+        }
+        col = (ACT ? wn / 2 : wn) + 16 * (j + (kTrade == 1 ? quarter & 1 : 0)) + 8 * (quarter >> 1);
+        if (kTrade == 2) row += 16 * (quarter & 1);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = __float_as_uint(v[0][q]);
+      }
+      if (row >= mn) continue;
+      O* y = Y + (int64_t)row * s.ldy + col;
+      const i32x4 o = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      if (s.y16 && col + kPer <= nn) {
+        *reinterpret_cast<i32x4*>(y) = o;
+      } else {
+        const On e = __builtin_bit_cast(On, o);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+          if (col + q < nn) y[q] = e[q];
       }
     }
   }
