@@ -604,7 +604,10 @@ __global__ __launch_bounds__(512, 2) void k_mm8_tile(Mm8Args s) {
   if constexpr (kExact) {
     mm8_tile<O, kTile, kTile / 2, 2, 4, 3, ACT, true>(s, base, t.e, t.row0, t.n, n0, nn);
   } else if (part < 0) {
-    mm8_tile<O, kTile, kTile, 2, 4, 2, ACT, false>(s, base, t.e, t.row0, t.n, n0, nn);
+    if (t.n <= kTile / 2)
+      mm8_tile<O, kTile / 2, kTile, 2, 4, 3, ACT, false>(s, base, t.e, t.row0, t.n, n0, nn);
+    else
+      mm8_tile<O, kTile, kTile, 2, 4, 2, ACT, false>(s, base, t.e, t.row0, t.n, n0, nn);
   } else if (parts == 4) {
     const int pm = (part & 1) * (kTile / 2), pn = (part >> 1) * (kCols / 2);
     t.n = min(kTile / 2, t.n - pm), nn = min(kCols / 2, nn - pn);
@@ -614,7 +617,10 @@ __global__ __launch_bounds__(512, 2) void k_mm8_tile(Mm8Args s) {
     const int pn = part * (kCols / 2);
     nn = min(kCols / 2, nn - pn);
     if (nn <= 0) return;
-    mm8_tile<O, kTile, kTile / 2, 2, 4, 3, ACT, false>(s, base, t.e, t.row0, t.n, n0 + pn, nn);
+    if (t.n <= kTile / 2)
+      mm8_tile<O, kTile / 2, kTile / 2, 2, 4, 4, ACT, false>(s, base, t.e, t.row0, t.n, n0 + pn, nn);
+    else
+      mm8_tile<O, kTile, kTile / 2, 2, 4, 3, ACT, false>(s, base, t.e, t.row0, t.n, n0 + pn, nn);
   }
 }
 
