@@ -108,8 +108,9 @@ struct FewLds {
   float scales[16 * kFewTurn];
 };
 
+// (at: for rows that are not codes, the index of row `lane` of all R <= 64 rows)
 template <class X, class O, bool ACT, int MB>
-__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, FewLds& lds) {
+__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int at, FewLds& lds) {
   constexpr bool kCodes = std::is_same<X, E4M3>::value;
   constexpr int kTurn = kFewTurn / MB;     // groups of a turn
   constexpr int U = kTurn / kFewWaves;     // of a wave, whose loads are in flight together
@@ -144,6 +145,26 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, FewLd
     // (groups past the last are loaded as it and not used)
     i32x8 vw[U][2], vx[U][MB];
     float sw[U][2], sx[U][MB];
+    // rows on their way to codes: 16 lanes a group, as in k_fp8_rows.  The first
+    // ones' loads come before the weights', so that their codes are made while
+    // the weights are on their way.
+    const int groups = t.n * kTurn, l = threadIdx.x & 15;
+    auto load_row = [&](int i, float (&v)[8]) {
+      const int row = i / kTurn, c = (g0 + i % kTurn) * kGroup + 8 * l;
+      int xr = t.row0 + min(row, t.n - 1);
+      if (s.rows) {
+        const int p = __shfl(at, xr, 64);
+        xr = p < 0 || p / s.div >= s.x_rows ? -1 : p / s.div;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      typedef typename std::conditional<kCodes, f16, X>::type Elem;
+      if (i < groups && xr >= 0) load8_any((const Elem*)s.x + (int64_t)xr * s.ldx + c, s.K - c, v);
+      return xr;
+    };
+    float v[8];
+    int xr = 0;
+    if constexpr (!kCodes) xr = load_row(threadIdx.x >> 4, v);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int g = min(g0 + u * kFewWaves + wv, s.kg - 1);
@@ -159,13 +180,9 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, FewLd
     }
     if constexpr (!kCodes) {
       if (g0) __syncthreads();  // (the turn before is read)
-      // 16 lanes a group, as in k_fp8_rows
-      const int groups = t.n * kTurn, l = threadIdx.x & 15;
       for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
-        const int row = i / kTurn, g = i % kTurn, c = (g0 + g) * kGroup + 8 * l;
-        const int xr = i < groups ? x_row8(s, t.row0 + row) : -1;
-        float v[8] = {};
-        if (xr >= 0) load8_any((const X*)s.x + (int64_t)xr * s.ldx + c, s.K - c, v);
+        const int row = i / kTurn, g = i % kTurn;
+        if (i >= 16) xr = load_row(i, v);
         uint32_t a = row_max(amax_bits<false>(v));
         if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
         const Factors f = factors8(a);
@@ -246,6 +263,8 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, FewLd
 template <class X, class O, bool ACT>
 __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
   __shared__ FewLds lds;
+  int at = 0;
+  if (!std::is_same<X, E4M3>::value && s.rows) at = s.rows[min((int)threadIdx.x & 63, s.R - 1)];
   Tile t{0, 0, 0};
   if (s.bounds) {
     t = find_tile(s.bounds, s.E, s.R, blockIdx.y, kFewRows);
@@ -255,11 +274,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
   }
   if (t.n <= 0) return;
   if (t.n <= 16)
-    few8_rows<X, O, ACT, 1>(s, t, lds);
+    few8_rows<X, O, ACT, 1>(s, t, at, lds);
   else if (t.n <= 32)
-    few8_rows<X, O, ACT, 2>(s, t, lds);
+    few8_rows<X, O, ACT, 2>(s, t, at, lds);
   else
-    few8_rows<X, O, ACT, 4>(s, t, lds);
+    few8_rows<X, O, ACT, 4>(s, t, at, lds);
 }
 
 // --------------------------------------------------------------- tiled
@@ -634,24 +653,36 @@ void with_out(int o_dtype, F f) {
     f(bf16{});
 }
 
-// Up to kFewMean rows per expert on average the few-rows kernel is the faster
-// one, up to kFewMeanSmall while there are few 256 x 256 tiles to spread over
-// the chip.
-constexpr int kFewMean = 12, kFewMeanSmall = 32, kFewTiles = 32;
+// The few-rows kernel is the faster one up to 7 rows per expert on average, and
+// up to 2048 / tiles where there are few 256 x 256 tiles to spread over the
+// chip.  us by it and by the tiled one, from codes: 128 experts of 1536 x 2048
+// (768 tiles), 4 rows 75 and 80, 8 rows 81 and 81, 16 rows 95 and 82; 8 experts
+// of 4096 x 4096 (128 tiles), 16 rows 34 and 36, 32 rows 42 and 36; one of
+// 14336 x 4096 (56 tiles), 32 rows 22 and 22, 64 rows 33 and 25; one of 4096 x
+// 4096 (16 tiles), 64 rows 18 and 22, 128 rows 19 and 30.
+constexpr int kFewMean = 7, kFewByTiles = 2048, kFewMost = 256;
 
 bool few8(int R, int E, int N) {
   const long long tiles = (long long)((N + kTile - 1) / kTile) * E * ((R / E + kTile - 1) / kTile);
-  return R <= (long long)(tiles <= kFewTiles ? kFewMeanSmall : kFewMean) * E &&
-         max_tiles(R, E, kFewRows) <= 65535;
+  const long long by = tiles ? kFewByTiles / tiles : kFewMost;
+  const long long mean = by < kFewMean ? kFewMean : by < kFewMost ? by : kFewMost;
+  return R <= mean * E && max_tiles(R, E, kFewRows) <= 65535;
 }
 
-// The workspace of rows that are quantized before the tiled products: codes,
-// then scales.
+// Rows are quantized by the work-groups that use them, without a launch of
+// their own, where hardly an expert has more than one: each work-group of an
+// expert does it again (one row of 128 experts 76 us, from codes 70; 8 rows of
+// one 4096 x 4096 projection 19 us, from codes 9 and 3 to make them).
+// (k_mm8_few reads the indexes of up to 64 rows at once for it.)
+bool on_the_way(int R, int E) { return R <= 2 || (R <= 32 && R <= E); }
+
+// The workspace of rows that are quantized before the products: codes, then
+// scales.
 struct RowsWs {
   size_t codes, scales;
 };
 RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K) {
-  if (x_dtype == kE4M3 || few8(R, E, N)) return RowsWs{0, 0};
+  if (x_dtype == kE4M3 || (few8(R, E, N) && on_the_way(R, E))) return RowsWs{0, 0};
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   return RowsWs{al((size_t)rows * groups_of(K) * kGroup), al((size_t)rows * groups_of(K) * 4)};
 }
@@ -762,7 +793,7 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
         hipLaunchKernelGGL((k_mm8_few<X, O, false>), grid, dim3(64 * kFewWaves), 0,
                            (hipStream_t)stream, s);
     };
-    if (given)
+    if (given || need)
       go(E4M3{});
     else if constexpr (std::is_same<O, f16>::value)
       go(f16{});
