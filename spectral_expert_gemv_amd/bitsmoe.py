@@ -892,16 +892,16 @@ def fp8_matmul(x, codes, scales, y=None, x_scales=None, bounds=None, rows=None, 
             raise ValueError("x_scales must be float32")
         ps, lds = _matrix("x_scales", x_scales, (x_rows, kp // GROUP))
     pr, div = _gather(x, rows, div, R)
+    pc = _array("codes", codes, _F8)
+    pw = _array("scales", scales, _F32, (E, -(-N // GROUP) * (2 if act else 1), kp // GROUP))
+    pb = None if bounds is None else _bounds(bounds, E)
     if y is None:
         y = _new((R, N), torch.bfloat16 if given else x.dtype, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
-    if ws is None:
+    if ws is None and not given:
         ws = _scratch(fp8_matmul_workspace_size(x.dtype, x_rows, R, E, N, K, act), dev, stream)
     _enqueue(_lib.bitsmoe_fp8_matmul, dev, stream, 3 if given else _dtype(x), px, ldx, ps, lds, x_rows,
-             pr, div, _array("codes", codes, _F8),
-             _array("scales", scales, _F32, (E, _groups(N) * (2 if act else 1), kp // GROUP)),
-             None if bounds is None else _bounds(bounds, E), R, E, N, K, ACT[act], py, _dtype(y),
-             ldy, _ptr(ws), _ws_bytes(ws))
+             pr, div, pc, pw, pb, R, E, N, K, ACT[act], py, _dtype(y), ldy, _ptr(ws), _ws_bytes(ws))
     return y
 
 

@@ -43,8 +43,59 @@ __device__ inline float reduce_sum(float v) {
   return reduce<L>(v, [](float a, float b) { return a + b; });
 }
 
-// The softmax of one token over the L lanes that hold it, expert v L + l in
-// value v of lane l.
+// exp(x), x <= 0: exp2 of the product with log2(e), whose rounding error and low
+// part are put back by one multiplication (each within a float32 step; for -inf
+// the median keeps the factor finite).
+__device__ __forceinline__ float exp_below(float x) {
+#pragma clang fp contract(off)
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;
+  const float t = x * kHi;
+  const float lo = __builtin_amdgcn_fmed3f(fmaf(x, kLo, fmaf(x, kHi, -t)), -1.0f, 1.0f);
+  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182464599609375f, 1.0f);
+}
+
+// Experts l V .. l V + V - 1 of a token in lane l of its L: V consecutive
+// elements from any element's alignment (the hardware takes it).
+template <class T, int V>
+struct Run {
+  T v[V];
+};
+template <class T, int V>
+__device__ __forceinline__ Run<T, V> load_run(const T* p, int left) {  // -inf from the left-th on
+  Run<T, V> r;
+  if (left >= V) {
+    __builtin_memcpy(&r, p, sizeof(r));
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.v[v] = v < left ? p[v] : (T)-INFINITY;
+  }
+  return r;
+}
+template <class T, int V>
+__device__ __forceinline__ void store_run(T* p, const Run<T, V>& r, int left) {
+  if (left >= V) {
+    __builtin_memcpy(p, &r, sizeof(r));
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < left) p[v] = r.v[v];
+  }
+}
+
+// What a lane reads of a token: its experts' logits, and whether one of its ids
+// (every L-th) is one of the experts'.
+template <class T, int L, int V>
+struct Token {
+  Run<T, V> x;
+  int32_t id;  // the lane's first id, -1 past the k-th
+  __device__ __forceinline__ void load(const T* logits, const int32_t* ids, int E, int k, bool live) {
+    const int l = threadIdx.x & (L - 1);
+    x = load_run<T, V>(logits + l * V, live ? E - l * V : 0);
+    id = live && l < k ? ids[l] : -1;
+  }
+};
+
+// The softmax of one token over its L lanes.
 template <int V>
 struct Soft {
   float p[V];   // probabilities; NaN everywhere for a NaN or +inf among the logits
@@ -53,32 +104,31 @@ struct Soft {
 };
 
 template <class T, int L, int V>
-__device__ __forceinline__ Soft<V> soft(const T* __restrict__ logits, const int32_t* __restrict__ ids,
-                                        int E, int k, bool live) {
+__device__ __forceinline__ Soft<V> soft(const Token<T, L, V>& in, const int32_t* ids, int E, int k,
+                                        bool live) {
   const int l = threadIdx.x & (L - 1);
   Soft<V> o;
   float m = -INFINITY;
-  bool bad = false, any = false;
+  bool bad = false, any = in.id >= 0 && in.id < E;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * L + l;
-    o.p[v] = live && e < E ? to_f32(logits[e]) : -INFINITY;
+    o.p[v] = to_f32(in.x.v[v]);
     bad |= !(o.p[v] < INFINITY);
     m = fmaxf(m, o.p[v]);
   }
-  for (int j = l; j < k; j += L) any |= live && ids[j] >= 0 && ids[j] < E;
+  for (int j = l + L; j < k; j += L) any |= live && ids[j] >= 0 && ids[j] < E;
   m = reduce<L>(m, [](float a, float b) { return fmaxf(a, b); });
-  // bit 0: an id of the experts', bit 1: a NaN or +inf
-  float flags = (any ? 1.f : 0.f) + (bad ? 256.f : 0.f);
-  flags = reduce_sum<L>(flags);  // (at most 64 of each: exact)
-  bad = flags >= 256.f;
-  any = flags != (bad ? floorf(flags * (1.f / 256.f)) * 256.f : 0.f);
+  // (whole waves; the flags of a token's lanes are a run of the ballots)
+  const int lane = threadIdx.x & 63;
+  const uint64_t mine = L == 64 ? ~0ull : 0xFFFFull << (lane & 48);
+  any = (__ballot(any) & mine) != 0;
+  bad = (__ballot(bad) & mine) != 0;
   o.part = any && (bad || m > -INFINITY);
   const float top = m > -INFINITY ? m : 0.f;
   float total = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    o.p[v] = expf(o.p[v] - top);
+    o.p[v] = exp_below(o.p[v] - top);
     total += o.p[v];
   }
   total = reduce_sum<L>(total);
@@ -96,88 +146,152 @@ __device__ __forceinline__ Tile chunk_of(const int32_t* __restrict__ seqs, int S
   return Tile{0, at * per, min(per, T - at * per)};
 }
 
-struct Part {  // of a chunk, after E probabilities' sums and E counts
-  float z;
-  int32_t n;
+// Calls f for the chunk's tokens, NT / L at a time, kFlight tokens' loads in
+// flight together.
+template <class T, int L, int V, int NT, class F>
+__device__ __forceinline__ void each_token(const Tile& c, const T* __restrict__ logits, int64_t ld,
+                                           const int32_t* __restrict__ ids, int E, int k, F f) {
+  constexpr int G = NT / L;
+  constexpr int kFlight = V <= 16 ? 2 : 1;
+  const int group = threadIdx.x / L;
+  for (int i0 = 0; i0 < c.n; i0 += G * kFlight) {
+    Token<T, L, V> in[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const bool live = i0 + u * G + group < c.n;
+      const int64_t t = c.row0 + (live ? i0 + u * G + group : 0);
+      in[u].load(logits + t * ld, ids + t * k, E, k, live);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (i0 + u * G >= c.n) break;
+      const bool live = i0 + u * G + group < c.n;
+      const int64_t t = c.row0 + (live ? i0 + u * G + group : 0);
+      f(t, live, in[u], soft<T, L, V>(in[u], ids + t * k, E, k, live));
+    }
+  }
+}
+
+// Sum over a work-group of W waves, in lane 0 of wave 0 (buf: W doubles, not
+// read or written by others before the next barrier).
+template <int W>
+__device__ __forceinline__ double block_sum(double v, double* buf) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  if (lane == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = lane < W ? buf[lane] : 0.0;
+#pragma unroll
+  for (int d = 1; d < W; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// Words of a chunk's record: E probabilities' sums (float), E counts, z, n.
+__host__ __device__ inline size_t record(int E) { return (2 * (size_t)E + 2 + 3) / 4 * 4; }
+
+struct Outs {
+  float *loss, *z;
+  int32_t *counts, *tokens;
 };
 
-// Sums of one chunk: [E] float probabilities, [E] counts, z, n.
-template <class T, int L, int V>
-__global__ __launch_bounds__(kThreads) void k_balance_part(
+// Sums of one chunk into its record; ONE: of the only chunk there is, whose
+// losses it writes.  Bound by latencies and the exp (16384 tokens of 128
+// experts, 8.4 MB: 5 us).
+template <class T, int L, int V, int NT, bool ONE>
+__global__ __launch_bounds__(NT) void k_balance_part(
     const T* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ seqs, int S, int T_, int E, int k, int per,
-    uint32_t* __restrict__ parts) {
-  constexpr int G = kThreads / L;  // tokens at a time
-  extern __shared__ uint32_t lds[];
-  float* sums = (float*)lds;       // [G][E]
-  int32_t* count = (int32_t*)(lds + G * E);
-  float* zs = (float*)(count + E);
-  int32_t* ns = (int32_t*)(zs + G);
+    uint32_t* __restrict__ parts, Outs o) {
+  constexpr int W = NT / 64;
+  extern __shared__ double dlds[];
+  double* buf = dlds;              // [W]
+  float* sums = (float*)(dlds + W);  // [W][E]
+  float* zs = sums + (size_t)W * E;
+  int32_t* ns = (int32_t*)(zs + W);
+  int32_t* count = ns + W;         // [E]
   const Tile c = chunk_of(seqs, S, T_, blockIdx.x, per);
-  if (c.n <= 0) return;
-  const int tid = threadIdx.x, l = tid & (L - 1), group = tid / L;
-  for (int e = tid; e < E; e += kThreads) count[e] = 0;
+  if (!ONE && c.n <= 0) return;
+  const int tid = threadIdx.x, l = tid & (L - 1), wv = tid >> 6;
+  for (int e = tid; e < E; e += NT) count[e] = 0;
   __syncthreads();
   float sum[V] = {}, z = 0.f;
   int n = 0;
-  for (int i0 = 0; i0 < c.n; i0 += G) {
-    const int64_t t = c.row0 + i0 + group;
-    const bool live = i0 + group < c.n;
-    const Soft<V> s = soft<T, L, V>(logits + (live ? t : 0) * ld, ids + (live ? t : 0) * k, E, k, live);
+  each_token<T, L, V, NT>(c, logits, ld, ids, E, k, [&](int64_t t, bool, const Token<T, L, V>& in, const Soft<V>& s) {
     if (s.part) {
 #pragma unroll
       for (int v = 0; v < V; ++v) sum[v] += s.p[v];
       z += s.lse * s.lse;
       ++n;
-      for (int j = l; j < k; j += L) {
+      if (in.id >= 0 && in.id < E) atomicAdd(&count[in.id], 1);
+      for (int j = l + L; j < k; j += L) {
         const int id = ids[t * k + j];
         if (id >= 0 && id < E) atomicAdd(&count[id], 1);
       }
     }
-  }
+  });
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (v * L + l < E) sums[group * E + v * L + l] = sum[v];
-  if (l == 0) zs[group] = z, ns[group] = n;
-  __syncthreads();
-  uint32_t* out = parts + (size_t)blockIdx.x * (2 * E + 2);
-  for (int e = tid; e < E; e += kThreads) {
-    float p = 0.f;
-#pragma unroll 4
-    for (int g = 0; g < G; ++g) p += sums[g * E + e];
-    out[e] = __float_as_uint(p);
-    out[E + e] = (uint32_t)count[e];
+  for (int d = L; d < 64; d <<= 1) {  // the wave's tokens
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] += __shfl_xor(sum[v], d, 64);
+    z += __shfl_xor(z, d, 64);
+    n += __shfl_xor(n, d, 64);
   }
-  if (tid == 0) {
+  if ((tid & 63) < L) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (l * V + v < E) sums[wv * E + l * V + v] = sum[v];
+    if (l == 0) zs[wv] = z, ns[wv] = n;
+  }
+  __syncthreads();
+  z = 0.f, n = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) z += zs[w], n += ns[w];
+  double part = 0.0;
+  uint32_t* out = ONE ? nullptr : parts + (size_t)blockIdx.x * record(E);
+  for (int e = tid; e < E; e += NT) {
     float p = 0.f;
-    int32_t m = 0;
-    for (int g = 0; g < G; ++g) p += zs[g], m += ns[g];
-    out[2 * E] = __float_as_uint(p);
-    out[2 * E + 1] = (uint32_t)m;
+#pragma unroll
+    for (int w = 0; w < W; ++w) p += sums[w * E + e];
+    if (ONE) {
+      o.counts[e] = count[e];
+      part += (double)count[e] * (double)p;
+    } else {
+      out[e] = __float_as_uint(p);
+      out[E + e] = (uint32_t)count[e];
+    }
+  }
+  if (ONE) {
+    part = block_sum<W>(part, buf);
+    const double inv = n > 0 ? 1.0 / n : 0.0;
+    if (tid == 0) {
+      o.loss[0] = (float)(part * inv * inv * ((double)E / k));
+      o.z[0] = (float)((double)z * inv);
+      o.tokens[0] = n;
+    }
+  } else if (tid == 0) {
+    out[2 * E] = __float_as_uint(z);
+    out[2 * E + 1] = (uint32_t)n;
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* buf) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < (int)blockDim.x / 64; ++w) v += buf[w];
-  return v;
-}
-
-// One work-group per sequence: its chunks' sums in chunk order, then the
-// losses.  `split` threads share an expert's chunks.
+// One work-group per sequence: its chunks' records in chunk order, then the
+// losses.  A thread takes W words of a record (4, 16 bytes, where E allows it)
+// of every `split`-th chunk, up to 16 of them in flight.  Bound by what one
+// compute unit reads (256 records of 128 experts, 262 KB: 5 us).
 constexpr int kJoin = 1024;
+__host__ __device__ inline int join_split(int E, int W) {
+  const int n = kJoin / (2 * E / W);
+  return n < 1 ? 1 : n > 16 ? 16 : n;
+}
+template <int W>
 __global__ __launch_bounds__(kJoin) void k_balance_join(
     const uint32_t* __restrict__ parts, const int32_t* __restrict__ seqs, int S, int T_, int E,
-    int k, int per, int chunks, float* __restrict__ loss, float* __restrict__ z,
-    int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
+    int k, int per, int chunks, Outs o) {
   extern __shared__ double dlds[];
-  double* buf = dlds;                // [16]
-  double* ps = dlds + 16;            // [split][E]
+  const int split = join_split(E, W), q2 = 2 * E / W;  // words / W of a record's sums
+  double* ps = dlds;                              // [split][E]
+  int32_t* cs = (int32_t*)(ps + (size_t)split * E);  // [split][E]
   const int s = blockIdx.x, tid = threadIdx.x;
   int first = 0, last = chunks;
   if (seqs) {  // chunks of the sequences before this one
@@ -186,41 +300,70 @@ __global__ __launch_bounds__(kJoin) void k_balance_join(
     expert_rows(seqs, s, T_, lo, hi);
     last = min(chunks, first + (hi - lo + per - 1) / per);
   }
-  const size_t len = 2 * (size_t)E + 2;
-  const int split = kJoin / E < 1 ? 1 : kJoin / E;
-  int32_t* cs = (int32_t*)(ps + (size_t)split * E);  // [split][E]
-  for (int i = tid; i < split * E; i += kJoin) {
-    const int e = i % E, q = i / E;
-    double p = 0.0;
-    int32_t c = 0;
-#pragma unroll 4
-    for (int b = first + q; b < last; b += split) {
-      p += (double)__uint_as_float(parts[b * len + e]);
-      c += (int32_t)parts[b * len + E + e];
-    }
-    ps[i] = p, cs[i] = c;
-  }
+  const size_t len = record(E);
+  struct Words {
+    uint32_t w[W];
+  };
   double zz = 0.0, nn = 0.0;
-  for (int b = first + tid; b < last; b += kJoin) {
-    zz += (double)__uint_as_float(parts[b * len + 2 * E]);
-    nn += (double)(int32_t)parts[b * len + 2 * E + 1];
+  if (tid < 64)
+    for (int b = first + tid; b < last; b += 64) {
+      zz += (double)__uint_as_float(parts[b * len + 2 * E]);
+      nn += (double)(int32_t)parts[b * len + 2 * E + 1];
+    }
+  for (int i = tid; i < split * q2; i += kJoin) {
+    const int q = i / q2, j = (i - q * q2) * W;
+    const bool whole = j >= E;  // counts
+    double p[W] = {};
+    int32_t c[W] = {};
+    constexpr int kFlight = 16;
+    const uint32_t* at = parts + (size_t)(first + q) * len + j;
+    for (int b0 = first + q; b0 < last; b0 += split * kFlight) {
+      Words x[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        x[u] = Words{};
+        if (b0 + u * split < last) __builtin_memcpy(&x[u], __builtin_assume_aligned(at, 4 * W), sizeof(Words));
+        at += split * len;
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+          if (whole)
+            c[v] += (int32_t)x[u].w[v];
+          else
+            p[v] += (double)__uint_as_float(x[u].w[v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      if (whole)
+        cs[q * E + j - E + v] = c[v];
+      else
+        ps[q * E + j + v] = p[v];
+    }
   }
-  zz = block_sum(zz, buf);
-  nn = block_sum(nn, buf);
-  const double inv = nn > 0.0 ? 1.0 / nn : 0.0;
+  __syncthreads();
+  if (tid >= 64) return;
   double part = 0.0;
-  for (int e = tid; e < E; e += kJoin) {
+  for (int e = tid; e < E; e += 64) {
     double p = 0.0;
     int32_t c = 0;
+#pragma unroll 8
     for (int q = 0; q < split; ++q) p += ps[q * E + e], c += cs[q * E + e];
-    counts[(size_t)s * E + e] = c;
-    part += (double)c * inv * p * inv;
+    o.counts[(size_t)s * E + e] = c;
+    part += (double)c * p;
   }
-  part = block_sum(part, buf);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const double a = __shfl_xor(part, d, 64), b = __shfl_xor(zz, d, 64), n = __shfl_xor(nn, d, 64);
+    part += a, zz += b, nn += n;
+  }
   if (tid == 0) {
-    loss[s] = (float)(part * ((double)E / k));
-    z[s] = (float)(zz * inv);
-    tokens[s] = (int32_t)nn;
+    const double inv = nn > 0.0 ? 1.0 / nn : 0.0;
+    o.loss[s] = (float)(part * inv * inv * ((double)E / k));
+    o.z[s] = (float)(zz * inv);
+    o.tokens[s] = (int32_t)nn;
   }
 }
 
@@ -231,10 +374,9 @@ __global__ __launch_bounds__(kThreads) void k_balance_grad(
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
     const float* __restrict__ dloss, const float* __restrict__ dz, T* __restrict__ dl,
     int64_t ldd) {
-  constexpr int G = kThreads / L;
   const Tile c = chunk_of(seqs, S, T_, blockIdx.x, per);
   if (c.n <= 0) return;
-  const int tid = threadIdx.x, l = tid & (L - 1), group = tid / L;
+  const int l = threadIdx.x & (L - 1);
   const int n = tokens[c.e];
   const float inv = n > 0 ? 1.0f / (float)n : 0.f;
   const float a = dloss ? dloss[c.e] * inv : 0.f, b = dz ? 2.0f * dz[c.e] * inv : 0.f;
@@ -242,27 +384,26 @@ __global__ __launch_bounds__(kThreads) void k_balance_grad(
   const float unit = (float)E / (float)k * inv;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * L + l;
+    const int e = l * V + v;
     f[v] = e < E ? (float)counts[(size_t)c.e * E + e] * unit : 0.f;
   }
-  for (int i0 = 0; i0 < c.n; i0 += G) {
-    const int64_t t = c.row0 + i0 + group;
-    const bool live = i0 + group < c.n;
-    const Soft<V> s = soft<T, L, V>(logits + (live ? t : 0) * ld, ids + (live ? t : 0) * k, E, k, live);
+  each_token<T, L, V, kThreads>(c, logits, ld, ids, E, k, [&](int64_t t, bool live, const Token<T, L, V>&, const Soft<V>& s) {
     float mean = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) mean += s.p[v] * f[v];
     mean = reduce_sum<L>(mean);
-    if (!live || (ADD && !s.part)) continue;
+    if (!live || (ADD && !s.part)) return;
+    T* to = dl + t * ldd + l * V;
+    Run<T, V> d;
+    if (ADD) d = load_run<T, V>(to, E - l * V);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * L + l;
-      if (e >= E) continue;
-      float d = s.part ? s.p[v] * (a * (f[v] - mean) + b * s.lse) : 0.f;
-      if (ADD) d += to_f32(dl[t * ldd + e]);
-      dl[t * ldd + e] = from_f32<T>(d);
+      float g = s.part ? s.p[v] * (a * (f[v] - mean) + b * s.lse) : 0.f;
+      if (ADD) g += to_f32(d.v[v]);
+      d.v[v] = from_f32<T>(g);
     }
-  }
+    store_run<T, V>(to, d, E - l * V);
+  });
 }
 
 // As in the router: a row of 16 lanes up to 256 experts, a wave beyond.
@@ -294,17 +435,23 @@ void with_type(int dtype, F f) {
     f(bf16{});
 }
 
-// Tokens of a chunk: four turns of 16 tokens at a time, more where that would
-// make over 512 chunks of a sequence.
+// Tokens of a chunk: two turns of 32 tokens at a time, more where that would
+// make over 512 chunks of a sequence; one chunk (of 1024 lanes) of few tokens
+// in one sequence.
+constexpr int kOneTokens = 256;
 int chunk_tokens(int T) {
   const int per = (T + 511) / 512;
-  return per < 64 ? 64 : (per + 15) / 16 * 16;
+  return per < 64 ? 64 : (per + 31) / 32 * 32;
 }
+bool one_chunk(int T, int E, int S) { return S == 1 && T >= 1 && T <= kOneTokens && E <= 256; }
+constexpr int kGradTokens = 32;  // of a work-group of the gradient: two turns
 int max_chunks(int T, int S) {
   const int per = chunk_tokens(T);
   return T / per + (S < T ? S : T);
 }
-size_t parts_bytes(int T, int S, int E) { return (size_t)max_chunks(T, S) * (2 * (size_t)E + 2) * 4; }
+size_t parts_bytes(int T, int S, int E) {
+  return one_chunk(T, E, S) ? 0 : (size_t)max_chunks(T, S) * record(E) * 4;
+}
 
 int sizes(int dtype, int T, int E, int k, int S) {
   if (dtype != BITSMOE_F32 && !is_half(dtype)) return fail(BITSMOE_EINVAL, "dtype=%d", dtype);
@@ -342,28 +489,50 @@ int bitsmoe_moe_balance(int dtype, const void* logits, int64_t ld, const int32_t
   if (ld < E) return fail(BITSMOE_ESHAPE, "a row stride is smaller than E=%d", E);
   if (!loss || !z || !counts || !tokens || (T && (!logits || !ids)))
     return fail(BITSMOE_EINVAL, "null pointer argument");
-  if (parts_bytes(T, S, E) > ws_bytes || (T && !ws))
+  if (parts_bytes(T, S, E) > ws_bytes || (parts_bytes(T, S, E) && !ws))
     return fail(BITSMOE_ENOSPC, "ws_bytes=%zu < %zu", ws_bytes, parts_bytes(T, S, E));
   if ((uintptr_t)ws & 3u) return fail(BITSMOE_EINVAL, "misaligned workspace");
   const int per = chunk_tokens(T), chunks = seqs ? max_chunks(T, S) : (T + per - 1) / per;
+  const Outs o{loss, z, counts, tokens};
   hipStream_t q = (hipStream_t)stream;
+  const bool one = one_chunk(T, E, S);
   if (T) {
     with_type(dtype, [&](auto tag) {
       using X = decltype(tag);
       with_shape(E, [&](auto l, auto v) {
-        constexpr int L = decltype(l)::value, V = decltype(v)::value, G = kThreads / L;
-        const size_t lds = ((size_t)G * E + E + 2 * G) * 4;
-        hipLaunchKernelGGL((k_balance_part<X, L, V>), dim3((unsigned)chunks), dim3(kThreads), lds,
-                           q, (const X*)logits, ld, ids, seqs, S, T, E, k, per, (uint32_t*)ws);
+        constexpr int L = decltype(l)::value, V = decltype(v)::value;
+        auto go = [&](auto threads, auto one_) {
+          constexpr int NT = decltype(threads)::value, W = NT / 64;
+          constexpr bool ONE = decltype(one_)::value;
+          const size_t lds = W * 8 + ((size_t)W * E + 2 * W + E) * 4;
+          hipLaunchKernelGGL((k_balance_part<X, L, V, NT, ONE>), dim3(ONE ? 1u : (unsigned)chunks),
+                             dim3(NT), lds, q, (const X*)logits, ld, ids, seqs, S, T, E, k,
+                             ONE ? T : per, (uint32_t*)ws, o);
+        };
+        using std::integral_constant;
+        if constexpr (L == 16) {
+          if (one)
+            go(integral_constant<int, 1024>{}, std::true_type{});
+          else
+            go(integral_constant<int, 512>{}, std::false_type{});
+        } else {
+          go(integral_constant<int, 256>{}, std::false_type{});
+        }
       });
     });
     const int rc = launched("moe_balance sums");
-    if (rc) return rc;
+    if (rc || one) return rc;
   }
-  const int split = kJoin / E < 1 ? 1 : kJoin / E;
-  const size_t lds = 16 * 8 + (size_t)split * E * 12;
-  hipLaunchKernelGGL(k_balance_join, dim3((unsigned)S), dim3(kJoin), lds, q, (const uint32_t*)ws,
-                     seqs, S, T, E, k, per, chunks, loss, z, counts, tokens);
+  auto join = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    const size_t lds = (size_t)join_split(E, W) * E * 12;
+    hipLaunchKernelGGL((k_balance_join<W>), dim3((unsigned)S), dim3(kJoin), lds, q,
+                       (const uint32_t*)ws, seqs, S, T, E, k, per, chunks, o);
+  };
+  if (E % 4 == 0 && ((uintptr_t)ws & 15u) == 0)
+    join(std::integral_constant<int, 4>{});
+  else
+    join(std::integral_constant<int, 1>{});
   return launched("moe_balance");
 }
 
@@ -379,13 +548,14 @@ int bitsmoe_moe_balance_grad(int dtype, const void* logits, int64_t ld, const in
   if (T == 0) return BITSMOE_OK;
   if (!logits || !ids || !counts || !tokens || !dlogits)
     return fail(BITSMOE_EINVAL, "null pointer argument");
-  const int per = chunk_tokens(T), chunks = seqs ? max_chunks(T, S) : (T + per - 1) / per;
+  constexpr int per = kGradTokens;
+  const unsigned chunks = (unsigned)(seqs ? T / per + (S < T ? S : T) : (T + per - 1) / per);
   with_type(dtype, [&](auto tag) {
     using X = decltype(tag);
     with_shape(E, [&](auto l, auto v) {
       constexpr int L = decltype(l)::value, V = decltype(v)::value;
       auto go = [&](auto more) {
-        hipLaunchKernelGGL((k_balance_grad<X, L, V, decltype(more)::value>), dim3((unsigned)chunks),
+        hipLaunchKernelGGL((k_balance_grad<X, L, V, decltype(more)::value>), dim3(chunks),
                            dim3(kThreads), 0, (hipStream_t)stream, (const X*)logits, ld, ids, seqs,
                            S, T, E, k, per, counts, tokens, dloss, dz, (X*)dlogits, ldd);
       };
