@@ -405,8 +405,8 @@ def ssd(W, r, max_sweeps=30, ws=None, stream=None):
 
 # ------------------------------------------------ the expert layer's operators
 #
-# Routing, products with dense or 4-bit experts, the gated activation and the
-# combine, with their gradients.  Sorted rows: the T*k (token, slot) pairs
+# Routing with its balance loss, products with dense, 8-bit or 4-bit experts, the
+# gated activation and the combine, with their gradients.  Sorted rows: the T*k (token, slot) pairs
 # grouped by expert; `bounds` (E + 1), `order` (row -> pair) and `slot`
 # (pair -> row) come from moe_route or moe_group.  Matrices may have any row
 # stride; their rows are contiguous.  Without `stream` a call runs on the
@@ -475,16 +475,18 @@ def _enqueue(fn, index, stream, *args):
         _check(status)
 
 
-def _new(shape, dtype, index, stream, zero=False):
-    """A tensor that belongs to the stream the call runs on."""
+def _new(shape, dtype, index, stream, zero=False, value=None):
+    """A tensor that belongs to the stream the call runs on (and is filled on it)."""
     make = torch.zeros if zero else torch.empty
     dev = torch.device("cuda", index)
     if stream is None:
-        return make(shape, dtype=dtype, device=dev)
+        t = make(shape, dtype=dtype, device=dev)
+        return t if value is None else t.fill_(value)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
     with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=dev)
+        t = make(shape, dtype=dtype, device=dev)
+        return t if value is None else t.fill_(value)
 
 
 def _ws_bytes(ws):

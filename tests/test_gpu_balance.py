@@ -254,3 +254,25 @@ def test_repeats_streams_and_graphs(bm):
             assert torch.equal(a, b)
         for a, b in zip(both(), want):
             assert torch.equal(a, b)
+
+
+def test_logits_past_32_bits(bm):
+    """17 GB of them: the last sequence as by itself."""
+    T, E, k = 4200000, 1024, 2
+    l = torch.zeros(T, E, device="cuda")
+    g = rng(8)
+    tail, _ = make(g, 1000, E, k, F32, wide=0)
+    l[-1000:] = tail
+    ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    ids[-1000:] = torch.topk(tail, k, dim=1).indices.int()
+    seqs = torch.tensor([0, T - 1000, T], dtype=torch.int32, device="cuda")
+    loss, z, counts, tokens = bm.moe_balance(l, ids, seqs)
+    w = bm.moe_balance(tail, ids[-1000:].contiguous())
+    assert torch.equal(counts[1:], w[2]) and torch.equal(tokens[1:], w[3]) and tokens.tolist() == [T - 1000, 1000]
+    assert int(counts[0, 0]) == k * (T - 1000)
+    check(loss[1:], w[0].double(), w[0].double() * 2.0 ** -16, "loss")
+    check(z[1:], w[1].double(), w[1].double() * 2.0 ** -16, "z")
+    one = torch.ones(2, device="cuda")
+    d = bm.moe_balance_grad(l, ids, counts, tokens, one, one, seqs)
+    assert torch.equal(d[-1000:], bm.moe_balance_grad(tail, ids[-1000:].contiguous(), w[2], w[3], one[:1], one[:1]))
+    assert bool(d[:100].isfinite().all())

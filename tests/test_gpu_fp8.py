@@ -447,3 +447,296 @@ def test_no_rows(bm):
     bm.fp8_matmul(torch.ones(9, 128, dtype=BF16, device="cuda"), codes, scales, y, bounds=b)
     assert bool((y == 7.0).all())
     assert bm.fp8_weights(torch.empty(0, 5, 7, device="cuda"))[0].shape == (0, 5, 128)
+
+
+@pytest.mark.parametrize("E, step, most, N, K", [(4, 37, 1000, 2000, 256), (5, 100, 900, 2500, 128), (5, 61, 900, 3500, 256), (16, 40, 500, 1500, 384),
+                                                 (7, 13, 128, 4000, 256)])
+@pytest.mark.parametrize("out, act", [(BF16, None), (F32, None), (F16, "silu_mul"), (F32, "silu_mul")])
+def test_rounds_of_tiles(bm, E, step, most, N, K, out, act):
+    """Whole rounds of the chip's compute units and what is left over, whole or
+    cut in two or four, with experts of every height up to `most` rows."""
+    _say("fp8 rounds", E, step, most, N, K, out, act)
+    g = rng(E * most)
+    counts = [max(0, most - step * i) for i in range(E)]
+    bounds, R = ragged(counts)
+    n = R - 3
+    N = N // 2 if act else N
+    codes, scales = make_weights(bm, g, E, N, K, 2 if act else 1)
+    x = normal(g, R, K, dtype=BF16)
+    q, s = bm.fp8_rows(x)
+    y = torch.full((R, N), 7.0, dtype=out, device="cuda")
+    bm.fp8_matmul(q, codes, scales, y, x_scales=s, bounds=bounds, act=act)
+    want, off = reference(values(q, s, 1), weight_values(codes, scales, 2 if act else 1), bounds, R, act, out)
+    check(y[:n], want[:n], (half_step(want, out) + off + (want.abs() * 2.0 ** -20 if act else 0) + 1e-30)[:n], "y")
+    assert bool((y[n:] == 7.0).all())
+
+
+# ------------------------------------------------------- a run of them together
+
+def layer_inputs(T, E, k, D, F, dtype, seed):
+    g = rng(seed)
+    logits = normal(g, T, E)
+    if T > 5:
+        logits[T - 2:] = -INF  # padding
+    w1, w2 = normal(g, E, 2 * F, D, dtype=dtype, scale=D ** -0.5), normal(g, E, D, F, dtype=dtype, scale=F ** -0.5)
+    return logits, normal(g, T, D, dtype=dtype), w1, w2, normal(g, T, D, dtype=dtype)
+
+
+def dequantized(codes, scales, parts, cols):
+    return weight_values(codes, scales, parts)[:, :, :cols]
+
+
+@pytest.mark.parametrize("T, E, k, D, F", [(1, 8, 2, 64, 128), (1, 16, 4, 200, 96), (50, 16, 4, 200, 256), (300, 4, 2, 128, 128), (900, 8, 2, 384, 333)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_layer_of_8_bit_experts(bm, T, E, k, D, F, dtype, on_stream):
+    from spectral_expert_gemv_amd import ExpertLayer
+    _say("8-bit layer", T, E, k, D, F, dtype, on_stream)
+    logits, x, w1, w2, dout = layer_inputs(T, E, k, D, F, dtype, 23)
+    stream = torch.cuda.Stream() if on_stream else None
+    torch.cuda.synchronize()
+    grads = F % 128 == 0
+    layer = ExpertLayer.fp8(w1, w2, transposed=grads, stream=stream)
+    assert (layer.E, layer.D, layer.F) == (E, D, F)
+    out = layer.forward(x, logits, k, stream=stream)
+    got = layer.gradients(x, logits, k, dout, stream=stream) if grads else None
+    torch.cuda.synchronize()
+
+    # against the layer of the weights that the codes stand for, in 64 bits
+    parts = 1 if grads else 2
+    v1, v2 = dequantized(*layer.w1[:2], parts, D), dequantized(*layer.w2[:2], 1, F)
+    leaves = [t.double().requires_grad_() for t in (logits, x)]
+    l, xd = leaves
+    p = torch.softmax(l, 1)
+    top = torch.topk(logits, k, 1).indices
+    gate = p.gather(1, top)
+    gate = torch.zeros(T, E, dtype=F64, device="cuda").scatter(1, top, gate / gate.sum(1, keepdim=True)).nan_to_num(0.0)
+    want = 0
+    for e in range(E):
+        a = xd @ v1[e].t()
+        want = want + gate[:, e:e + 1] * ((torch.nn.functional.silu(a[:, :F]) * a[:, F:]) @ v2[e].t())
+    # 8-bit roundings of up to 2^-4 of a value: x enters h twice, and h; the 16-bit ones are far smaller
+    off = float((out.double() - want.detach()).norm() / want.detach().norm())
+    assert off < 3 * 2.0 ** -4, off
+    if T > 5:
+        assert not bool(out[T - 2:].any())
+
+    # the same bits from the operators one after another
+    ids, g, bounds, order, slot = layer.route(logits, k)
+    h = bm.fp8_matmul(x, *layer.w1[:2], bounds=bounds, rows=order, div=k, act="silu_mul")
+    y = bm.fp8_matmul(h, *layer.w2[:2], bounds=bounds)
+    assert torch.equal(bm.moe_combine(y, slot, g), out)
+    if not grads:
+        with pytest.raises(ValueError, match="transposed"):
+            layer.gradients(x, logits, k, dout)
+        if F % 128:
+            with pytest.raises(ValueError, match="multiple"):
+                ExpertLayer.fp8(w1, w2, transposed=True)
+        return
+    dx, dlogits, dw1, dw2 = got[1:5]
+    want.backward(dout.double())
+    # da is off by dy's rounding and, through a, by x's twice; its own rounding comes fourth
+    for name, a, b in (("dx", dx, xd.grad), ("dlogits", dlogits, l.grad.nan_to_num(0.0))):
+        err = float((a.double() - b).norm() / b.norm())
+        assert err < 4 * 2.0 ** -4, (name, err)
+    a = bm.fp8_matmul(x, *layer.w1[:2], bounds=bounds, rows=order, div=k)
+    hh = bm.silu_mul(a, bounds=bounds)
+    yy = bm.fp8_matmul(hh, *layer.w2[:2], bounds=bounds)
+    dy, dg = bm.moe_combine_grad(dout, yy, slot, g)
+    da = bm.silu_mul_grad(a, bm.fp8_matmul(dy, *layer.w2[2:], bounds=bounds), bounds=bounds)
+    assert torch.equal(bm.moe_combine(yy, slot, g), got[0])
+    assert torch.equal(bm.moe_combine(bm.fp8_matmul(da, *layer.w1[2:], bounds=bounds), slot), dx)
+    assert torch.equal(bm.grouped_matmul_dw(dy, hh, bounds), dw2)
+    assert torch.equal(bm.grouped_matmul_dw(da, x, bounds, rows=order, div=k), dw1)
+    assert torch.equal(bm.moe_route_grad(logits, ids, dg, renorm=True), dlogits)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_layer_gradients_with_the_balance_loss(bm, eight):
+    """Its gradient is added to the router's, whatever the experts are made of."""
+    from spectral_expert_gemv_amd import ExpertLayer
+    T, E, k, D, F = 120, 8, 2, 128, 128
+    logits, x, w1, w2, dout = layer_inputs(T, E, k, D, F, BF16, 4)
+    layer = ExpertLayer.fp8(w1, w2, transposed=True) if eight else ExpertLayer(w1, w2)
+    seqs = torch.tensor([0, 50, 120], dtype=torch.int32, device="cuda")
+    base = layer.gradients(x, logits, k, dout)
+    got = layer.gradients(x, logits, k, dout, balance=0.02, z=0.001, seqs=seqs)
+    assert len(base) == 5 and len(got) == 6
+    for i in (0, 1, 3, 4):
+        assert torch.equal(base[i], got[i])
+    l = logits.double().requires_grad_()
+    ids = layer.route(logits, k)[0]
+    total, loss, z, counts = 0, [], [], []
+    for a, b in ((0, 50), (50, T - 2)):  # the last two tokens are padding
+        p = torch.softmax(l[a:b], 1)
+        c = torch.bincount(ids[a:b].reshape(-1), minlength=E)
+        loss.append(((c.double() * E / (k * (b - a))) * p.mean(0)).sum())
+        z.append((torch.logsumexp(l[a:b], 1) ** 2).mean())
+        counts.append(c)
+    total = 0.02 * sum(loss) / 2 + 0.001 * sum(z) / 2
+    total.backward()
+    extra = l.grad.nan_to_num(0.0)
+    got_loss, got_z, got_counts, tokens = got[5]
+    assert tokens.tolist() == [50, 68] and torch.equal(got_counts.long(), torch.stack(counts))
+    rel = 2.0 ** -17
+    check(got_loss, torch.stack(loss).detach(), torch.stack(loss).detach() * rel, "loss")
+    check(got_z, torch.stack(z).detach(), torch.stack(z).detach() * rel, "z")
+    want = base[2].double() + extra
+    check(got[2], want, want.abs() * 2.0 ** -22 + extra.abs() * rel + 1e-9, "dlogits")
+
+
+def run_all(bm, x, a, w, given, ids, bounds, order, codes, scales, dy, ws):
+    """Every operator once, in the order a step has them; ws: workspaces to share."""
+    q, s = bm.fp8_rows(x)
+    h, hs = bm.fp8_rows(a, act="silu_mul", bounds=bounds)
+    qw = bm.fp8_weights(w, transposed=True)
+    y = bm.fp8_matmul(x, codes, scales, bounds=bounds, rows=order, div=2, act="silu_mul", ws=ws)
+    z = bm.fp8_matmul(q, qw[0], qw[1], torch.empty(order.shape[0], w.shape[1], device="cuda"), x_scales=s, bounds=bounds, rows=order, div=2)
+    dx = bm.fp8_matmul(dy, qw[2], qw[3], bounds=bounds, ws=ws)
+    n = int(given)
+    return [q.view(torch.uint8), s, h[:n].view(torch.uint8), hs[:n], *(t.view(torch.uint8) if t.dtype == F8 else t for t in qw), y[:n], z[:n], dx[:n]]
+
+
+def step_inputs(bm, seed, T=160):
+    g = rng(seed)
+    E, k, D, F = 8, 2, 300, 160
+    logits = normal(g, T, E)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bounds, order, slot = torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty(T, k, **i32)
+    ids, _ = bm.moe_route(logits, k, bounds=bounds, order=order, slot=slot)
+    x, a, w = normal(g, T, D, dtype=BF16), normal(g, T * k, 2 * F, dtype=BF16), normal(g, E, 200, D, dtype=BF16)
+    codes, scales = make_weights(bm, g, E, F, D, 2)
+    dy = normal(g, T * k, 200, dtype=BF16)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    return x, a, w, T * k, ids, bounds, order, codes, scales, dy, ws
+
+
+@pytest.mark.parametrize("T", [3, 160, 900])
+def test_repeats_streams_and_graphs(bm, T):
+    """The same bits eagerly, again, on another stream, and from two captured
+    graphs that share a workspace, replayed in turn with eager work between."""
+    args = step_inputs(bm, 3, T)
+    want = run_all(bm, *args)
+    for a, b in zip(run_all(bm, *args), want):
+        assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run_all(bm, *args)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    other = step_inputs(bm, 4, T)[:-1] + args[-1:]
+    want2 = run_all(bm, *other)
+    torch.cuda.synchronize()
+    graphs = []
+    for inputs in (args, other):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run_all(bm, *inputs)
+        graphs.append((g, out))
+    for _ in range(3):
+        for (g, out), w in zip(graphs, (want, want2)):
+            for t in out:
+                t.fill_(3)
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(out, w):
+                assert torch.equal(a, b)
+        for a, b in zip(run_all(bm, *args), want):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once(bm):
+    ins = [step_inputs(bm, 5, 700), step_inputs(bm, 6, 700)]
+    want = [run_all(bm, *i) for i in ins]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for j, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[j].append(run_all(bm, *ins[j]))
+    torch.cuda.synchronize()
+    for j in range(2):
+        for run in got[j]:
+            for a, b in zip(run, want[j]):
+                assert torch.equal(a, b)
+
+
+def test_an_explicit_stream(bm):
+    g = rng(12)
+    x = normal(g, 40, 300, dtype=BF16)
+    codes, scales = make_weights(bm, g, 1, 64, 300)
+    want = bm.fp8_matmul(x, codes, scales), bm.fp8_rows(x)[1], bm.fp8_weights(x.unsqueeze(0), transposed=True)[3]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (st, st.cuda_stream):
+        got = bm.fp8_matmul(x, codes, scales, stream=s), bm.fp8_rows(x, stream=s)[1], bm.fp8_weights(x.unsqueeze(0), transposed=True, stream=s)[3]
+        st.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 6, 200])
+def test_batches_of_padding(bm, T):
+    """No token has an expert: nothing is read or written."""
+    g = rng(T)
+    ids = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    bounds, order, slot = bm.moe_group(ids, 4)
+    codes, scales = make_weights(bm, g, 4, 40, 200)
+    x = torch.full((T, 200), NAN, dtype=BF16, device="cuda")
+    for y in (torch.full((2 * T, 40), 7.0, dtype=BF16, device="cuda"), torch.full((2 * T, 40), 7.0, device="cuda")):
+        bm.fp8_matmul(x, codes, scales, y, bounds=bounds, rows=order, div=2)
+        assert bool((y == 7.0).all())
+    q, s = torch.full((2 * T, 256), 3.0, device="cuda").to(F8), torch.full((2 * T, 2), 7.0, device="cuda")
+    bm.fp8_rows(torch.full((2 * T, 200), NAN, device="cuda"), q, s, bounds=bounds)
+    assert bool((s == 7.0).all()) and bool((q.float() == 3.0).all())
+
+
+# ---------------------------------------------------------- past 32 bits
+
+def test_rows_past_32_bits(bm):
+    """4.6 GB of codes: the last rows as by themselves, and gathered from there."""
+    R, K = 70000, 65536
+    x = torch.zeros(R, K, dtype=BF16, device="cuda")
+    g = rng(1)
+    tail = normal(g, 40, K, dtype=BF16)
+    x[-40:] = tail
+    q, s = bm.fp8_rows(x)
+    tq, ts = bm.fp8_rows(tail)
+    assert torch.equal(q[-40:].view(torch.uint8), tq.view(torch.uint8)) and torch.equal(s[-40:], ts)
+    assert not bool(q[:100].view(torch.uint8).any())
+    codes, scales = make_weights(bm, g, 1, 64, K)
+    b = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    rows = torch.arange(R - 40, R, dtype=torch.int32, device="cuda")
+    want = bm.fp8_matmul(tq, codes, scales, x_scales=ts, bounds=b)
+    assert torch.equal(bm.fp8_matmul(q, codes, scales, x_scales=s, bounds=b, rows=rows), want)
+    assert torch.equal(bm.fp8_matmul(x, codes, scales, bounds=b, rows=rows), want)
+    many = rows.repeat(20)  # the tiled kernel
+    b = torch.tensor([0, 800], dtype=torch.int32, device="cuda")
+    wide, ws = make_weights(bm, g, 1, 512, K)
+    want = bm.fp8_matmul(tq, wide, ws, x_scales=ts, bounds=b, rows=many - (R - 40))
+    assert torch.equal(bm.fp8_matmul(q, wide, ws, x_scales=s, bounds=b, rows=many), want)
+
+
+@pytest.mark.parametrize("per", [2, 300])
+def test_weights_and_outputs_past_32_bits(bm, per):
+    E, N, K = 40, 8192, 16384
+    g = rng(2)
+    w = torch.zeros(E, N, K, dtype=BF16, device="cuda")
+    w[-1] = normal(g, N, K, dtype=BF16)
+    codes, scales, ct, st = bm.fp8_weights(w, transposed=True)
+    one = bm.fp8_weights(w[-1:].clone(), transposed=True)
+    del w
+    for a, b in zip((codes, scales, ct, st), one):
+        assert torch.equal(a[-1:].view(torch.uint8), b.view(torch.uint8))
+    x = normal(g, E * per, K, dtype=BF16)
+    b = torch.arange(E + 1, dtype=torch.int32, device="cuda") * per
+    y = bm.fp8_matmul(x, codes, scales, bounds=b)
+    assert torch.equal(y[-per:], bm.fp8_matmul(x[-per:], one[0], one[1])) and not bool(y[:per].any())
+    # rows of 2^26 elements apart
+    wide = torch.empty(70, 1 << 26, dtype=BF16, device="cuda")
+    out = wide[:, :N] if per == 2 else wide[:, 5:5 + N]
+    out = bm.fp8_matmul(x[-70:].contiguous(), one[0], one[1], out)
+    assert torch.equal(out, bm.fp8_matmul(x[-70:].contiguous(), one[0], one[1]))
