@@ -183,8 +183,8 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
       for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
         const int row = i / kTurn, g = i % kTurn;
         if (i >= 16) xr = load_row(i, v);
-        uint32_t a = row_max(amax_bits<false>(v));
-        if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
+        float a = row_max(amax8<false>(v));
+        if (__any(!(a < INFINITY))) a = row_max(amax8<true>(v));
         const Factors f = factors8(a);
         if (i < groups) {
           uint2 o;
@@ -424,16 +424,22 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
   // group and meets the others; then nobody reads this group's buffer any more.
   //
   // With two buffers the copies of a later group would have one group's time,
-  // and come all at once: so the waves meet twice more, and what is read by
-  // then (the weights, which lie in registers; the first half of the rows) is
-  // copied over early.
+  // and come all at once: so the waves meet once more, halfway, and what is read
+  // by then (the weights, which lie in registers; the first half of the rows) is
+  // copied over early (8 experts of about 1024 rows, 4096 x 14336: 529 -> 470
+  // us; meeting twice for it 490).
   constexpr bool kEarly = kBufs == 2;
   static_assert(!kEarly || (MI == 8 && kCa == 4 && kCb == 4), "early copies");
   auto stage = [&](int g, int c) {  // in turn g of group c, into its own buffer
     if constexpr (kEarly) {
-      if (g >= 1 && g <= 4) stage_piece(kCa + g - 1, c + kBufs, cur);
-      if (g == 5) stage_piece(0, c + kBufs, cur);
-      if (g == 6) stage_piece(2, c + kBufs, cur);
+      if (g == 4 || g == 5) {
+        stage_piece(kCa + 2 * (g - 4), c + kBufs, cur);
+        stage_piece(kCa + 2 * (g - 4) + 1, c + kBufs, cur);
+      }
+      if (g == 6) {
+        stage_piece(0, c + kBufs, cur);
+        stage_piece(2, c + kBufs, cur);
+      }
       if (g == 7) {
         stage_piece(1, c + kBufs, cur);
         stage_piece(3, c + kBufs, cur);
@@ -448,7 +454,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
     if (g == MI - 1) {
       wait_copies<kEarly ? 6 : (kBufs - 2) * kPieces>();
       lds_barrier();
-    } else if (kEarly && (g == 1 || g == 5)) {
+    } else if (kEarly && (g == 4)) {
       lds_barrier();
     }
   };
