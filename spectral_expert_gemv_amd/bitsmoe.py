@@ -462,7 +462,8 @@ def _same_device(first, *rest):
 
 def _enqueue(fn, index, stream, *args):
     """Calls fn(*args, stream) with the tensors' device as the current one."""
-    if index != torch.cuda.current_device():
+    # (the tensors are on a GPU, so the runtime is up: without torch.cuda's own look)
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _enqueue(fn, index, stream, *args)
     if stream is None:
@@ -856,8 +857,10 @@ def fp8_weights(w, codes=None, scales=None, codes_t=None, scales_t=None, transpo
 def fp8_matmul_workspace_size(x_dtype, x_rows, R, E, N, K, act=None):
     """Bytes that fp8_matmul needs for these sizes (x_dtype: x's)."""
     out = ctypes.c_size_t(0)
-    _check(_lib.bitsmoe_fp8_matmul_workspace_size(3 if x_dtype is _F8 else _DTYPES[x_dtype], x_rows, R,
-                                                  E, N, K, ACT[act], ctypes.byref(out)))
+    code = 3 if x_dtype is _F8 else _DTYPES.get(x_dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % x_dtype)
+    _check(_lib.bitsmoe_fp8_matmul_workspace_size(code, x_rows, R, E, N, K, ACT[act], ctypes.byref(out)))
     return out.value
 
 
@@ -880,10 +883,11 @@ def fp8_matmul(x, codes, scales, y=None, x_scales=None, bounds=None, rows=None, 
     if act not in ACT or (act and n2 % 2):
         raise ValueError("act=%r with %d rows of codes" % (act, n2))
     x_rows, K = x.shape
-    given = x.dtype is _F8
+    kind = x.dtype
+    given = kind is _F8
     if given != (x_scales is not None):
         raise ValueError("rows of codes and x_scales go together")
-    if kp % GROUP or _groups(K) * GROUP != kp:
+    if kp % GROUP or not 0 <= kp - K < GROUP:
         raise ValueError("x has %d inputs, the weights %d" % (K, kp))
     R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x_rows
     dev = _same_device(x, codes, scales, y, x_scales, bounds, rows, ws)
@@ -898,12 +902,15 @@ def fp8_matmul(x, codes, scales, y=None, x_scales=None, bounds=None, rows=None, 
     pw = _array("scales", scales, _F32, (E, -(-N // GROUP) * (2 if act else 1), kp // GROUP))
     pb = None if bounds is None else _bounds(bounds, E)
     if y is None:
-        y = _new((R, N), torch.bfloat16 if given else x.dtype, dev, stream)
+        y = _new((R, N), torch.bfloat16 if given else kind, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
     if ws is None and not given:
-        ws = _scratch(fp8_matmul_workspace_size(x.dtype, x_rows, R, E, N, K, act), dev, stream)
+        need = fp8_matmul_workspace_size(kind, x_rows, R, E, N, K, act)
+        if need:
+            ws = _scratch(need, dev, stream)
     _enqueue(_lib.bitsmoe_fp8_matmul, dev, stream, 3 if given else _dtype(x), px, ldx, ps, lds, x_rows,
-             pr, div, pc, pw, pb, R, E, N, K, ACT[act], py, _dtype(y), ldy, _ptr(ws), _ws_bytes(ws))
+             pr, div, pc, pw, pb, R, E, N, K, ACT[act], py, _dtype(y), ldy,
+             None if ws is None else ws.data_ptr(), _ws_bytes(ws))
     return y
 
 
@@ -940,7 +947,9 @@ def moe_balance(logits, ids, seqs=None, loss=None, z=None, counts=None, tokens=N
     counts = _new((S, E), _I32, dev, stream) if counts is None else counts
     tokens = _new(S, _I32, dev, stream) if tokens is None else tokens
     if ws is None:
-        ws = _scratch(moe_balance_workspace_size(T, E, S), dev, stream)
+        need = moe_balance_workspace_size(T, E, S)
+        if need:
+            ws = _scratch(need, dev, stream)
     _enqueue(_lib.bitsmoe_moe_balance, dev, stream, _dtype(logits), pl, ld,
              _array("ids", ids, _I32, (T, k)), pq, S, T, E, k, _array("loss", loss, _F32, (S,)),
              _array("z", z, _F32, (S,)), _array("counts", counts, _I32, (S, E)),
