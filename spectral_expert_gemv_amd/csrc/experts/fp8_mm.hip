@@ -675,12 +675,15 @@ bool few8(int R, int E, int N) {
   return R <= mean * E && max_tiles(R, E, kFewRows) <= 65535;
 }
 
-// Rows are quantized by the work-groups that use them, without a launch of
-// their own, where hardly an expert has more than one: each work-group of an
-// expert does it again (one row of 128 experts 76 us, from codes 70; 8 rows of
-// one 4096 x 4096 projection 19 us, from codes 9 and 3 to make them).
-// (k_mm8_few reads the indexes of up to 64 rows at once for it.)
-bool on_the_way(int R, int E) { return R <= 2 || (R <= 32 && R <= E); }
+// Few rows are quantized by the work-groups that use them, without a launch of
+// their own: each work-group of an expert does it again, which takes it 1.2 us
+// per 4096 elements (one row of 8 experts of 1536 x 2048 9.0 us, by two launches
+// 13.7, of 32 experts 21 and 24; 4 rows of one 4096 x 4096 projection 12.0 and
+// 13.6, 6 rows 14.4 and 13.5).  k_mm8_few reads the indexes of all R <= 64 rows
+// at once for it; 32 at most, since one expert may have them all.
+bool on_the_way(int R, int E, int K) {
+  return R <= 32 && (long long)((R + E - 1) / E) * K <= 16384;
+}
 
 // The workspace of rows that are quantized before the products: codes, then
 // scales.
@@ -688,7 +691,7 @@ struct RowsWs {
   size_t codes, scales;
 };
 RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K) {
-  if (x_dtype == kE4M3 || (few8(R, E, N) && on_the_way(R, E))) return RowsWs{0, 0};
+  if (x_dtype == kE4M3 || (few8(R, E, N) && on_the_way(R, E, K))) return RowsWs{0, 0};
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   return RowsWs{al((size_t)rows * groups_of(K) * kGroup), al((size_t)rows * groups_of(K) * 4)};
 }
