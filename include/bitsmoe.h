@@ -478,8 +478,9 @@ int bitsmoe_fp8_weights(int dtype, const void* w, int E, int N, int K, void* cod
  * or SiLU(gate) * up of it: with BITSMOE_ACT_SILU_MUL codes are E x 2N x K',
  * gate rows first, and scales E x 2 ceil(N / 128) x K' / 128: the halves are
  * quantized each by itself (as 2E matrices of N rows).
- * x: rows of K, F16 or BF16, quantized on the way as by bitsmoe_fp8_rows (y
- * has their type or is F32), or BITSMOE_E4M3 rows of K' codes with x_scales
+ * x: rows of K, F16 or BF16, quantized on the way as by bitsmoe_fp8_rows (each
+ * row of x, or each sorted row where those are fewer; y has their type or is
+ * F32), or BITSMOE_E4M3 rows of K' codes with x_scales
  * (stride ldxs; y of any type).  y, rows, div, bounds as for
  * bitsmoe_grouped_matmul; bounds NULL (E = 1): one dense projection of all R
  * rows.  dx of a product: the call with dy's rows and the transposed weights.
@@ -510,7 +511,8 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
  * (either may be NULL: 0) with respect to the logits, f held fixed, from the
  * forward call's counts and tokens:
  *   dl_te = p_te (dloss / n (f_e - sum_m p_tm f_m) + 2 dz / n lse_t),
- * 0 for tokens that take no part; `add`: added to what dlogits holds.  Rows of
+ * 0 for tokens that take no part; `add`: added to what dlogits (another buffer
+ * than logits) holds.  Rows of
  * tokens in no sequence are neither read nor written.  E <= 2048, k <= 64,
  * T <= 2^24, S <= 65535.  ws: bitsmoe_moe_balance_workspace_size() bytes, 4-byte
  * aligned; its contents carry nothing between calls.  The sums do not depend on

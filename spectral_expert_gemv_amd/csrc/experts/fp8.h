@@ -88,10 +88,17 @@ __device__ __forceinline__ void load8_any(const T* p, int left, float (&v)[8]) {
   }
 }
 
+// Rows gathered on their way: row r is row rows[r] / div of x, which has x_rows
+// rows; an index outside them gives NaN scales.
+struct Gather {
+  const int32_t* rows;
+  int div, x_rows;
+};
+
 // Quantizes rows on `st` (what bitsmoe_fp8_rows launches); sizes are checked.
-int run_fp8_rows(int dtype, const void* x, int64_t ldx, int act, const int32_t* bounds, int R,
-                 int E, int K, void* codes, int64_t ldc, float* scales, int64_t lds,
-                 hipStream_t st);
+int run_fp8_rows(int dtype, const void* x, int64_t ldx, Gather from, int act,
+                 const int32_t* bounds, int R, int E, int K, void* codes, int64_t ldc,
+                 float* scales, int64_t lds, hipStream_t st);
 
 }  // namespace experts
 }  // namespace bitsmoe

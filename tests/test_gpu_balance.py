@@ -142,6 +142,30 @@ def test_sequences(bm, T, E, k, cuts, dtype):
     assert bool((left[: cuts[0]] == 7.0).all()) and bool((left[cuts[-1]:] == 7.0).all()) and bool(left.isfinite().all())
 
 
+@pytest.mark.parametrize("T, E, k, cuts", [(50, 20, 3, [5, 20]), (50, 20, 3, [7, 7]), (250, 256, 8, [0, 250]), (257, 100, 40, [0, 257]), (30, 100, 40, [0, 30]),
+                                           (400, 300, 5, [3, 390])])
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_one_sequence_among_the_tokens(bm, T, E, k, cuts, dtype):
+    """In one launch and in two, with more slots than lanes, and ids that repeat or lie outside."""
+    _say("balance of one sequence", T, E, k, cuts, dtype)
+    g = rng(T + k)
+    l, _ = make(g, T, E, k if k < E else 1, dtype)
+    ids = torch.randint(-2, E + 2, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    ids[T // 3] = -1
+    ids[T // 2] = E
+    compare(bm, l, ids, cuts, E, g)
+
+
+def test_a_workspace_at_any_word(bm):
+    g = rng(77)
+    l, ids = make(g, 700, 64, 4, F32)
+    want = bm.moe_balance(l, ids)
+    ws = torch.empty(bm.moe_balance_workspace_size(700, 64) + 4, dtype=torch.uint8, device="cuda")
+    got = bm.moe_balance(l, ids, ws=ws[4:])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_gradient_by_differences(bm):
     """Against central differences of a 64-bit loss with the counts held."""
     g = rng(9)

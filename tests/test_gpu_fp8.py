@@ -183,6 +183,34 @@ def test_rows_of_the_activation(bm, R, F, dtype, layout):
     assert bool((c2[n:].float() == 3.0).all()) and bool((s2[n:] == 3.0).all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_rows_of_the_activation_of_infinities_and_nan(bm, dtype):
+    """What is not finite after the activation gets the code of NaN; the others'
+    codes and every scale are as without it."""
+    F = 300
+    a = normal(rng(5), 8, 2 * F, dtype=dtype, scale=2.0)
+    base = bm.fp8_rows(a, act="silu_mul")
+    b = a.clone()
+    bad = {0: [(3, INF, None), (140, NAN, None)], 2: [(5, None, -INF)], 3: [(299, None, NAN)], 5: [(7, -INF, None)], 6: [(0, INF, 0.0)]}
+    where = torch.zeros(8, 384, dtype=torch.bool, device="cuda")
+    for r, cells in bad.items():
+        for c, g, u in cells:
+            if g is not None:
+                b[r, c] = g
+            if u is not None:
+                b[r, F + c] = u
+            where[r, c] = True
+    zeroed = a.clone()
+    for r, cells in bad.items():
+        for c, _, _ in cells:
+            zeroed[r, F + c] = 0.0  # out of the largest magnitude
+    codes, scales = bm.fp8_rows(b, act="silu_mul")
+    want, ws = bm.fp8_rows(zeroed, act="silu_mul")
+    assert bool(codes.float()[where].isnan().all()) and torch.equal(scales, ws)
+    assert torch.equal(codes.float()[~where], want.float()[~where])
+    assert torch.equal(base[0].float()[1], codes.float()[1])
+
+
 # --------------------------------------------------------------- weights
 
 @pytest.mark.parametrize("E, N, K", [(1, 1, 1), (1, 128, 128), (3, 129, 127), (2, 48, 300), (5, 768, 256), (1, 1000, 1000), (2, 33, 2048), (4, 300, 40)])
@@ -336,6 +364,28 @@ def test_gathered_strided_rows_and_bad_indexes(bm, E, counts, N, K, given):
     good[n:] = False
     check(y[good], want[good], (half_step(want, F32) + off + 1e-30)[good], "y")
     assert bool((out[n:] == 7.0).all()) and bool((out[:, 0] == 7.0).all()) and bool((out[:, 1 + N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("E, per, N, K, X", [(2, 5, 64, 4500, 3000), (3, 120, 300, 400, 5000), (2, 300, 700, 256, 900)])
+def test_a_few_rows_of_many(bm, E, per, N, K, X):
+    """Fewer sorted rows than x has: the rows that are not named are not read."""
+    _say("fp8 few of many", E, per, N, K, X)
+    g = rng(X)
+    bounds, R = ragged([per] * E, tail=2)
+    n = R - 2
+    codes, scales = make_weights(bm, g, E, N, K)
+    x = normal(g, X, K, dtype=BF16)
+    rows = torch.randperm(X, generator=g, device="cuda")[:R].int()
+    q, s = bm.fp8_rows(x)
+    want = bm.fp8_matmul(q, codes, scales, torch.full((R, N), 7.0, dtype=BF16, device="cuda"), x_scales=s, bounds=bounds, rows=rows)
+    left = torch.ones(X, dtype=torch.bool, device="cuda")
+    left[rows[:n].long()] = False
+    x[left] = NAN
+    rows[n - 1] = X
+    y = bm.fp8_matmul(x, codes, scales, torch.full((R, N), 7.0, dtype=BF16, device="cuda"), bounds=bounds, rows=rows)
+    assert bool(y[n - 1].isnan().all())
+    keep = torch.arange(R, device="cuda") != n - 1
+    assert torch.equal(y[keep], want[keep])
 
 
 @pytest.mark.parametrize("R, N, K", [(1, 4096, 2048), (1, 33, 100), (7, 512, 512), (70, 300, 384), (600, 520, 700)])
