@@ -21,9 +21,11 @@ inline int64_t groups_of(int64_t n) { return (n + kGroup - 1) / kGroup; }
 struct Factors {
   float s, r;
 };
-// a: a finite magnitude.  a / 448 from the rounded reciprocal and one correction
-// by the remainder, which is exact: the rounded quotient for every mantissa.
-__device__ __forceinline__ Factors factors8(float a) {
+// a_bits: of a finite magnitude a.  a / 448 from the rounded reciprocal and one
+// correction by the remainder, which is exact: the rounded quotient for every
+// mantissa.
+__device__ __forceinline__ Factors factors8(uint32_t a_bits) {
+  const float a = __uint_as_float(a_bits);
   Factors f{1.0f, 1.0f};
   if (a >= 0x1p-80f) {
     constexpr float kInv = 1.0f / 448.0f;
@@ -34,15 +36,17 @@ __device__ __forceinline__ Factors factors8(float a) {
   return f;
 }
 
-// The largest magnitude, infinities among them (a maximum passes NaN over), or
-// `finite`: of the finite ones.
+constexpr uint32_t kInfBits = 0x7F800000u;
+// The largest magnitude's bits (ordered as the magnitudes, infinities and NaN
+// above all finite ones), or `finite`: of the finite ones.
 template <bool finite, int N>
-__device__ __forceinline__ float amax8(const float (&v)[N]) {
-  float m = 0.f;
+__device__ __forceinline__ uint32_t amax_bits(const float (&v)[N]) {
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float a = fabsf(v[i]);
-    m = fmaxf(m, finite && !(a < INFINITY) ? 0.f : a);
+    uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    if (finite) u = u < kInfBits ? u : 0u;
+    m = m > u ? m : u;
   }
   return m;
 }
@@ -55,10 +59,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 
 // maximum over the 16 lanes of a DPP row, in every lane
 template <int kCtrl>
-__device__ __forceinline__ float dpp_max(float v) {
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, false)));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false);
+  return v > o ? v : o;
 }
-__device__ __forceinline__ float row_max(float v) {
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = dpp_max<0xB1>(v);   // quad_perm [1,0,3,2]
   v = dpp_max<0x4E>(v);   // quad_perm [2,3,0,1]
   v = dpp_max<0x141>(v);  // row_half_mirror

@@ -48,8 +48,8 @@ __global__ __launch_bounds__(kThreads) void k_fp8_rows(const T* __restrict__ x, 
         for (int i = 0; i < 8; ++i) v[i] = gated(v[i], u[i]);
       }
     }
-    float a = row_max(amax8<false>(v));
-    if (__any(!(a < INFINITY))) a = row_max(amax8<true>(v));
+    uint32_t a = row_max(amax_bits<false>(v));
+    if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
     const Factors f = factors8(a);
     if (live) {
       uint2 q;
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void k_fp8_weights(const T* __restrict__ 
                                                           uint8_t* __restrict__ codes_t,
                                                           float* __restrict__ scales_t) {
   __shared__ uint32_t tile[kGroup * kPitch];
-  __shared__ float part[2][kThreads / 64];
+  __shared__ uint32_t part[2][kThreads / 64];
   const int tid = threadIdx.x, l = tid & 15;
   const int64_t b = blockIdx.x;
   const int ki = (int)(b % kb);
@@ -90,29 +90,38 @@ __global__ __launch_bounds__(kThreads) void k_fp8_weights(const T* __restrict__ 
   const int64_t kp = (int64_t)kb * kGroup, np = (int64_t)nb * kGroup;
   const int k0 = ki * kGroup + 8 * l, n0 = ni * kGroup + (tid >> 4);
   float v[8][8];
-  float a = 0.f;
+  uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = n0 + 16 * i;
     load8_any(w + (e * N + (n < N ? n : 0)) * K + k0, n < N ? K - k0 : 0, v[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, amax8<false>(v[i]));
-  auto block_max = [&](float m, int turn) {
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = amax_bits<false>(v[i]);
+    a = a > m ? a : m;
+  }
+  auto block_max = [&](uint32_t m, int turn) {
     m = row_max(m);
 #pragma unroll
-    for (int d = 16; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    for (int d = 16; d < 64; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
+      m = m > o ? m : o;
+    }
     if ((tid & 63) == 0) part[turn][tid >> 6] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) m = fmaxf(m, part[turn][i]);
+    for (int i = 0; i < kThreads / 64; ++i) m = m > part[turn][i] ? m : part[turn][i];
     return m;
   };
   a = block_max(a, 0);
-  if (!(a < INFINITY)) {  // (the same in all threads)
-    a = 0.f;
+  if (a >= kInfBits) {  // (the same in all threads)
+    a = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, amax8<true>(v[i]));
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t m = amax_bits<true>(v[i]);
+      a = a > m ? a : m;
+    }
     a = block_max(a, 1);
   }
   const Factors f = factors8(a);

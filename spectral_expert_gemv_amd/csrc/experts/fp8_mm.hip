@@ -188,8 +188,8 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
       for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
         const int row = i / kTurn, g = i % kTurn;
         if (i >= 16) xr = load_row(i, v);
-        float a = row_max(amax8<false>(v));
-        if (__any(!(a < INFINITY))) a = row_max(amax8<true>(v));
+        uint32_t a = row_max(amax_bits<false>(v));
+        if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
         const Factors f = factors8(a);
         if (i < groups) {
           uint2 o;
