@@ -195,8 +195,8 @@ struct Outs {
   int32_t *counts, *tokens;
 };
 
-// Sums of one chunk into its record; ONE: of the only chunk there is, whose
-// losses it writes.  Bound by latencies and the exp (16384 tokens of 128
+// Sums of one chunk into its record; ONE: of a whole sequence, whose losses it
+// writes.  Bound by latencies and the exp (16384 tokens of 128
 // experts, 8.4 MB: 6 us; 67 tokens of 8 experts with the losses 4.1).
 template <class T, int L, int V, int NT, bool ONE>
 __global__ __launch_bounds__(NT) void k_balance_part(
@@ -210,8 +210,15 @@ __global__ __launch_bounds__(NT) void k_balance_part(
   float* zs = sums + (size_t)W * E;
   int32_t* ns = (int32_t*)(zs + W);
   int32_t* count = ns + W;         // [E]
-  const Tile c = chunk_of(seqs, S, T_, blockIdx.x, per);
-  if (!ONE && c.n <= 0) return;
+  Tile c{(int)blockIdx.x, 0, T_};
+  if (!ONE) {
+    c = chunk_of(seqs, S, T_, blockIdx.x, per);
+    if (c.n <= 0) return;
+  } else if (seqs) {
+    int hi;
+    expert_rows(seqs, c.e, T_, c.row0, hi);
+    c.n = hi - c.row0;
+  }
   const int tid = threadIdx.x, l = tid & (L - 1), wv = tid >> 6;
   for (int e = tid; e < E; e += NT) count[e] = 0;
   __syncthreads();
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(NT) void k_balance_part(
 #pragma unroll
     for (int w = 0; w < W; ++w) p += sums[w * E + e];
     if (ONE) {
-      o.counts[e] = count[e];
+      o.counts[(size_t)c.e * E + e] = count[e];
       part += (double)count[e] * (double)p;
     } else {
       out[e] = __float_as_uint(p);
@@ -265,9 +272,9 @@ __global__ __launch_bounds__(NT) void k_balance_part(
     part = block_sum<W>(part, buf);
     const double inv = n > 0 ? 1.0 / n : 0.0;
     if (tid == 0) {
-      o.loss[0] = (float)(part * inv * inv * ((double)E / k));
-      o.z[0] = (float)((double)z * inv);
-      o.tokens[0] = n;
+      o.loss[c.e] = (float)(part * inv * inv * ((double)E / k));
+      o.z[c.e] = (float)((double)z * inv);
+      o.tokens[c.e] = n;
     }
   } else if (tid == 0) {
     out[2 * E] = __float_as_uint(z);
@@ -438,14 +445,19 @@ void with_type(int dtype, F f) {
 }
 
 // Tokens of a chunk: two turns of 32 tokens at a time, more where that would
-// make over 512 chunks of a sequence; one chunk (of 1024 lanes) of few tokens
-// in one sequence.
-constexpr int kOneTokens = 256;
+// make over 512 chunks of a sequence.
 int chunk_tokens(int T) {
   const int per = (T + 511) / 512;
   return per < 64 ? 64 : (per + 31) / 32 * 32;
 }
-bool one_chunk(int T, int E, int S) { return S == 1 && T >= 1 && T <= kOneTokens && E <= 256; }
+// A work-group of 1024 lanes per sequence, one launch: for few tokens, and a few
+// more of sequences that are short on average.  (us by it and by two launches,
+// which also take the host 4 us longer: 67 tokens 4.2 and 8, 256 of 128 experts
+// 8.9 and 8, 512 14 and 8, whatever sequence has them.)
+constexpr int kOneTokens = 256, kOneMost = 1024, kOneMean = 128;
+bool one_chunk(int T, int E, int S) {
+  return T >= 1 && E <= 256 && (T <= kOneTokens || (T <= kOneMost && T <= (long long)kOneMean * S));
+}
 constexpr int kGradTokens = 32;  // of a work-group of the gradient: two turns
 int max_chunks(int T, int S) {
   const int per = chunk_tokens(T);
@@ -507,9 +519,9 @@ int bitsmoe_moe_balance(int dtype, const void* logits, int64_t ld, const int32_t
           constexpr int NT = decltype(threads)::value, W = NT / 64;
           constexpr bool ONE = decltype(one_)::value;
           const size_t lds = W * 8 + ((size_t)W * E + 2 * W + E) * 4;
-          hipLaunchKernelGGL((k_balance_part<X, L, V, NT, ONE>), dim3(ONE ? 1u : (unsigned)chunks),
+          hipLaunchKernelGGL((k_balance_part<X, L, V, NT, ONE>), dim3((unsigned)(ONE ? S : chunks)),
                              dim3(NT), lds, q, (const X*)logits, ld, ids, seqs, S, T, E, k,
-                             ONE ? T : per, (uint32_t*)ws, o);
+                             per, (uint32_t*)ws, o);
         };
         using std::integral_constant;
         if constexpr (L == 16) {

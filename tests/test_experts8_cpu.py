@@ -76,7 +76,7 @@ def balance_grad(**kw):
     (balance, dict(k=65), bm.EINVAL), (balance, dict(T=-1), bm.ESHAPE), (balance, dict(T=(1 << 24) + 1), bm.ESHAPE), (balance, dict(S=0), bm.ESHAPE),
     (balance, dict(S=65536, seqs=P), bm.ESHAPE), (balance, dict(S=2), bm.EINVAL), (balance, dict(ld=63), bm.ESHAPE), (balance, dict(logits=None), bm.EINVAL),
     (balance, dict(ids=None), bm.EINVAL), (balance, dict(loss=None), bm.EINVAL), (balance, dict(z=None), bm.EINVAL), (balance, dict(counts=None), bm.EINVAL),
-    (balance, dict(tokens=None), bm.EINVAL), (balance, dict(T=1000, ws=None), bm.ENOSPC), (balance, dict(T=1000, ws_bytes=10), bm.ENOSPC), (balance, dict(T=1000, ws=P + 2), bm.EINVAL),
+    (balance, dict(tokens=None), bm.EINVAL), (balance, dict(T=2000, ws=None), bm.ENOSPC), (balance, dict(T=2000, ws_bytes=10), bm.ENOSPC), (balance, dict(T=2000, ws=P + 2), bm.EINVAL),
     (balance_grad, dict(dtype=5), bm.EINVAL), (balance_grad, dict(E=2049, ld=4096, ldd=4096), bm.ESHAPE), (balance_grad, dict(k=65), bm.EINVAL),
     (balance_grad, dict(S=3), bm.EINVAL), (balance_grad, dict(ldd=63), bm.ESHAPE), (balance_grad, dict(ld=63), bm.ESHAPE),
     (balance_grad, dict(counts=None), bm.EINVAL), (balance_grad, dict(tokens=None), bm.EINVAL), (balance_grad, dict(dlogits=None), bm.EINVAL),
@@ -93,10 +93,10 @@ def test_nothing_to_do_is_fine(call, empty):
 
 
 def test_balance_workspace():
-    for T, E, S in [(300, 1, 1), (100, 64, 2), (100, 600, 1), (16384, 128, 1), (1 << 24, 2048, 65535), (50, 8, 300)]:
+    for T, E, S in [(1025, 1, 1), (4096, 64, 2), (100, 600, 1), (16384, 128, 1), (1 << 24, 2048, 65535), (50, 800, 300)]:
         n = bm.moe_balance_workspace_size(T, E, S)
         assert 0 < n and n % 4 == 0
-    assert bm.moe_balance_workspace_size(0, 8, 1) == 0 == bm.moe_balance_workspace_size(256, 256, 1)
+    assert bm.moe_balance_workspace_size(0, 8, 1) == 0 == bm.moe_balance_workspace_size(256, 256, 1) == bm.moe_balance_workspace_size(1024, 8, 8)
     with pytest.raises(bm.BitsMoEError):
         bm.moe_balance_workspace_size(10, 3000, 1)
 

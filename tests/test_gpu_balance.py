@@ -121,6 +121,7 @@ def test_one_sequence(bm, T, E, k, dtype):
 
 
 @pytest.mark.parametrize("T, E, k, cuts", [(50, 8, 2, [0, 0, 1, 50]), (700, 64, 6, [0, 64, 65, 65, 300, 700]), (500, 128, 8, [0, 100, 300, 490]),
+                                           (1500, 64, 6, [0, 64, 65, 65, 300, 1500]), (4096, 32, 4, [0, 1, 1, 4000, 4000, 4001, 4050, 4090, 4096]),
                                            (300, 300, 4, [5, 20, 20, 290]), (4096, 16, 2, list(range(0, 4097, 32))), (90, 2048, 8, [0, 30, 90])])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_sequences(bm, T, E, k, cuts, dtype):
@@ -142,7 +143,7 @@ def test_sequences(bm, T, E, k, cuts, dtype):
     assert bool((left[: cuts[0]] == 7.0).all()) and bool((left[cuts[-1]:] == 7.0).all()) and bool(left.isfinite().all())
 
 
-@pytest.mark.parametrize("T, E, k, cuts", [(50, 20, 3, [5, 20]), (50, 20, 3, [7, 7]), (250, 256, 8, [0, 250]), (257, 100, 40, [0, 257]), (30, 100, 40, [0, 30]),
+@pytest.mark.parametrize("T, E, k, cuts", [(50, 20, 3, [5, 20]), (50, 20, 3, [7, 7]), (250, 256, 8, [0, 250]), (257, 100, 40, [0, 257]), (1100, 100, 40, [0, 1100]), (1025, 7, 2, [0, 1025]), (30, 100, 40, [0, 30]),
                                            (400, 300, 5, [3, 390])])
 @pytest.mark.parametrize("dtype", [F32, F16])
 def test_one_sequence_among_the_tokens(bm, T, E, k, cuts, dtype):
@@ -158,9 +159,9 @@ def test_one_sequence_among_the_tokens(bm, T, E, k, cuts, dtype):
 
 def test_a_workspace_at_any_word(bm):
     g = rng(77)
-    l, ids = make(g, 700, 64, 4, F32)
+    l, ids = make(g, 1700, 64, 4, F32)
     want = bm.moe_balance(l, ids)
-    ws = torch.empty(bm.moe_balance_workspace_size(700, 64) + 4, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(bm.moe_balance_workspace_size(1700, 64) + 4, dtype=torch.uint8, device="cuda")
     got = bm.moe_balance(l, ids, ws=ws[4:])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
