@@ -35,10 +35,12 @@ __device__ __forceinline__ Halves halves(i32x8 q) {
   }
   return h;
 }
-// a group's sums, in float32: four fp16 instructions.  (The 8-bit instruction
-// aligns eight products at a time to their largest and drops what lies more
-// than 13 bits below its first one: 1.4e-5 to 5e-5 of the result where this is
-// 1e-7.)
+// A group's sums.  The 8-bit instruction aligns eight products at a time to their
+// largest and drops what lies more than 13 bits below its first bit: an error of
+// 1.4e-5 to 5e-5 of a result, where rounding it to fp16 adds up to 4.9e-4, to
+// bf16 3.9e-3.  So 16-bit outputs come from it, and float32 ones (EXACT) from
+// codes turned to fp16, four instructions in float32 (1e-7 of a result) at under
+// half the rate, and a slow conversion of every two codes.
 __device__ __forceinline__ f32x4 group_sums(const Halves& a, const Halves& b) {
   f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -46,11 +48,22 @@ __device__ __forceinline__ f32x4 group_sums(const Halves& a, const Halves& b) {
   return p;
 }
 
-// the same by the 8-bit instruction (scale operands of 0: none of its own)
+// (scale operands of 0: none of its own)
 __device__ __forceinline__ f32x4 group_sums(const i32x8& a, const i32x8& b) {
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
+
+template <bool EXACT>
+struct Operands {
+  typedef i32x8 type;
+  static __device__ __forceinline__ i32x8 of(const i32x8& q) { return q; }
+};
+template <>
+struct Operands<true> {
+  typedef Halves type;
+  static __device__ __forceinline__ Halves of(const i32x8& q) { return halves(q); }
+};
 
 struct E4M3 {};  // rows that are codes already
 
@@ -70,6 +83,8 @@ struct Mm8Args {
   int y16;              // rows of y are whole 16-byte pieces
 };
 
+__device__ const float g_nan = __builtin_nanf("");
+
 __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
   if (!s.rows) return i;
   const int p = s.rows[i];
@@ -78,7 +93,7 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 }
 
 // ------------------------------------------------- few rows per expert
-// A work-group takes up to 64 sorted rows of one expert and 32 rows of its
+// A work-group takes up to 32 sorted rows of one expert and 32 rows of its
 // weights (with the activation 16 of the gate and the same 16 of the up half);
 // its four waves split the groups, a whole line of each weight row each, and
 // add up their sums through LDS.  Weights go straight into registers, once;
@@ -90,12 +105,15 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // Rows that are not codes yet are quantized by the work-group, a turn's groups
 // at a time, into LDS, while its weights are on their way.
 //
-// Bound by the weights' bytes: one row of each of 128 experts of 1536 x 2048
-// (403 MB) 70 us from codes, 5.8 TB/s; 32 tokens of them, Zipf, 50 us (5.1 TB/s
-// over the experts reached); the 8 of one token (25 MB) 8.4 us, a chain of
-// latencies: bounds, row, its codes, weights, sums of the waves.
-constexpr int kFewRows = 64, kFewCols = 32, kFewWaves = 4;
-constexpr int kFewTurn = 16;  // groups of 16 rows (8 of 32, 4 of 64) in a turn
+// Bound by the weights' bytes: two rows of each of 128 experts of 1536 x 2048
+// (403 MB) 68 us from codes, 5.9 TB/s; 32 tokens of them, Zipf, 46 us (5.6 TB/s
+// over the experts reached); the 8 of one token (25 MB) 8.3 us, a chain of
+// latencies: bounds, row, its codes, weights, sums of the waves.  With more rows
+// (up to 64 a work-group) 64 rows of 4096 x 4096 19 us instead of 12; with the
+// last turn always whole, where half its groups do not exist, 64 experts of 512 x
+// 1024, 8 rows each, 14.6 instead of 9.7.
+constexpr int kFewRows = 32, kFewCols = 32, kFewWaves = 4;
+constexpr int kFewTurn = 16;  // groups of 16 rows (8 of 32) in a turn
 
 // 16 + 16 bytes of a row of codes at group start p (+ 16 q)
 __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
@@ -107,8 +125,8 @@ struct FewLds {
   // rows of a turn's codes, 16 bytes apart from a multiple of 256 so that the
   // reads of 16 rows spread over the banks; later the waves' sums
   union {
-    uint8_t codes[16 * (kFewTurn * kGroup) + 64 * 16];
-    f32x4 part[kFewWaves * 8 * 64];
+    uint8_t codes[16 * (kFewTurn * kGroup) + 32 * 16];
+    f32x4 part[kFewWaves * 4 * 64];
   };
   float scales[16 * kFewTurn];
 };
@@ -117,8 +135,10 @@ struct FewLds {
 template <class X, class O, bool ACT, int MB>
 __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int at, FewLds& lds) {
   constexpr bool kCodes = std::is_same<X, E4M3>::value;
+  typedef typename Operands<sizeof(O) == 4>::type Frag;
+  constexpr auto operand = Operands<sizeof(O) == 4>::of;
   constexpr int kTurn = kFewTurn / MB;     // groups of a turn
-  constexpr int U = kTurn / kFewWaves;     // of a wave, whose loads are in flight together
+  constexpr int kMine = kTurn / kFewWaves;   // of a wave, whose loads are in flight together
   constexpr int kRow = kTurn * kGroup + 16;  // bytes of an LDS row
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -136,26 +156,30 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
   }
   const uint8_t* x[MB];
   const float* xs[MB];
+  int xs_step[MB];  // (a row outside x: the same NaN for every group)
   if constexpr (kCodes) {
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const int xr = x_row8(s, t.row0 + min(16 * m + r, t.n - 1));
       x[m] = (const uint8_t*)s.x + (int64_t)max(xr, 0) * s.ldx + 16 * q;
-      xs[m] = xr < 0 ? nullptr : s.xs + (int64_t)xr * s.ldxs;
+      xs[m] = xr < 0 ? &g_nan : s.xs + (int64_t)xr * s.ldxs;
+      xs_step[m] = xr < 0 ? 0 : 1;
     }
   }
   f32x4 acc[MB][2] = {};
-#pragma unroll 1
-  for (int g0 = 0; g0 < s.kg; g0 += kTurn) {
+  // groups g0 .., U of each wave
+  auto turn = [&](int g0, auto mine) {
+    constexpr int U = decltype(mine)::value;
     // (groups past the last are loaded as it and not used)
     i32x8 vw[U][2], vx[U][MB];
     float sw[U][2], sx[U][MB];
     // rows on their way to codes: 16 lanes a group, as in k_fp8_rows.  The first
     // ones' loads come before the weights', so that their codes are made while
     // the weights are on their way.
-    const int groups = t.n * kTurn, l = threadIdx.x & 15;
+    constexpr int kGroups = U * kFewWaves;
+    const int groups = t.n * kGroups, l = threadIdx.x & 15;
     auto load_row = [&](int i, float (&v)[8]) {
-      const int row = i / kTurn, c = (g0 + i % kTurn) * kGroup + 8 * l;
+      const int row = i / kGroups, c = (g0 + i % kGroups) * kGroup + 8 * l;
       int xr = t.row0 + min(row, t.n - 1);
       if (s.rows) {
         const int p = __shfl(at, xr, 64);
@@ -179,14 +203,16 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
           vx[u][m] = load_codes(x[m] + (int64_t)g * kGroup);
-          sx[u][m] = xs[m] ? xs[m][g] : __builtin_nanf("");
+          sx[u][m] = xs[m][g * xs_step[m]];
         }
       }
     }
+    // (all of a turn's loads before the first use)
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (!kCodes) {
       if (g0) __syncthreads();  // (the turn before is read)
       for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
-        const int row = i / kTurn, g = i % kTurn;
+        const int row = i / kGroups, g = i % kGroups;
         if (i >= 16) xr = load_row(i, v);
         uint32_t a = row_max(amax_bits<false>(v));
         if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
@@ -205,7 +231,7 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
     for (int u = 0; u < U; ++u) {
       const int gl = u * kFewWaves + wv;
       if (g0 + gl >= s.kg) break;
-      const Halves hw[2] = {halves(vw[u][0]), halves(vw[u][1])};
+      const Frag hw[2] = {operand(vw[u][0]), operand(vw[u][1])};
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         if constexpr (!kCodes) {
@@ -213,7 +239,7 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
           vx[u][m] = load_codes(lds.codes + row * kRow + gl * kGroup + 16 * q);
           sx[u][m] = lds.scales[row * kTurn + gl];
         }
-        const Halves hx = halves(vx[u][m]);
+        const Frag hx = operand(vx[u][m]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const f32x4 p = group_sums(hw[b], hx);
@@ -223,6 +249,13 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
         }
       }
     }
+  };
+#pragma unroll 1
+  for (int g0 = 0; g0 < s.kg; g0 += kTurn) {
+    if (s.kg - g0 > kTurn / 2)
+      turn(g0, std::integral_constant<int, kMine>{});
+    else
+      turn(g0, std::integral_constant<int, kMine / 2>{});
   }
 
   // sums of the four waves: [wave][tile of 16 x 16][lane]
@@ -265,8 +298,13 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
   }
 }
 
+// (16-bit outputs of codes fit four work-groups a compute unit; the others would
+// spill, or are too few to need them)
+template <class X, class O>
+constexpr int kFewOnUnit = sizeof(O) == 2 && std::is_same<X, E4M3>::value ? 4 : 3;
+
 template <class X, class O, bool ACT>
-__global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
+__global__ __launch_bounds__(64 * kFewWaves, (kFewOnUnit<X, O>)) void k_mm8_few(Mm8Args s) {
   __shared__ FewLds lds;
   int at = 0;
   if (!std::is_same<X, E4M3>::value && s.rows) at = s.rows[min((int)threadIdx.x & 63, s.R - 1)];
@@ -280,10 +318,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
   if (t.n <= 0) return;
   if (t.n <= 16)
     few8_rows<X, O, ACT, 1>(s, t, at, lds);
-  else if (t.n <= 32)
-    few8_rows<X, O, ACT, 2>(s, t, at, lds);
   else
-    few8_rows<X, O, ACT, 4>(s, t, at, lds);
+    few8_rows<X, O, ACT, 2>(s, t, at, lds);
 }
 
 // --------------------------------------------------------------- tiled
@@ -300,11 +336,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
 // wave's order, while the matrix cores work on: four multiply-adds a lane
 // against 32 cycles of the matrix cores.
 //
-// 16-bit outputs come from the 8-bit instruction, whose sums of eight products
-// keep 14 bits of the largest (an error of 1.4e-5 to 5e-5 of a result, where
-// rounding it to fp16 adds up to 4.9e-4, to bf16 3.9e-3); float32 outputs from
-// codes turned to fp16 (EXACT), at under half the rate.
-//
 // 8192 rows x 4096 weight rows x 14336 inputs 382 us, 2520 TFLOP/s (the library's
 // 8192^3 product with one scale for each operand 2710), with 2048 inputs 69 us,
 // 2000; 24576 rows of 64 experts with the activation 198 us, 8 experts of about
@@ -314,8 +345,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 3) void k_mm8_few(Mm8Args s) {
 constexpr int kTile = 256;  // rows and weight rows of a whole tile
 constexpr uint32_t kScaleLds = 2048;                              // of one buffer
 constexpr uint32_t kLds8 = 3 * ((kTile + kTile / 2) * kGroup + kScaleLds);  // three buffers of a 256 x 128 tile
-
-__device__ const float g_nan = __builtin_nanf("");
 
 // As copy16, 4 bytes per lane.
 __device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
@@ -396,7 +425,8 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
   };
 
   static_assert(MI % 2 == 0, "turns of the registers");
-  typedef typename std::conditional<EXACT, Halves, i32x8>::type Frag;
+  typedef typename Operands<EXACT>::type Frag;
+  constexpr auto operand = Operands<EXACT>::of;
   const int wm = (wv / WN) * (TM / WM), wn = (wv % WN) * (TN / WN);
   const int l16 = lane & 15;
   const uint32_t piece = ((lane >> 4) ^ ((l16 >> 1) & 7)) << 4;
@@ -406,12 +436,6 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& s, uint32_t base, int e,
   auto raw = [&](uint32_t at, int g) {
     const i32x4 a = lds_read<i32x4>(at + g * 16 * kGroup), b = lds_read<i32x4>((at ^ 64) + g * 16 * kGroup);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  auto operand = [&](const i32x8& q) -> Frag {
-    if constexpr (EXACT)
-      return halves(q);
-    else
-      return q;
   };
   f32x4 acc[MI][NI] = {}, part[NI] = {};
   i32x8 fa[2], fb[NI];
@@ -671,28 +695,30 @@ void with_out(int o_dtype, F f) {
     f(bf16{});
 }
 
-// The few-rows kernel is the faster one up to 7 rows per expert on average, and
-// up to 2048 / tiles where there are few 256 x 256 tiles to spread over the
-// chip.  us by it and by the tiled one, from codes: 128 experts of 1536 x 2048
-// (768 tiles), 4 rows 75 and 80, 8 rows 81 and 81, 16 rows 95 and 82; 8 experts
-// of 4096 x 4096 (128 tiles), 16 rows 34 and 36, 32 rows 42 and 36; one of
-// 14336 x 4096 (56 tiles), 32 rows 22 and 22, 64 rows 33 and 25; one of 4096 x
-// 4096 (16 tiles), 64 rows 18 and 22, 128 rows 19 and 30.
-constexpr int kFewMean = 7, kFewByTiles = 2048, kFewMost = 256;
+// The few-rows kernel is the faster one up to 8 rows per expert on average, up to
+// 16 where it makes at most four work-groups a compute unit, and where it makes
+// at most one.  us by it and by the tiled one, from codes: 128 experts of 1536 x
+// 2048 (6144 work-groups), 4 rows 70 and 80, 8 rows 76 and 81, 16 rows 92 and 82;
+// 8 experts of 4096 x 4096 (1024), 16 rows 34 and 36, 32 rows 43 and 36; 32 of
+// 1536 x 2048 (1536), 16 rows 26 and 24; one of 4096 x 4096, 64 rows (256) 12.4
+// and 15.4, 128 rows (512) 20.5 and 20.4; one of 8192 x 2048, 64 rows (512) 12.3
+// and 9.8; one of 2048 x 2048, 128 rows (256) 8.0 and 12.1.
+constexpr int kFewMean = 8, kFewMean4 = 16;
 
-bool few8(int R, int E, int N) {
-  const long long tiles = (long long)((N + kTile - 1) / kTile) * E * ((R / E + kTile - 1) / kTile);
-  const long long by = tiles ? kFewByTiles / tiles : kFewMost;
-  const long long mean = by < kFewMean ? kFewMean : by < kFewMost ? by : kFewMost;
-  return R <= mean * E && max_tiles(R, E, kFewRows) <= 65535;
+bool few8(int R, int E, int N, int act) {
+  const long long mean = ((long long)R + E - 1) / E;
+  const long long wn = act ? 2ll * N : N;
+  const long long parts = (wn + kFewCols - 1) / kFewCols * ((mean + kFewRows - 1) / kFewRows) * E;
+  return max_tiles(R, E, kFewRows) <= 65535 &&
+         (mean <= kFewMean || (mean <= kFewMean4 && parts <= 4 * kUnits) || parts <= kUnits);
 }
 
 // Few rows are quantized by the work-groups that use them, without a launch of
 // their own: each work-group of an expert does it again, which takes it 1.2 us
 // per 4096 elements (one row of 8 experts of 1536 x 2048 9.0 us, by two launches
 // 13.7, of 32 experts 21 and 24; 4 rows of one 4096 x 4096 projection 12.0 and
-// 13.6, 6 rows 14.4 and 13.5).  k_mm8_few reads the indexes of all R <= 64 rows
-// at once for it; 32 at most, since one expert may have them all.
+// 13.6, 6 rows 14.4 and 13.5).  At most 32 rows, which one expert may have all:
+// k_mm8_few reads the indexes of all R rows at once, one a lane.
 bool on_the_way(int R, int E, int K) {
   return R <= 32 && (long long)((R + E - 1) / E) * K <= 16384;
 }
@@ -702,8 +728,8 @@ bool on_the_way(int R, int E, int K) {
 struct RowsWs {
   size_t codes, scales;
 };
-RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K) {
-  if (x_dtype == kE4M3 || (few8(R, E, N) && on_the_way(R, E, K))) return RowsWs{0, 0};
+RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K, int act) {
+  if (x_dtype == kE4M3 || (few8(R, E, N, act) && on_the_way(R, E, K))) return RowsWs{0, 0};
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   return RowsWs{al((size_t)rows * groups_of(K) * kGroup), al((size_t)rows * groups_of(K) * 4)};
 }
@@ -738,7 +764,7 @@ int bitsmoe_fp8_matmul_workspace_size(int x_dtype, int x_rows, int R, int E, int
   if (!bytes) return fail(BITSMOE_EINVAL, "bytes is null");
   const int st = sizes8(x_dtype, x_rows, R, E, N, K, act);
   if (st) return st;
-  const RowsWs w = rows_ws(x_dtype, x_rows < R ? x_rows : R, R, E, N, K);
+  const RowsWs w = rows_ws(x_dtype, x_rows < R ? x_rows : R, R, E, N, K, act);
   *bytes = w.codes + w.scales;
   return BITSMOE_OK;
 }
@@ -769,7 +795,7 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
   // indexes only the first R rows of x are read).
   const bool sorted = !rows || R < x_rows;
   const int live = sorted ? R : x_rows;
-  const RowsWs w = rows_ws(x_dtype, live, R, E, N, K);
+  const RowsWs w = rows_ws(x_dtype, live, R, E, N, K, act);
   const size_t need = w.codes + w.scales;
   if (need > ws_bytes || (need && !ws))
     return fail(BITSMOE_ENOSPC, "ws_bytes=%zu < %zu", ws_bytes, need);
@@ -778,7 +804,7 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
   Mm8Args s{x, ldx, x_scales, ldxs, rows, div, x_rows, (const uint8_t*)codes, scales, bounds, R, E,
             N, K, (int)kg, (int)nb, y, ldy, 0};
   s.y16 = rows16(y, ldy, y_dtype == BITSMOE_F32 ? 4 : 2);
-  const bool few = few8(R, E, N);
+  const bool few = few8(R, E, N, act);
   const int fp = act ? kFewCols / 2 : kFewCols;
   const dim3 grid((unsigned)((N + fp - 1) / fp),
                   (unsigned)(bounds ? max_tiles(R, E, kFewRows) : (R + kFewRows - 1) / kFewRows));
