@@ -697,12 +697,12 @@ void with_out(int o_dtype, F f) {
 
 // The few-rows kernel is the faster one up to 8 rows per expert on average, up to
 // 16 where it makes at most four work-groups a compute unit, and where it makes
-// at most one.  us by it and by the tiled one, from codes: 128 experts of 1536 x
-// 2048 (6144 work-groups), 4 rows 70 and 80, 8 rows 76 and 81, 16 rows 92 and 82;
-// 8 experts of 4096 x 4096 (1024), 16 rows 34 and 36, 32 rows 43 and 36; 32 of
-// 1536 x 2048 (1536), 16 rows 26 and 24; one of 4096 x 4096, 64 rows (256) 12.4
-// and 15.4, 128 rows (512) 20.5 and 20.4; one of 8192 x 2048, 64 rows (512) 12.3
-// and 9.8; one of 2048 x 2048, 128 rows (256) 8.0 and 12.1.
+// at most two.  us by it and by the tiled one, from codes, over weights that no
+// cache holds: 128 experts of 1536 x 2048 (6144 work-groups), 4 rows 70 and 80,
+// 8 rows 76 and 81, 16 rows 92 and 82; 8 experts of 4096 x 4096 (1024), 16 rows
+// 34 and 36, 32 rows 43 and 36; 32 of 1536 x 2048 (1536), 16 rows 26 and 25; one
+// of 4096 x 4096, 64 rows (256) 13 and 23, 128 rows (512) 21 and 30, 192 rows
+// (768) 30 and 27; one of 8192 x 2048, 64 rows (512) 12.7 and 12.6.
 constexpr int kFewMean = 8, kFewMean4 = 16;
 
 bool few8(int R, int E, int N, int act) {
@@ -710,7 +710,7 @@ bool few8(int R, int E, int N, int act) {
   const long long wn = act ? 2ll * N : N;
   const long long parts = (wn + kFewCols - 1) / kFewCols * ((mean + kFewRows - 1) / kFewRows) * E;
   return max_tiles(R, E, kFewRows) <= 65535 &&
-         (mean <= kFewMean || (mean <= kFewMean4 && parts <= 4 * kUnits) || parts <= kUnits);
+         (mean <= kFewMean || (mean <= kFewMean4 && parts <= 4 * kUnits) || parts <= 2 * kUnits);
 }
 
 // Few rows are quantized by the work-groups that use them, without a launch of
