@@ -96,11 +96,13 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // A work-group takes up to 32 sorted rows of one expert and 32 rows of its
 // weights (with the activation 16 of the gate and the same 16 of the up half);
 // its four waves split the groups, a whole line of each weight row each, and
-// add up their sums through LDS.  Weights go straight into registers, once;
-// they are the products' first operand, so a lane holds 4 outputs of one row of
-// x, whose scale it needs once.  Which of a group's 128 elements lie in which
-// lane does not matter as long as both operands agree: lane (r, q) holds bytes
-// 16 q .. and 64 + 16 q .. of row r, so that a load covers 64 bytes of 16 rows.
+// add up their sums through LDS (eight waves: a pair takes 16 of the weight
+// rows each, so that the sums keep their order).  Weights go straight into
+// registers, once; they are the products' first operand, so a lane holds 4
+// outputs of one row of x, whose scale it needs once.  Which of a group's 128
+// elements lie in which lane does not matter as long as both operands agree:
+// lane (r, q) holds bytes 16 q .. and 64 + 16 q .. of row r, so that a load
+// covers 64 bytes of 16 rows.
 //
 // Rows that are not codes yet are quantized by the work-group, a turn's groups
 // at a time, into LDS, while its weights are on their way.
@@ -112,8 +114,7 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // (up to 64 a work-group) 64 rows of 4096 x 4096 19 us instead of 12; with the
 // last turn always whole, where half its groups do not exist, 64 experts of 512 x
 // 1024, 8 rows each, 14.6 instead of 9.7.
-constexpr int kFewRows = 32, kFewCols = 32, kFewWaves = 4;
-constexpr int kFewTurn = 16;  // groups of 16 rows (8 of 32) in a turn
+constexpr int kFewRows = 32, kFewCols = 32;
 
 // 16 + 16 bytes of a row of codes at group start p (+ 16 q)
 __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
@@ -121,38 +122,42 @@ __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+template <int W>
 struct FewLds {
+  static constexpr int kTurn = 4 * W;  // groups of 16 rows (half as many of 32) in a turn
   // rows of a turn's codes, 16 bytes apart from a multiple of 256 so that the
   // reads of 16 rows spread over the banks; later the waves' sums
   union {
-    uint8_t codes[16 * (kFewTurn * kGroup) + 32 * 16];
-    f32x4 part[kFewWaves * 4 * 64];
+    uint8_t codes[16 * (kTurn * kGroup) + 32 * 16];
+    f32x4 part[4 * 4 * 64];
   };
-  float scales[16 * kFewTurn];
+  float scales[16 * kTurn];
 };
 
 // (at: for rows that are not codes, the index of row `lane` of all R <= 64 rows)
-template <class X, class O, bool ACT, int MB>
-__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int at, FewLds& lds) {
+template <class X, class O, bool ACT, int MB, int W>
+__device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int at, FewLds<W>& lds) {
   constexpr bool kCodes = std::is_same<X, E4M3>::value;
   typedef typename Operands<sizeof(O) == 4>::type Frag;
   constexpr auto operand = Operands<sizeof(O) == 4>::of;
-  constexpr int kTurn = kFewTurn / MB;     // groups of a turn
-  constexpr int kMine = kTurn / kFewWaves;   // of a wave, whose loads are in flight together
+  constexpr int kTurn = FewLds<W>::kTurn / MB;  // groups of a turn
+  constexpr int kMine = kTurn / 4;              // of a wave, whose loads are in flight together
+  constexpr int NB = 8 / W;                     // its 16 x 16 tiles across, from b0
   constexpr int kRow = kTurn * kGroup + 16;  // bytes of an LDS row
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int r = lane & 15, q = lane >> 4, quarter = wv & 3, b0 = wv >> 2;
   const int n0 = blockIdx.x * (ACT ? kFewCols / 2 : kFewCols);
   const int64_t kp = (int64_t)s.kg * kGroup;
-  const uint8_t* w[2];
-  const float* ws[2];
+  const uint8_t* w[NB];
+  const float* ws[NB];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int i = 0; i < NB; ++i) {
+    const int b = b0 + i;
     const int n = n0 + (ACT ? 0 : 16 * b);
     const int64_t row = (int64_t)(ACT ? b : 0) * s.N + min(n + r, s.N - 1);
-    w[b] = s.w + ((int64_t)t.e * (ACT ? 2 : 1) * s.N + row) * kp + 16 * q;
+    w[i] = s.w + ((int64_t)t.e * (ACT ? 2 : 1) * s.N + row) * kp + 16 * q;
     // (32 and 16 divide 128: a work-group's rows share a block)
-    ws[b] = s.ws + ((int64_t)t.e * (ACT ? 2 : 1) * s.nb + (ACT ? b : 0) * s.nb + n0 / kGroup) * s.kg;
+    ws[i] = s.ws + ((int64_t)t.e * (ACT ? 2 : 1) * s.nb + (ACT ? b : 0) * s.nb + n0 / kGroup) * s.kg;
   }
   const uint8_t* x[MB];
   const float* xs[MB];
@@ -166,17 +171,17 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
       xs_step[m] = xr < 0 ? 0 : 1;
     }
   }
-  f32x4 acc[MB][2] = {};
+  f32x4 acc[MB][NB] = {};
   // groups g0 .., U of each wave
   auto turn = [&](int g0, auto mine) {
     constexpr int U = decltype(mine)::value;
     // (groups past the last are loaded as it and not used)
-    i32x8 vw[U][2], vx[U][MB];
-    float sw[U][2], sx[U][MB];
+    i32x8 vw[U][NB], vx[U][MB];
+    float sw[U][NB], sx[U][MB];
     // rows on their way to codes: 16 lanes a group, as in k_fp8_rows.  The first
     // ones' loads come before the weights', so that their codes are made while
     // the weights are on their way.
-    constexpr int kGroups = U * kFewWaves;
+    constexpr int kGroups = U * 4;
     const int groups = t.n * kGroups, l = threadIdx.x & 15;
     auto load_row = [&](int i, float (&v)[8]) {
       const int row = i / kGroups, c = (g0 + i % kGroups) * kGroup + 8 * l;
@@ -196,9 +201,9 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
     if constexpr (!kCodes) xr = load_row(threadIdx.x >> 4, v);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int g = min(g0 + u * kFewWaves + wv, s.kg - 1);
+      const int g = min(g0 + u * 4 + quarter, s.kg - 1);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) vw[u][b] = load_codes(w[b] + (int64_t)g * kGroup), sw[u][b] = ws[b][g];
+      for (int b = 0; b < NB; ++b) vw[u][b] = load_codes(w[b] + (int64_t)g * kGroup), sw[u][b] = ws[b][g];
       if constexpr (kCodes) {
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
@@ -211,9 +216,9 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!kCodes) {
       if (g0) __syncthreads();  // (the turn before is read)
-      for (int i = threadIdx.x >> 4; i < (groups + 15) / 16 * 16; i += 64 * kFewWaves / 16) {
+      for (int i = threadIdx.x >> 4; i < (groups + 4 * W - 1) / (4 * W) * (4 * W); i += 4 * W) {
         const int row = i / kGroups, g = i % kGroups;
-        if (i >= 16) xr = load_row(i, v);
+        if (i >= 4 * W) xr = load_row(i, v);
         uint32_t a = row_max(amax_bits<false>(v));
         if (__any(a >= kInfBits)) a = row_max(amax_bits<true>(v));
         const Factors f = factors8(a);
@@ -229,9 +234,11 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int gl = u * kFewWaves + wv;
+      const int gl = u * 4 + quarter;
       if (g0 + gl >= s.kg) break;
-      const Frag hw[2] = {operand(vw[u][0]), operand(vw[u][1])};
+      Frag hw[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) hw[b] = operand(vw[u][b]);
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         if constexpr (!kCodes) {
@@ -241,7 +248,7 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
         }
         const Frag hx = operand(vx[u][m]);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
           const f32x4 p = group_sums(hw[b], hx);
           const float f = sx[u][m] * sw[u][b];
 #pragma unroll
@@ -258,16 +265,16 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
       turn(g0, std::integral_constant<int, kMine / 2>{});
   }
 
-  // sums of the four waves: [wave][tile of 16 x 16][lane]
+  // sums of the waves: [wave][tile of 16 x 16][lane]
   if (!kCodes) __syncthreads();
   f32x4* part = lds.part;
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) part[(wv * MB * 2 + m * 2 + b) * 64 + lane] = acc[m][b];
+    for (int b = 0; b < NB; ++b) part[(quarter * MB * 2 + m * 2 + b0 + b) * 64 + lane] = acc[m][b];
   __syncthreads();
   O* Y = (O*)s.y;
-  for (int i = wv; i < (ACT ? MB : MB * 2); i += kFewWaves) {
+  for (int i = wv; i < (ACT ? MB : MB * 2); i += W) {
     const int m = ACT ? i : i >> 1;
     f32x4 v[2];
 #pragma unroll
@@ -275,7 +282,7 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
       const int at = ACT ? m * 2 + b : i;
       v[b] = part[at * 64 + lane];
 #pragma unroll
-      for (int o = 1; o < kFewWaves; ++o) {
+      for (int o = 1; o < 4; ++o) {
         const f32x4 p = part[(o * MB * 2 + at) * 64 + lane];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[b][j] += p[j];
@@ -303,9 +310,9 @@ __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int a
 template <class X, class O>
 constexpr int kFewOnUnit = sizeof(O) == 2 && std::is_same<X, E4M3>::value ? 4 : 3;
 
-template <class X, class O, bool ACT>
-__global__ __launch_bounds__(64 * kFewWaves, (kFewOnUnit<X, O>)) void k_mm8_few(Mm8Args s) {
-  __shared__ FewLds lds;
+template <class X, class O, bool ACT, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : (kFewOnUnit<X, O>)) void k_mm8_few(Mm8Args s) {
+  __shared__ FewLds<W> lds;
   int at = 0;
   if (!std::is_same<X, E4M3>::value && s.rows) at = s.rows[min((int)threadIdx.x & 63, s.R - 1)];
   Tile t{0, 0, 0};
@@ -317,9 +324,9 @@ __global__ __launch_bounds__(64 * kFewWaves, (kFewOnUnit<X, O>)) void k_mm8_few(
   }
   if (t.n <= 0) return;
   if (t.n <= 16)
-    few8_rows<X, O, ACT, 1>(s, t, at, lds);
+    few8_rows<X, O, ACT, 1, W>(s, t, at, lds);
   else
-    few8_rows<X, O, ACT, 2>(s, t, at, lds);
+    few8_rows<X, O, ACT, 2, W>(s, t, at, lds);
 }
 
 // --------------------------------------------------------------- tiled
@@ -705,22 +712,38 @@ void with_out(int o_dtype, F f) {
 // (768) 30 and 27; one of 8192 x 2048, 64 rows (512) 12.7 and 12.6.
 constexpr int kFewMean = 8, kFewMean4 = 16;
 
+long long few_parts(int R, int E, int N, int act) {
+  const long long mean = ((long long)R + E - 1) / E, wn = act ? 2ll * N : N;
+  return (wn + kFewCols - 1) / kFewCols * ((mean + kFewRows - 1) / kFewRows) * E;
+}
+
 bool few8(int R, int E, int N, int act) {
-  const long long mean = ((long long)R + E - 1) / E;
-  const long long wn = act ? 2ll * N : N;
-  const long long parts = (wn + kFewCols - 1) / kFewCols * ((mean + kFewRows - 1) / kFewRows) * E;
+  const long long mean = ((long long)R + E - 1) / E, parts = few_parts(R, E, N, act);
   return max_tiles(R, E, kFewRows) <= 65535 &&
          (mean <= kFewMean || (mean <= kFewMean4 && parts <= 4 * kUnits) || parts <= 2 * kUnits);
 }
 
+// Rows quantized by the work-groups that use them: eight waves where there is at
+// most one work-group a compute unit (4 rows of 4096 x 4096 9.3 us instead of
+// 12.1; 8 experts of 1536 x 2048, 384 work-groups, 10.8 instead of 8.9) and at
+// least a turn of 16 groups (one row of 2048 x 512 4.4 instead of 3.4).
+bool few_more(int R, int E, int N, int K, int act) {
+  return few_parts(R, E, N, act) <= kUnits && K >= 16 * kGroup;
+}
+
 // Few rows are quantized by the work-groups that use them, without a launch of
-// their own: each work-group of an expert does it again, which takes it 1.2 us
-// per 4096 elements (one row of 8 experts of 1536 x 2048 9.0 us, by two launches
-// 13.7, of 32 experts 21 and 24; 4 rows of one 4096 x 4096 projection 12.0 and
-// 13.6, 6 rows 14.4 and 13.5).  At most 32 rows, which one expert may have all:
-// k_mm8_few reads the indexes of all R rows at once, one a lane.
-bool on_the_way(int R, int E, int K) {
-  return R <= 32 && (long long)((R + E - 1) / E) * K <= 16384;
+// their own: each work-group of an expert does it again, which takes four waves
+// 1.2 us per 4096 elements.  us by it and by two launches: one row of 8 experts
+// of 1536 x 2048 8.9 and 12.2, of 32 experts 21 and 24; of 8 experts of 4096 x
+// 4096, one row 31 and 33, four rows 37 and 34; of one such projection, one row
+// 7.6 and 11.3, 4 rows 9.3 and 12.0, 6 rows 10.9 and 12.2, 8 rows 12.5 and 12.5;
+// 16 rows of 4096 x 2048 10.7 and 9.5.
+// At most 32 rows, which one expert may have all: k_mm8_few reads the indexes of
+// all R rows at once, one a lane.
+bool on_the_way(int R, int E, int N, int K, int act) {
+  const long long mean = ((long long)R + E - 1) / E;
+  const long long most = mean <= 8 && few_more(R, E, N, K, act) ? 32768 : few_parts(R, E, N, act) <= 2 * kUnits ? 16384 : 8192;
+  return R <= 32 && mean * K <= most;
 }
 
 // The workspace of rows that are quantized before the products: codes, then
@@ -729,7 +752,7 @@ struct RowsWs {
   size_t codes, scales;
 };
 RowsWs rows_ws(int x_dtype, int64_t rows, int R, int E, int N, int K, int act) {
-  if (x_dtype == kE4M3 || (few8(R, E, N, act) && on_the_way(R, E, K))) return RowsWs{0, 0};
+  if (x_dtype == kE4M3 || (few8(R, E, N, act) && on_the_way(R, E, N, K, act))) return RowsWs{0, 0};
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   return RowsWs{al((size_t)rows * groups_of(K) * kGroup), al((size_t)rows * groups_of(K) * 4)};
 }
@@ -837,12 +860,11 @@ int bitsmoe_fp8_matmul(int x_dtype, const void* x, int64_t ldx, const float* x_s
     }
     auto go = [&](auto tag) {
       using X = decltype(tag);
-      if (act)
-        hipLaunchKernelGGL((k_mm8_few<X, O, true>), grid, dim3(64 * kFewWaves), 0,
-                           (hipStream_t)stream, s);
-      else
-        hipLaunchKernelGGL((k_mm8_few<X, O, false>), grid, dim3(64 * kFewWaves), 0,
-                           (hipStream_t)stream, s);
+      constexpr int W = std::is_same<X, E4M3>::value ? 4 : 8;  // (codes: four waves always)
+      const bool more = W == 8 && few_more(R, E, N, K, act);
+      void (*kernel)(Mm8Args) = act ? k_mm8_few<X, O, true, 4> : k_mm8_few<X, O, false, 4>;
+      if (more) kernel = act ? k_mm8_few<X, O, true, W> : k_mm8_few<X, O, false, W>;
+      hipLaunchKernelGGL(kernel, grid, dim3(more ? 512 : 256), 0, (hipStream_t)stream, s);
     };
     if (given || need)
       go(E4M3{});

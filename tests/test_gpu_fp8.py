@@ -388,6 +388,27 @@ def test_a_few_rows_of_many(bm, E, per, N, K, X):
     assert torch.equal(y[keep], want[keep])
 
 
+@pytest.mark.parametrize("E, counts, N, K", [(1, [1], 100, 2048), (1, [8], 40, 4096), (1, [2], 33, 14000), (2, [1, 15], 48, 2050), (3, [7, 0, 1], 200, 5000),
+                                             (4, [0, 20, 0, 0], 64, 2176), (1, [6], 16, 4224), (1, [32], 130, 500), (1, [30], 4100, 4096), (1, [20], 8200, 384)])
+@pytest.mark.parametrize("dtype, out", [(BF16, BF16), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("act", [None, "silu_mul"])
+def test_few_rows_with_many_inputs(bm, E, counts, N, K, dtype, out, act):
+    """Some turns of groups and a part of one, rows on the way or not."""
+    _say("fp8 few rows", E, counts, N, K, dtype, out, act)
+    g = rng(K + N)
+    bounds, R = ragged(counts, tail=0)
+    codes, scales = make_weights(bm, g, E, N, K, 2 if act else 1)
+    x = normal(g, 9, K, dtype=dtype)
+    rows = torch.randint(0, 18, (R,), generator=g, device="cuda", dtype=torch.int32)
+    q, s = bm.fp8_rows(x)
+    y = torch.full((R, N), 7.0, dtype=out, device="cuda")
+    bm.fp8_matmul(x, codes, scales, y, bounds=bounds, rows=rows, div=2, act=act)
+    want, off = reference(values(q, s, 1)[rows.long() // 2], weight_values(codes, scales, 2 if act else 1), bounds, R, act, out)
+    check(y, want, half_step(want, out) + off + (want.abs() * 2.0 ** -20 if act else 0) + 1e-30, "y")
+    given = bm.fp8_matmul(q, codes, scales, torch.full_like(y, 7.0), x_scales=s, bounds=bounds, rows=rows, div=2, act=act)
+    assert torch.equal(given, y)
+
+
 @pytest.mark.parametrize("R, N, K", [(1, 4096, 2048), (1, 33, 100), (7, 512, 512), (70, 300, 384), (600, 520, 700)])
 @pytest.mark.parametrize("given", [False, True])
 def test_one_dense_projection(bm, R, N, K, given):
