@@ -108,10 +108,10 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // at a time, into LDS, while its weights are on their way.
 //
 // Bound by the weights' bytes: two rows of each of 128 experts of 1536 x 2048
-// (403 MB) 68 us from codes, 5.9 TB/s; 32 tokens of them, Zipf, 46 us (5.6 TB/s
-// over the experts reached); the 8 of one token (25 MB) 8.3 us, a chain of
+// (403 MB) 68 us from codes, 5.9 TB/s; 32 tokens of them, Zipf, 45 us (5.2 TB/s
+// over the experts reached); the 8 of one token (25 MB) 8.2 us, a chain of
 // latencies: bounds, row, its codes, weights, sums of the waves.  With more rows
-// (up to 64 a work-group) 64 rows of 4096 x 4096 19 us instead of 12; with the
+// (up to 64 a work-group) 64 rows of 4096 x 4096 19 us instead of 13; with the
 // last turn always whole, where half its groups do not exist, 64 experts of 512 x
 // 1024, 8 rows each, 14.6 instead of 9.7.
 constexpr int kFewRows = 32, kFewCols = 32;
