@@ -432,11 +432,17 @@ def _matrix(name, t, shape=None):
     if len(have) != 2 or (shape is not None and have != shape):
         raise ValueError("%s must be %s, got %s" % (name, "2-d" if shape is None else
                                                     "of shape %s" % (shape,), tuple(have)))
+    return _strided(name, t, have[0], have[1])
+
+
+def _strided(name, t, rows, columns):
+    """_matrix for a tensor whose shape the caller has read (each look at a tensor
+    costs about a tenth of a microsecond, a small call seven)."""
     step, one = t.stride()
-    if one != 1 and have[1] > 1:
+    if one != 1 and columns > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
     # the stride of a single row says nothing
-    return t.data_ptr(), max(step, have[1]) if have[0] <= 1 else step
+    return t.data_ptr(), max(step, columns) if rows <= 1 else step
 
 
 def _array(name, t, dtype, shape=None):
@@ -805,13 +811,13 @@ def fp8_rows(x, codes=None, scales=None, act=None, bounds=None, stream=None):
     float32 scale for each 128 elements, K' = K rounded up to whole groups.
     With act="silu_mul" of SiLU(gate) * up of rows x = [gate | up] (R x 2K).
     With bounds only the experts' rows."""
-    R, K = x.shape
-    if act not in ACT or (act and K % 2):
-        raise ValueError("act=%r with %d columns of x" % (act, K))
-    K = K // 2 if act else K
+    R, columns = x.shape
+    if act not in ACT or (act and columns % 2):
+        raise ValueError("act=%r with %d columns of x" % (act, columns))
+    K = columns // 2 if act else columns
     G = _groups(K)
     dev = _same_device(x, codes, scales, bounds)
-    px, ldx = _matrix("x", x)
+    px, ldx = _strided("x", x, R, columns)
     if codes is None:
         codes = _new((R, G * GROUP), _F8, dev, stream)
     if scales is None:
@@ -891,16 +897,23 @@ def fp8_matmul(x, codes, scales, y=None, x_scales=None, bounds=None, rows=None, 
         raise ValueError("x has %d inputs, the weights %d" % (K, kp))
     R = rows.shape[0] if rows is not None else y.shape[0] if y is not None else x_rows
     dev = _same_device(x, codes, scales, y, x_scales, bounds, rows, ws)
-    px, ldx = _matrix("x", x, (x_rows, kp) if given else None)
+    px, ldx = _strided("x", x, x_rows, K)
     ps, lds = None, 0
     if given:
+        if K != kp:
+            raise ValueError("x must have %d codes a row, got %d" % (kp, K))
         if x_scales.dtype is not _F32:
             raise ValueError("x_scales must be float32")
         ps, lds = _matrix("x_scales", x_scales, (x_rows, kp // GROUP))
-    pr, div = _gather(x, rows, div, R)
+    if rows is not None:
+        pr = _array("rows", rows, _I32, (R,))
+    elif x_rows < R:
+        raise ValueError("x has %d rows, the sorted layout %d" % (x_rows, R))
+    else:
+        pr, div = None, 1
     pc = _array("codes", codes, _F8)
     pw = _array("scales", scales, _F32, (E, -(-N // GROUP) * (2 if act else 1), kp // GROUP))
-    pb = None if bounds is None else _bounds(bounds, E)
+    pb = None if bounds is None else _array("bounds", bounds, _I32, (E + 1,))
     if y is None:
         y = _new((R, N), torch.bfloat16 if given else kind, dev, stream)
     py, ldy = _matrix("y", y, (R, N))
@@ -940,7 +953,7 @@ def moe_balance(logits, ids, seqs=None, loss=None, z=None, counts=None, tokens=N
     T, E = logits.shape
     k = ids.shape[1]
     dev = _same_device(logits, ids, seqs, loss, z, counts, tokens, ws)
-    pl, ld = _matrix("logits", logits)
+    pl, ld = _strided("logits", logits, T, E)
     pq, S = _sequences(seqs)
     loss = _new(S, _F32, dev, stream) if loss is None else loss
     z = _new(S, _F32, dev, stream) if z is None else z
@@ -967,7 +980,7 @@ def moe_balance_grad(logits, ids, counts, tokens, dloss=None, dz=None, seqs=None
     T, E = logits.shape
     k = ids.shape[1]
     dev = _same_device(logits, ids, counts, tokens, dloss, dz, seqs, dlogits)
-    pl, ld = _matrix("logits", logits)
+    pl, ld = _strided("logits", logits, T, E)
     pq, S = _sequences(seqs)
     if dlogits is None:
         if add:
