@@ -7,9 +7,12 @@
 //   f_e = E / (k n) #{(t, j): id_tj = e},   P_e = 1/n sum_t p_te
 //   loss = sum_e f_e P_e,   z = 1/n sum_t lse_t^2,   lse = log sum_e exp(l_te)
 //   dl_te = p_te (dloss / n (f_e - sum_m p_tm f_m) + 2 dz / n lse_t)
-// (f does not depend on the logits as far as a gradient goes).  softmax and
-// each work-group's sums are float32; the sums over work-groups and the losses
-// are float64.  No sum depends on the order of atomics.
+// (f does not depend on the logits as far as a gradient goes).  softmax is
+// float32, and so are the sums of a run of up to 32 tokens of a lane and of the
+// work-group's lanes: at most 50 additions between a token's term and the sums of
+// runs and work-groups and the losses, which are float64.  (A work-group's share
+// of the tokens grows with them: in float32 to its end, z of 2^24 tokens of 257
+// experts was off by 5e-5.)  No sum depends on the order of atomics.
 #include <type_traits>
 
 #include "experts.h"
@@ -20,6 +23,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxSlots = 64, kMaxExperts = 2048;
+constexpr int kRunTurns = 32;    // tokens that a lane adds up in float32
+constexpr int kOneMost = 1024;   // tokens of a call in one launch (one_chunk)
 
 template <int kCtrl>
 __device__ inline float dpp(float v) {
@@ -195,8 +200,8 @@ struct Outs {
   int32_t *counts, *tokens;
 };
 
-// Sums of one chunk into its record; ONE: of a whole sequence, whose losses it
-// writes.  Bound by latencies and the exp (16384 tokens of 128
+// Sums of one chunk, a run of tokens at a time, into its record; ONE: of a whole
+// sequence, one run, whose losses it writes.  Bound by latencies and the exp (16384 tokens of 128
 // experts, 8.4 MB: 6 us; 67 tokens of 8 experts with the losses 4.1).
 template <class T, int L, int V, int NT, bool ONE>
 __global__ __launch_bounds__(NT) void k_balance_part(
@@ -222,63 +227,84 @@ __global__ __launch_bounds__(NT) void k_balance_part(
   const int tid = threadIdx.x, l = tid & (L - 1), wv = tid >> 6;
   for (int e = tid; e < E; e += NT) count[e] = 0;
   __syncthreads();
-  float sum[V] = {}, z = 0.f;
-  int n = 0;
-  each_token<T, L, V, NT>(c, logits, ld, ids, E, k, [&](int64_t t, bool, const Token<T, L, V>& in, const Soft<V>& s) {
-    if (s.part) {
+  constexpr int kRun = kRunTurns * (NT / L);  // tokens
+  static_assert(!ONE || kOneMost <= kRun, "one run");
+  constexpr int kOwn = (L * V + NT - 1) / NT;  // experts tid, tid + NT, .. of a thread
+  double own[kOwn] = {}, zz = 0.0;
+  int nn = 0, at = 0;
+  do {
+    const Tile run{c.e, c.row0 + at, ONE ? c.n : min(kRun, c.n - at)};
+    float sum[V] = {}, z = 0.f;
+    int n = 0;
+    each_token<T, L, V, NT>(run, logits, ld, ids, E, k, [&](int64_t t, bool, const Token<T, L, V>& in, const Soft<V>& s) {
+      if (s.part) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[v] += s.p[v];
-      z += s.lse * s.lse;
-      ++n;
-      if (in.id >= 0 && in.id < E) atomicAdd(&count[in.id], 1);
-      for (int j = l + L; j < k; j += L) {
-        const int id = ids[t * k + j];
-        if (id >= 0 && id < E) atomicAdd(&count[id], 1);
+        for (int v = 0; v < V; ++v) sum[v] += s.p[v];
+        z += s.lse * s.lse;
+        ++n;
+        if (in.id >= 0 && in.id < E) atomicAdd(&count[in.id], 1);
+        for (int j = l + L; j < k; j += L) {
+          const int id = ids[t * k + j];
+          if (id >= 0 && id < E) atomicAdd(&count[id], 1);
+        }
       }
+    });
+#pragma unroll
+    for (int d = L; d < 64; d <<= 1) {  // the wave's tokens
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum[v] += __shfl_xor(sum[v], d, 64);
+      z += __shfl_xor(z, d, 64);
+      n += __shfl_xor(n, d, 64);
     }
-  });
+    if (!ONE && at) __syncthreads();  // (the run before is read)
+    if ((tid & 63) < L) {
 #pragma unroll
-  for (int d = L; d < 64; d <<= 1) {  // the wave's tokens
+      for (int v = 0; v < V; ++v)
+        if (l * V + v < E) sums[wv * E + l * V + v] = sum[v];
+      if (l == 0) zs[wv] = z, ns[wv] = n;
+    }
+    __syncthreads();
+    z = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] += __shfl_xor(sum[v], d, 64);
-    z += __shfl_xor(z, d, 64);
-    n += __shfl_xor(n, d, 64);
-  }
-  if ((tid & 63) < L) {
+    for (int w = 0; w < W; ++w) z += zs[w], nn += ns[w];
+    zz += (double)z;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (l * V + v < E) sums[wv * E + l * V + v] = sum[v];
-    if (l == 0) zs[wv] = z, ns[wv] = n;
-  }
-  __syncthreads();
-  z = 0.f, n = 0;
+    for (int i = 0; i < kOwn; ++i) {
+      const int e = tid + i * NT;
+      float p = 0.f;
+      if (e < E) {
 #pragma unroll
-  for (int w = 0; w < W; ++w) z += zs[w], n += ns[w];
+        for (int w = 0; w < W; ++w) p += sums[w * E + e];
+      }
+      own[i] += (double)p;
+    }
+    at += kRun;
+  } while (!ONE && at < c.n);
   double part = 0.0;
   uint32_t* out = ONE ? nullptr : parts + (size_t)blockIdx.x * record(E);
-  for (int e = tid; e < E; e += NT) {
-    float p = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) p += sums[w * E + e];
+  for (int i = 0; i < kOwn; ++i) {
+    const int e = tid + i * NT;
+    if (e >= E) break;
     if (ONE) {
       o.counts[(size_t)c.e * E + e] = count[e];
-      part += (double)count[e] * (double)p;
+      part += (double)count[e] * own[i];
     } else {
-      out[e] = __float_as_uint(p);
+      out[e] = __float_as_uint((float)own[i]);
       out[E + e] = (uint32_t)count[e];
     }
   }
   if (ONE) {
     part = block_sum<W>(part, buf);
-    const double inv = n > 0 ? 1.0 / n : 0.0;
+    const double inv = nn > 0 ? 1.0 / nn : 0.0;
     if (tid == 0) {
       o.loss[c.e] = (float)(part * inv * inv * ((double)E / k));
-      o.z[c.e] = (float)((double)z * inv);
-      o.tokens[c.e] = n;
+      o.z[c.e] = (float)(zz * inv);
+      o.tokens[c.e] = nn;
     }
   } else if (tid == 0) {
-    out[2 * E] = __float_as_uint(z);
-    out[2 * E + 1] = (uint32_t)n;
+    out[2 * E] = __float_as_uint((float)zz);
+    out[2 * E + 1] = (uint32_t)nn;
   }
 }
 
@@ -454,7 +480,7 @@ int chunk_tokens(int T) {
 // more of sequences that are short on average.  (us by it and by two launches,
 // which also take the host 4 us longer: 67 tokens 4.2 and 8, 256 of 128 experts
 // 8.9 and 8, 512 14 and 8, whatever sequence has them.)
-constexpr int kOneTokens = 256, kOneMost = 1024, kOneMean = 128;
+constexpr int kOneTokens = 256, kOneMean = 128;
 bool one_chunk(int T, int E, int S) {
   return T >= 1 && E <= 256 && (T <= kOneTokens || (T <= kOneMost && T <= (long long)kOneMean * S));
 }
