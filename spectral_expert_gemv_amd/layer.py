@@ -93,19 +93,23 @@ class ExpertLayer:
     @classmethod
     def fp8(cls, w1, w2, transposed=False, stream=None, **kw):
         """8-bit experts (e4m3 with a scale for each block of 128 x 128) from
-        dense device weights, float32, float16 or bfloat16.  transposed: also
+        dense contiguous device weights, float32, float16 or bfloat16.  transposed: also
         their transposed copies, which gradients() needs; F must then be a
         multiple of 128."""
         E, F2, D = w1.shape
         F = F2 // 2
         if F2 % 2 or w2.shape != (E, D, F):
             raise ValueError("w1 of shape %s with w2 of shape %s" % (tuple(w1.shape), tuple(w2.shape)))
+        # (no copy on the way: it would not be made on `stream`)
+        for name, w in (("w1", w1), ("w2", w2)):
+            if not w.is_contiguous():
+                raise ValueError("%s must be contiguous" % name)
         if F % bitsmoe.GROUP == 0:  # no block lies in both halves
             q1 = bitsmoe.fp8_weights(w1, transposed=transposed, stream=stream)
         elif transposed:
             raise ValueError("F=%d is not a multiple of %d" % (F, bitsmoe.GROUP))
         else:
-            c, s = bitsmoe.fp8_weights(w1.reshape(2 * E, F, D), stream=stream)
+            c, s = bitsmoe.fp8_weights(w1.view(2 * E, F, D), stream=stream)
             q1 = c.reshape(E, F2, -1), s.reshape(E, -1, s.shape[2])
         return cls(q1, bitsmoe.fp8_weights(w2, transposed=transposed, stream=stream), fp8=True, **kw)
 

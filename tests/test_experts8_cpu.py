@@ -153,3 +153,15 @@ def test_binding_refuses(i):
     call, what = BAD[i]
     with pytest.raises(ValueError, match=what):
         call()
+
+
+@pytest.mark.parametrize("F", [96, 128])
+@pytest.mark.parametrize("which", ["w1", "w2"])
+def test_layer_refuses_weights_with_gaps(F, which):
+    """Whether F makes whole blocks or not: a copy of them would be made on
+    another stream than the call's."""
+    from spectral_expert_gemv_amd.layer import ExpertLayer
+    w = dict(w1=gpu(2, 2 * F, 256), w2=gpu(2, 256, F))
+    w[which] = gpu(2, w[which].shape[2], w[which].shape[1]).transpose(1, 2)
+    with pytest.raises(ValueError, match="%s must be contiguous" % which):
+        ExpertLayer.fp8(**w, stream=1)
