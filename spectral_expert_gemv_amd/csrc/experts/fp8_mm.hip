@@ -115,6 +115,10 @@ __device__ __forceinline__ int x_row8(const Mm8Args& s, int i) {
 // last turn always whole, where half its groups do not exist, 64 experts of 512 x
 // 1024, 8 rows each, 14.6 instead of 9.7.
 constexpr int kFewRows = 32, kFewCols = 32;
+// Most sorted rows of a call that quantizes them on the way: every wave holds
+// the indexes of all of them, one a lane.
+constexpr int kWayRows = 32;
+static_assert(kWayRows <= 64, "a shuffle finds a row's index");
 
 // 16 + 16 bytes of a row of codes at group start p (+ 16 q)
 __device__ __forceinline__ i32x8 load_codes(const uint8_t* p) {
@@ -134,7 +138,7 @@ struct FewLds {
   float scales[16 * kTurn];
 };
 
-// (at: for rows that are not codes, the index of row `lane` of all R <= 64 rows)
+// (at: for rows that are not codes, the index of row `lane` of all R <= kWayRows rows)
 template <class X, class O, bool ACT, int MB, int W>
 __device__ __forceinline__ void few8_rows(const Mm8Args& s, const Tile& t, int at, FewLds<W>& lds) {
   constexpr bool kCodes = std::is_same<X, E4M3>::value;
@@ -738,12 +742,11 @@ bool few_more(int R, int E, int N, int K, int act) {
 // 4096, one row 31 and 33, four rows 37 and 34; of one such projection, one row
 // 7.6 and 11.3, 4 rows 9.3 and 12.0, 6 rows 10.9 and 12.2, 8 rows 12.5 and 12.5;
 // 16 rows of 4096 x 2048 10.7 and 9.5.
-// At most 32 rows, which one expert may have all: k_mm8_few reads the indexes of
-// all R rows at once, one a lane.
+// At most kWayRows rows, which one expert may have all.
 bool on_the_way(int R, int E, int N, int K, int act) {
   const long long mean = ((long long)R + E - 1) / E;
   const long long most = mean <= 8 && few_more(R, E, N, K, act) ? 32768 : few_parts(R, E, N, act) <= 2 * kUnits ? 16384 : 8192;
-  return R <= 32 && mean * K <= most;
+  return R <= kWayRows && mean * K <= most;
 }
 
 // The workspace of rows that are quantized before the products: codes, then
