@@ -9,10 +9,11 @@
 //   dl_te = p_te (dloss / n (f_e - sum_m p_tm f_m) + 2 dz / n lse_t)
 // (f does not depend on the logits as far as a gradient goes).  softmax is
 // float32, and so are the sums of a run of up to 32 tokens of a lane and of the
-// work-group's lanes: at most 50 additions between a token's term and the sums of
+// work-group's lanes: at most 42 additions between a token's term and the sums of
 // runs and work-groups and the losses, which are float64.  (A work-group's share
 // of the tokens grows with them: in float32 to its end, z of 2^24 tokens of 257
-// experts was off by 5e-5.)  No sum depends on the order of atomics.
+// experts was off by 5e-5, their loss by 1.5e-5.)  No sum depends on the order of
+// atomics.
 #include <type_traits>
 
 #include "experts.h"
@@ -201,8 +202,9 @@ struct Outs {
 };
 
 // Sums of one chunk, a run of tokens at a time, into its record; ONE: of a whole
-// sequence, one run, whose losses it writes.  Bound by latencies and the exp (16384 tokens of 128
-// experts, 8.4 MB: 6 us; 67 tokens of 8 experts with the losses 4.1).
+// sequence, one run, whose losses it writes.  Bound by latencies and the exp
+// (16384 tokens of 128 experts, 8.4 MB: 6 us; 67 tokens of 8 experts with the
+// losses 4.1).
 template <class T, int L, int V, int NT, bool ONE>
 __global__ __launch_bounds__(NT) void k_balance_part(
     const T* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,

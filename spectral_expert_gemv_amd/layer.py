@@ -146,7 +146,8 @@ class ExpertLayer:
 
     def balance(self, logits, ids, balance=0.0, z=0.0, seqs=None, dlogits=None, stream=None):
         """(loss, z, counts, tokens) of moe_balance; with dlogits the gradient of
-        balance * mean(loss) + z * mean(z) over the sequences is added to it."""
+        balance * mean(loss) + z * mean(z) over the sequences is added to it (in
+        gradients() it holds the router's, rounded to its type before)."""
         bm, s = bitsmoe, stream
         out = bm.moe_balance(logits, ids, seqs, stream=s)
         if dlogits is not None:

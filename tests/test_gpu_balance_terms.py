@@ -145,3 +145,28 @@ def test_wide_gradients_by_differences(bm, E, k):
             size = float(t[:, i, e].abs().sum())
             slack = h * h * size + 2.0 ** -50 * (abs(loss(row)) + 1) / h
             assert abs((loss(up) - loss(dn)) / (2 * h) - float(got[i, e])) <= float(tol[i, e]) + slack
+
+
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_a_token_that_the_router_turned_away(bm, bad):
+    """Logits with a NaN or +inf: the router's ids of -1 keep the token out of the
+    layer's losses, which are those of the others."""
+    from spectral_expert_gemv_amd.layer import ExpertLayer
+    T, E, k, D, F = 40, 8, 2, 64, 64
+    g = torch.Generator()
+    g.manual_seed(3)
+    normal = lambda *s: torch.randn(*s, generator=g).to("cuda", F16) * 0.1  # noqa: E731
+    x, dout, l = normal(T, D), normal(T, D), torch.randn(T, E, generator=g).cuda()
+    l[7, 3] = bad
+    l[30, 0] = bad
+    layer = ExpertLayer(normal(E, 2 * F, D), normal(E, D, F))
+    seqs = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
+    loss, z, counts, tokens = layer.gradients(x, l, k, dout, balance=0.5, z=0.1, seqs=seqs)[5]
+    assert tokens.tolist() == [19, 19] and counts.sum(1).tolist() == [38, 38]
+    keep = (torch.arange(T, device="cuda") != 7) & (torch.arange(T, device="cuda") != 30)
+    want = layer.gradients(x[keep], l[keep], k, dout[keep], balance=0.5, z=0.1, seqs=torch.tensor([0, 19, 38], dtype=torch.int32, device="cuda"))
+    for a, b in zip((loss, z), want[5]):
+        # (their sums may have another order: terms of one sign, 42 additions each)
+        assert bool(((a - b).abs() <= 2.0 ** -18 * b.abs()).all())
+    d = layer.gradients(x, l, k, dout, balance=0.5, z=0.1, seqs=seqs)[2]
+    assert bool(d[~keep].isnan().all()) and torch.equal(d[keep], want[2])
