@@ -102,7 +102,9 @@ def test_every_element(bm, T, E, k, cuts, dtype):
     _, _, got_counts, got_tokens = bm.moe_balance(l, ids, seqs)
     assert torch.equal(got_counts.cpu(), counts) and torch.equal(got_tokens.cpu(), tokens)
     check(bm.moe_balance_grad(l, ids, got_counts, got_tokens, dloss, dz, seqs), want, tol, "dlogits")
-    there = torch.randn(T, E, device="cuda").to(dtype)
+    g = torch.Generator()
+    g.manual_seed(E)
+    there = torch.randn(T, E, generator=g).to("cuda", dtype)
     got = bm.moe_balance_grad(l, ids, got_counts, got_tokens, dloss, dz, seqs, there.clone(), add=True)
     total = there.double().cpu() + want
     # (the sum in float32 is rounded, then its rounding to the type)
