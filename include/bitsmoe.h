@@ -490,8 +490,9 @@ int bitsmoe_fp8_weights(int dtype, const void* w, int E, int N, int K, void* cod
  * 16-bit outputs: the 8-bit instruction aligns eight products at a time to their
  * largest and drops what lies more than 13 bits below its first bit, up to 7
  * 2^-13 of that product; 1.4e-5 to 5e-5 of a result where nothing cancels, where
- * its rounding adds up to 4.9e-4 (fp16) or 3.9e-3 (bf16).  Where outliers cancel
- * the error stays relative to them: ask for F32 where that matters.  SiLU's
+ * its rounding adds up to 4.9e-4 (fp16) or 3.9e-3 (bf16).  Where products cancel
+ * (a gate near 0 among large ones) the error stays relative to them: ask for F32
+ * where that matters.  SiLU's
  * exponent for 16-bit outputs of many rows keeps its own rounding (5e-6).
  * A call repeats its bits; those of a row may change with the call's sizes, which
  * choose the kernel (the order of its sums, and for 16-bit outputs the SiLU).

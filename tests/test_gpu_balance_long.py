@@ -69,3 +69,44 @@ def test_the_long_sequence_of_many(bm):
     tol = want.abs() * 2.0 ** -8 + 2 * (E + 32) * 2.0 ** -23 * (abs(a) * (f + 1.0) + abs(b) * (math.log(E) + 1)) / E
     for at in (slice(0, 300), slice(n // 2, n // 2 + 300), slice(n - 300, n)):
         assert bool(((d[at].double().cpu() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("T, E, k, S, step", [(70000, 8, 2, 65535, 1), (200, 8, 2, 65535, 0), (69000, 300, 3, 65535, 1), (300000, 16, 2, 5000, 59)])
+def test_thousands_of_sequences(bm, T, E, k, S, step):
+    """Of `step` tokens each (0: of one token, far apart), against the definition
+    in 64 bits.  Tolerances: (E + 32) 2^-23 of p for softmax, as in the sums of a
+    few tokens; lse is off by as much and its own steps."""
+    print("balance of", S, "sequences", T, E, k, flush=True)
+    g = torch.Generator()
+    g.manual_seed(S + E)
+    l = (torch.randn(T, E, generator=g) * 2).cuda()
+    ids = torch.topk(l, k, dim=1).indices.int()
+    at = torch.arange(S + 1, device="cuda")
+    seqs = (at * step if step else at // (S // T)).clamp(max=T).int()
+    loss, z, counts, tokens = bm.moe_balance(l, ids, seqs)
+    sign = torch.where(at[:S] % 2 == 0, 1.0, -1.0)
+    d = bm.moe_balance_grad(l, ids, counts, tokens, sign, 0.1 * sign, seqs)
+
+    seq = torch.bucketize(torch.arange(T, device="cuda", dtype=torch.int32), seqs[1:], right=True)
+    inside = seq < S
+    seq = seq.clamp(max=S - 1)
+
+    def sums(v):
+        return torch.zeros(S, *v.shape[1:], dtype=torch.float64, device="cuda").index_add_(0, seq[inside], v[inside].double())
+    lse = torch.logsumexp(l.double(), 1, keepdim=True)
+    p = torch.exp(l.double() - lse)
+    n = sums(torch.ones(T, device="cuda"))
+    c = sums(torch.zeros(T, E, device="cuda").scatter_(1, ids.long(), 1.0))
+    assert torch.equal(tokens.double(), n) and torch.equal(counts.double(), c)
+    inv = torch.where(n > 0, 1 / n, 0.0)
+    f = c * inv[:, None] * (E / k)
+    rel = (E + 32) * 2.0 ** -23
+    want = (f * sums(p)).sum(1) * inv
+    assert bool(((loss - want).abs() <= want * 2 * rel).all())
+    want, size = sums(lse[:, 0] ** 2) * inv, sums(lse[:, 0].abs() + 1) * inv
+    assert bool(((z - want).abs() <= want * 2.0 ** -18 + 2 * rel * size).all())
+    a, b, ft = (sign.double() * inv)[seq][:, None], (0.2 * sign.double() * inv)[seq][:, None], f[seq]
+    mean = (p * ft).sum(1, keepdim=True)
+    want = torch.where(inside[:, None], p * (a * (ft - mean) + b * lse), 0.0)
+    tol = 2 * rel * p * (a.abs() * (ft + mean) + b.abs() * (lse.abs() + 1)) + want.abs() * 2.0 ** -24 + 1e-36
+    assert bool(((d - want).abs() <= tol).all())
